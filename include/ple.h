@@ -48,15 +48,25 @@ typedef enum {
     PLE_ERR_GEOMETRY_HEADS = 4, /* num_heads != (ngram_size - 1) * heads_per_ngram */
     PLE_ERR_DTYPE = 5,          /* id_dtype is neither PLE_I32 nor PLE_I64 */
     PLE_ERR_ALIGN = 6,          /* a pointer is not aligned to its element size */
-    PLE_ERR_CUDA = 7            /* a CUDA call failed; see ple_last_cuda_error() */
+    PLE_ERR_CUDA = 7,           /* a CUDA call failed; see ple_last_cuda_error() */
+    PLE_ERR_ELEMENT = 8         /* an element dtype is neither PLE_BF16 nor PLE_F16 */
 } ple_status;
 
 typedef enum { PLE_I32 = 0, PLE_I64 = 1 } ple_id_dtype;
+typedef enum { PLE_BF16 = 0, PLE_F16 = 1 } ple_element_dtype;
+typedef enum {
+    PLE_ROPE_PLAIN = 0,   /* the base's own frequencies */
+    PLE_ROPE_LINEAR = 1,  /* every frequency divided by the factor */
+    PLE_ROPE_BASE = 2,    /* the base raised, so that the slowest pair slows by the factor */
+    PLE_ROPE_PARTS = 3    /* fast pairs kept, slow pairs divided, a ramp between */
+} ple_rope_scaling;
 
 #define PLE_MAX_NGRAM 16   /* largest supported ngram_size */
 #define PLE_MAX_HEADS 256  /* largest supported heads per layer */
 #define PLE_MAX_EMBED_DIM 65536  /* largest supported table row width */
 #define PLE_HEAD_BYTES 48  /* bytes of one head's prepared constants */
+#define PLE_MAX_TREE_WORDS 8  /* largest ancestor mask, in 64-bit words: 512 nodes a request */
+#define PLE_MAX_HEAD_DIM 256  /* largest attention head width */
 
 /*
  * ple_build_token_index -- per-token (request, offset) index.
@@ -414,6 +424,236 @@ ple_status ple_selftest_floor_mod(const int64_t* x, const int64_t* v, int64_t n,
  * A library tuning constant with no counterpart on the page; the row ids do
  * not depend on it. */
 int64_t ple_small_batch_max_rows(void);
+
+/*
+ * The verification step of drafted trees.  A request drafts a tree of tokens
+ * behind its cached ones and checks all of them in one pass of the model; the
+ * entry points below are what that pass needs besides its matrix products.
+ * The nodes of every request's tree are packed like the tokens of a ragged
+ * batch (cu_seqlens), in an order where parents come before children:
+ *   parent      [T] int32, device: the place, within its own request, of a
+ *               node's parent, or -1 for a node that follows the context
+ *               directly.  A parent that is not an earlier node of its request
+ *               counts as -1.
+ *   ctx_lens    [B] int32, device: the tokens cached before this step.
+ *   cu_seqlens  [B + 1] int32, device, as for ple_build_token_index; requests
+ *               without nodes are allowed.
+ * The key and value caches are paged.  Element d of head h in slot s of page p
+ * is at p * page_stride + h * head_stride + s * slot_stride + d, in elements
+ * (the two caches share their strides), and cached token i of request r is in
+ * slot i mod page_size of page page_table[r][i / page_size].  Node j of a
+ * request stands at cached token ctx_lens[r] + j until the step is committed.
+ * Strides are multiples of 8 elements and pointers 16-byte aligned, so that a
+ * row moves in 16-byte pieces.  No address outside the num_pages pages is read
+ * or written, whatever the page table holds: at another page number, or past
+ * the table's max_pages, an append or a move is dropped and keys and values
+ * read as zeros; tokens past max_pages * page_size are not seen.  No page may
+ * hold tokens of two requests that one call writes.
+ */
+
+/*
+ * ple_build_tree_index -- positions and ancestor masks of the drafted trees.
+ *
+ *   num_requests  B >= 1 when num_tokens > 0; num_tokens T <= INT32_MAX.
+ *   mask_words    W, 1 <= W <= PLE_MAX_TREE_WORDS: 64-bit words of a mask.
+ *   positions     [T] int32 output: ctx_lens[r] plus the node's depth.
+ *   tree_mask     [T, W] uint64 output: bit j of a node's mask (bit j mod 64 of
+ *                 word j / 64) is set when node j is the node itself or one of
+ *                 its ancestors.
+ * Nodes past the first 64 * W of a request have no bit; their outputs are
+ * written as for a node without parent and without bits.
+ *
+ * Errors: PLE_ERR_SIZE, PLE_ERR_NULL, PLE_ERR_ALIGN, PLE_ERR_CUDA.
+ * One kernel launch.
+ */
+ple_status ple_build_tree_index(const int32_t* parent, const int32_t* cu_seqlens,
+                                const int32_t* ctx_lens, int32_t num_requests,
+                                int64_t num_tokens, int32_t mask_words, int32_t* positions,
+                                uint64_t* tree_mask, void* stream);
+
+/*
+ * ple_tree_row_ids -- the row ids of drafted trees, all layers in one launch.
+ *
+ * ple_row_ids with every window taken along the node's branch: W(t, s) is the
+ * id of the node's s-th ancestor, and behind the branch's root the carried
+ * context, newest id first.  A tree that is a chain gives the row ids of the
+ * same tokens as a prefill.  Arguments, arithmetic and checks as
+ * ple_row_ids_ex; parent and cu_seqlens as above.
+ *
+ * Errors: as ple_row_ids_ex.  One kernel launch.
+ */
+ple_status ple_tree_row_ids(const void* input_ids, int32_t id_dtype, int64_t num_tokens,
+                            const int32_t* parent, const int32_t* cu_seqlens,
+                            const void* ngram_context, int32_t num_requests, int32_t ctx_len,
+                            const int64_t* layer_multipliers, const int64_t* vocab_sizes,
+                            const int64_t* offsets, int32_t num_heads, int32_t ngram_size,
+                            int32_t heads_per_ngram, int32_t num_layers, int64_t boundary_id,
+                            void* out, int32_t out_dtype, const void* heads, void* stream);
+
+/*
+ * ple_prepare_rope -- the rotation of each pair per position, set up once.
+ *
+ * Pair i of rotary_dim / 2 turns by w_i = base^(-2 i / rotary_dim) radians a
+ * position, scaled for contexts beyond the trained ones (s = factor):
+ *   PLE_ROPE_LINEAR  w_i / s;
+ *   PLE_ROPE_BASE    base * s^(R / (R - 2)) in place of base (R = rotary_dim;
+ *                    a single pair is left as it is);
+ *   PLE_ROPE_PARTS   with r_i = trained_positions * w_i / 2 pi turns over the
+ *                    trained context and g = clamp((r_i - beta_slow) /
+ *                    (beta_fast - beta_slow), 0, 1): g w_i + (1 - g) w_i / s
+ *                    (interpolation "by parts", Peng et al. 2023).
+ * It is kept as a whole number of 2^-64 turns, so that the angle at any
+ * position is one wrapping 64-bit product, with no loss at long contexts.
+ *
+ *   rotary_dim   R, even, 2 <= R <= PLE_MAX_HEAD_DIM.
+ *   base >= 1, factor >= 1; with PLE_ROPE_PARTS trained_positions > 0 and
+ *   beta_fast > beta_slow >= 0 (else these are not looked at).
+ *   rope         [R / 2] int64 output, device, 8-byte aligned.
+ *
+ * Errors: PLE_ERR_SIZE, PLE_ERR_NULL, PLE_ERR_ALIGN, PLE_ERR_CUDA.
+ * One kernel launch.
+ */
+ple_status ple_prepare_rope(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                            double trained_positions, double beta_fast, double beta_slow,
+                            int64_t* rope, void* stream);
+
+/*
+ * ple_qk_norm_rope -- norms of queries and keys, their rotation, and the
+ * append of keys and values to the cache, in one pass.
+ *
+ * For every head row x of q and k, in 32 bits, rounded once:
+ *   y = x / sqrt(mean(x^2) + eps) * weight   (without a weight: y = x)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) for the pairs of the
+ *   first rotary_dim elements, at the token's position; pair i is (i, i + R/2),
+ *   or (2i, 2i + 1) when interleaved; cos and sin times rope_scale.
+ * The query rows go to q_out.  With a cache the key rows and the unchanged
+ * value rows go to the slots of the token's node (positions do not decide the
+ * slot); without one (k_cache NULL) the key rows go to k_out and v is not
+ * read.
+ */
+typedef struct {
+    const void *q, *k, *v;          /* [T, heads, D], last dimension contiguous */
+    int64_t q_token, q_head;        /* strides in elements, multiples of 8 */
+    int64_t k_token, k_head;
+    int64_t v_token, v_head;
+    const int32_t* positions;       /* [T] */
+    const int64_t* rope;            /* [R / 2] from ple_prepare_rope; unused when R = 0 */
+    const void *q_weight, *k_weight; /* [D] of the element dtype, or NULL: no norm */
+    void* q_out;                    /* [T, q_heads, D]; may be q itself, with q's strides */
+    int64_t q_out_token, q_out_head;
+    void* k_out;                    /* without a cache: [T, kv_heads, D]; may be k itself */
+    int64_t k_out_token, k_out_head;
+    void *k_cache, *v_cache;        /* both or neither */
+    int64_t page_stride, head_stride, slot_stride;
+    int64_t num_pages;
+    const int32_t* page_table;      /* [B, max_pages] */
+    const int32_t* ctx_lens;        /* [B] */
+    const int32_t* cu_seqlens;      /* [B + 1] */
+    int64_t num_tokens;             /* T, 0 <= T <= INT32_MAX */
+    int32_t num_requests;           /* B >= 1 (with a cache) */
+    int32_t max_pages, page_size;   /* >= 1 */
+    int32_t dtype;                  /* ple_element_dtype of every row and weight */
+    int32_t q_heads, kv_heads;      /* >= 0, not both 0; at most 65535 together */
+    int32_t head_dim;               /* D, a multiple of 8 in [8, PLE_MAX_HEAD_DIM] */
+    int32_t rotary_dim;             /* R, even, 0 <= R <= D */
+    int32_t interleaved;
+    float rope_scale, eps;          /* eps >= 0 */
+} ple_qk_norm_rope_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_ELEMENT, PLE_ERR_NULL, PLE_ERR_ALIGN,
+ * PLE_ERR_CUDA.  One kernel launch. */
+ple_status ple_qk_norm_rope(const ple_qk_norm_rope_args* args, void* stream);
+
+/*
+ * ple_tree_attention -- attention of drafted nodes over the paged cache and
+ * their own branch.
+ *
+ * With key head h' = h / (q_heads / kv_heads), node i of request r sees the
+ * slots below ctx_lens[r] and slot ctx_lens[r] + j for each bit j of its mask
+ * below the request's node count, and
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale q . k_j),
+ *   lse[t][h] = log sum_j exp(scale q . k_j)
+ * over those.  A node that sees nothing gets zeros and -infinity.  What a slot
+ * that is not seen holds (infinities and NaN too) has no effect.  A request of
+ * one node is an ordinary decode step.
+ * Scores, the softmax's maximum and sum, and the output are held in 32 bits;
+ * the weights p enter the product with v in the element dtype.
+ */
+typedef struct {
+    const void* q;                  /* [T, q_heads, D], last dimension contiguous */
+    int64_t q_token, q_head;        /* strides in elements, multiples of 8 */
+    const void *k_cache, *v_cache;
+    int64_t page_stride, head_stride, slot_stride;
+    int64_t num_pages;              /* >= 1 */
+    const int32_t* page_table;      /* [B, max_pages] */
+    const int32_t* ctx_lens;        /* [B] */
+    const int32_t* cu_seqlens;      /* [B + 1] */
+    const uint64_t* tree_mask;      /* [T, W] */
+    void* out;                      /* [T, q_heads, D], contiguous */
+    float* lse;                     /* [T, q_heads], or NULL */
+    void* workspace;                /* 16-byte aligned; need not be cleared */
+    int64_t workspace_bytes;        /* >= ple_tree_attention_workspace's */
+    int64_t num_tokens;             /* T, 0 <= T <= INT32_MAX */
+    int32_t num_requests;           /* B >= 1 */
+    int32_t max_pages, page_size;   /* >= 1; max_pages * page_size <= INT32_MAX */
+    int32_t dtype;                  /* ple_element_dtype of q, the caches and out */
+    int32_t q_heads, kv_heads;      /* kv_heads divides q_heads; at most 65535 */
+    int32_t head_dim;               /* D, a multiple of 8 in [8, PLE_MAX_HEAD_DIM] */
+    int32_t mask_words;             /* W, 1 <= W <= PLE_MAX_TREE_WORDS */
+    float scale;
+} ple_tree_attention_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_ELEMENT, PLE_ERR_NULL, PLE_ERR_ALIGN,
+ * PLE_ERR_CUDA.  Two kernel launches. */
+ple_status ple_tree_attention(const ple_tree_attention_args* args, void* stream);
+
+/* The workspace that a call on the current device needs, in bytes, or -1 when
+ * the device cannot be asked or an argument is out of range.  It may be reused
+ * by calls on one stream, not by calls that can run at the same time. */
+int64_t ple_tree_attention_workspace(int64_t num_tokens, int32_t q_heads, int32_t kv_heads,
+                                     int32_t head_dim);
+
+/*
+ * ple_tree_commit -- keep the accepted branches: their keys and values move
+ * together in the cache of every layer, and the next step's state follows.
+ *
+ * For every request r with a = accepted[r] nodes kept, in this order:
+ *   cached token ctx_lens[r] + path[r][j] moves to ctx_lens[r] + j, j < a;
+ *   next_ctx_lens[r] = ctx_lens[r] + a;
+ *   next_context[r] = the last ctx_len ids of (ngram_context[r], the ids of
+ *   path[r][0..a-1]), oldest first.
+ * path[r] lists nodes of the request in ascending order.  accepted is clamped
+ * to [0, path_len] and to the request's nodes; an entry of path below its own
+ * place or past the request's nodes leaves its slot as it is.
+ */
+typedef struct {
+    const void* input_ids;          /* [T], id_dtype */
+    const int32_t* path;            /* [B, path_len] */
+    const int32_t* accepted;        /* [B] */
+    const int32_t* cu_seqlens;      /* [B + 1] */
+    const void* ngram_context;      /* [B, ctx_len], id_dtype; NULL: no context is carried */
+    void* next_context;             /* [B, ctx_len], not overlapping ngram_context */
+    const int32_t* ctx_lens;        /* [B] */
+    int32_t* next_ctx_lens;         /* [B]; must not overlap ctx_lens */
+    const int32_t* page_table;      /* [B, max_pages] */
+    void *k_cache, *v_cache;        /* num_layers caches each, layer_stride elements apart */
+    int64_t layer_stride, page_stride, head_stride, slot_stride;
+    int64_t num_pages;
+    int64_t num_tokens;             /* T, 0 <= T <= INT32_MAX */
+    int32_t num_requests;           /* B >= 0; 0: nothing to do */
+    int32_t path_len;               /* >= 1 */
+    int32_t id_dtype;               /* ple_id_dtype */
+    int32_t ctx_len;                /* 1 .. PLE_MAX_NGRAM - 1 (with a context) */
+    int32_t num_layers;             /* 1 .. 65535 */
+    int32_t max_pages, page_size;   /* >= 1 */
+    int32_t kv_heads;               /* 1 .. 65535 */
+    int32_t head_dim;               /* D, a multiple of 8 in [8, PLE_MAX_HEAD_DIM] */
+    int32_t dtype;                  /* ple_element_dtype of the caches */
+} ple_tree_commit_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_DTYPE, PLE_ERR_ELEMENT, PLE_ERR_NULL,
+ * PLE_ERR_ALIGN, PLE_ERR_CUDA.  One kernel launch. */
+ple_status ple_tree_commit(const ple_tree_commit_args* args, void* stream);
 
 /*
  * ple_set_programmatic_launch -- process-wide switch for programmatic

@@ -28,17 +28,27 @@ PLE_ERR_GEOMETRY_HEADS = 4
 PLE_ERR_DTYPE = 5
 PLE_ERR_ALIGN = 6
 PLE_ERR_CUDA = 7
+PLE_ERR_ELEMENT = 8
 PLE_I32 = 0
 PLE_I64 = 1
+PLE_BF16 = 0
+PLE_F16 = 1
+PLE_ROPE_PLAIN = 0
+PLE_ROPE_LINEAR = 1
+PLE_ROPE_BASE = 2
+PLE_ROPE_PARTS = 3
 PLE_MAX_NGRAM = 16
 PLE_MAX_HEADS = 256
 PLE_MAX_EMBED_DIM = 65536
 PLE_HEAD_BYTES = 48
+PLE_MAX_TREE_WORDS = 8
+PLE_MAX_HEAD_DIM = 256
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libple.so")
 
 # every symbol include/ple.h declares, with its ctypes signature
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_F64, _ARGS = ctypes.c_double, ctypes.c_char_p  # _ARGS: an argument struct, packed
 SIGNATURES = {
     "ple_build_token_index": (_I32, [_P, _I32, _I64, _I32, _P, _P, _P]),
     "ple_row_ids": (_I32, [_P, _I32, _I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _I32, _I32, _I32,
@@ -59,6 +69,14 @@ SIGNATURES = {
     "ple_shard_plan": (_I32, [_P, _I32, _I64, _I32, _I32, _P, _P, _P, _P]),
     "ple_shard_inputs": (_I32, [_P, _I32, _P, _P, _I32, _I64, _I32, _I64, _I64, _I32, _I32, _P,
                                 _P, _P]),
+    "ple_build_tree_index": (_I32, [_P, _P, _P, _I32, _I64, _I32, _P, _P, _P]),
+    "ple_tree_row_ids": (_I32, [_P, _I32, _I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _I32, _I32,
+                                _I32, _I32, _I64, _P, _I32, _P, _P]),
+    "ple_prepare_rope": (_I32, [_I32, _F64, _I32, _F64, _F64, _F64, _F64, _P, _P]),
+    "ple_qk_norm_rope": (_I32, [_ARGS, _P]),
+    "ple_tree_attention": (_I32, [_ARGS, _P]),
+    "ple_tree_attention_workspace": (_I64, [_I64, _I32, _I32, _I32]),
+    "ple_tree_commit": (_I32, [_ARGS, _P]),
 }
 
 _lock = threading.Lock()

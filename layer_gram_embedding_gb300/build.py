@@ -24,7 +24,9 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["ple_api.cu", "ple_rowids_fixed.cu", "ple_rowids_headlane.cu", "ple_rowids_runtime.cu",
-           "ple_rowids_small.cu", "ple_embed.cu", "ple_index.cu"]
+           "ple_rowids_small.cu", "ple_embed.cu", "ple_index.cu", "ple_tree_api.cu",
+           "ple_tree_index.cu", "ple_tree_rowids.cu", "ple_norm_rope.cu",
+           "ple_tree_attention.cu"]
 
 
 def nvcc() -> str:

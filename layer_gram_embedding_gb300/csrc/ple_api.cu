@@ -60,6 +60,10 @@ bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
 }  // namespace
 
+namespace ple {
+int32_t record_cuda_failure(cudaError_t e) { return cuda_failure(e); }
+}  // namespace ple
+
 extern "C" ple_status ple_build_token_index(const int32_t* cu_seqlens, int32_t num_requests,
                                             int64_t num_tokens, int32_t is_decode, int32_t* req,
                                             int32_t* local, void* stream) {
@@ -418,6 +422,7 @@ extern "C" const char* ple_status_string(int32_t status) {
         case PLE_ERR_DTYPE: return "id dtype must be PLE_I32 or PLE_I64";
         case PLE_ERR_ALIGN: return "a pointer is not aligned to its element size";
         case PLE_ERR_CUDA: return "a CUDA call failed";
+        case PLE_ERR_ELEMENT: return "element dtype must be PLE_BF16 or PLE_F16";
         default: return "unknown status";
     }
 }
