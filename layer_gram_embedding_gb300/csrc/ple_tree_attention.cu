@@ -182,12 +182,18 @@ tree_attention_any_kernel(const ple_tree_attention_args a) {
 
 }  // namespace
 
-int64_t tree_attention_workspace(int64_t, int32_t, int32_t, int32_t, const DeviceFacts&) {
-    return 16;
+int64_t tree_attention_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                 const DeviceFacts& dev) {
+    return tree_attention_tc_workspace(T, q_heads, kv_heads, head_dim, dev);
 }
 
-cudaError_t launch_tree_attention(const ple_tree_attention_args& a, const DeviceFacts&,
+cudaError_t launch_tree_attention(const ple_tree_attention_args& a, const DeviceFacts& dev,
                                   cudaStream_t stream) {
+    if (tree_attention_tc_fits(a)) {
+        bool taken;
+        const cudaError_t e = launch_tree_attention_tc(a, dev, stream, &taken);
+        if (e != cudaSuccess || taken) return e;
+    }
     const int group = a.q_heads / a.kv_heads;
     const dim3 grid((unsigned)a.num_tokens, (unsigned)a.kv_heads,
                     (unsigned)((group + kRows - 1) / kRows));

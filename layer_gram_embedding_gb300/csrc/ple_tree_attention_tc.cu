@@ -1,0 +1,974 @@
+// Attention of drafted nodes over the paged cache and their own branch, on the
+// tensor cores of sm_103a, for head widths 64 and 128.
+//
+// Rows.  The query heads of one key head share its keys, so for a request of n
+// nodes and G = q_heads / kv_heads a key head has n * G rows (node-major).  A
+// matrix instruction takes 128 of them.  For every tile of 128 keys
+//   S = Q K^T        (accumulated in tensor memory)
+//   P = exp2(c S - c m), m the running row maximum, c = scale * log2(e)
+//   O = O + P V      (P written over S in tensor memory, O beside it)
+// with the row sums of P kept in registers: the one-pass softmax of Milakov and
+// Gimelshein (2018).  O is scaled anew only when a row's maximum has grown by
+// more than 8 in the exponent since it was last set: until then P stays below
+// 2^8 and the sum and O share the old maximum, so nothing is lost.
+//
+// Blocks.  One block an SM: a warp that copies key and value tiles into a ring
+// of shared memory (tiled bulk copies, page by page, 128-byte swizzle), a warp
+// that issues the matrix instructions, and two groups of four warps that do the
+// softmax, one row a thread.  With more than 128 rows the two groups take 128
+// each over the same tiles, so that a key is read once for 256 rows; with fewer
+// they take the tiles in turn over the same rows and are joined in shared memory.
+// Either way one group's softmax runs while the tensor cores work for the other.
+//
+// Split.  All tiles of all (request, key head, 256 rows) are laid end to end
+// and cut into equal shares, one a block, so ragged requests and few long ones
+// fill the device alike.  A block writes a unit that it has whole; of a cut
+// unit it writes the state (row maximum, sum, O in 32 bits) to the workspace,
+// and a second kernel joins the states in block order: results do not depend
+// on timing.
+//
+// What is not seen.  Scores outside the mask are replaced by -infinity before
+// the maximum, so what their keys hold does not matter.  Zero weights would
+// not stop an infinity or a NaN among the values in the matrix product:
+// values past the request's tokens are cleared in shared memory, and values of
+// drafted nodes (seen by some rows only) that are not finite are cleared there
+// and added to the rows that see them at the end.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ple_tc.cuh"
+#include "ple_tree_common.cuh"
+
+namespace ple {
+namespace {
+
+constexpr int kTile = 128;           // keys a tile, rows a matrix instruction
+constexpr int kUnitRows = 2 * kTile; // rows a unit
+constexpr int kThreads = 384;        // two groups of 128; a copying, an issuing, two idle warps
+// The softmax keeps a row's 128 scores in registers.  A block of 384 threads
+// starts with 168 a thread; 256 * 216 + 128 * 72 is the same sum.
+constexpr int kGroupRegisters = 216, kOtherRegisters = 72;
+static_assert(256 * kGroupRegisters + 128 * kOtherRegisters <= kThreads * 168,
+              "the shares come out of the block's registers");
+constexpr int kCopyWarp = 8, kIssueWarp = 9;
+constexpr int kMaxBlocks = 1024;     // blocks of a launch: an SM's number of them is far below
+constexpr float kLag = 8.0f;         // how far, in the exponent, a maximum may lag
+
+template <int D>
+struct Shape {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = kTile * 128;
+    // as many tiles as fit beside the two query tiles: at D = 128 five of 32 KB,
+    // more in flight than the 54 KB that an SM's share of the measured
+    // bandwidth times a memory latency of 1.2 us asks for
+    static constexpr int kSlots = D == 128 ? 5 : 10;
+    static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
+    // half of the 512 columns for each group: S (and P over it), O behind it
+    static constexpr uint32_t kGroupColumns = 256;
+    static constexpr uint32_t kOut = 128;
+};
+
+struct TcArgs {
+    ple_tree_attention_args a;
+    int32_t blocks;      // shares
+    int32_t rows_cap;    // rows of a state in the workspace, a multiple of 4
+    float c;             // |scale| * log2(e)
+    uint32_t flip;       // sign bits to turn in Q: scale < 0
+};
+
+// One request's tiles.
+struct Request {
+    int64_t work;            // tiles of all its units
+    int32_t begin, nodes;
+    int32_t ctx, length;     // cached slots all rows see; slots with the nodes'
+    int32_t tiles, units;    // key tiles of a unit; units a key head
+};
+
+__device__ __forceinline__ Request request_of(const ple_tree_attention_args& a, int r) {
+    Request q;
+    int32_t end;
+    request_nodes(a.cu_seqlens, r, a.num_tokens, q.begin, end);
+    q.nodes = end - q.begin;
+    const int64_t cap = (int64_t)a.max_pages * a.page_size;
+    const int64_t ctx = max(__ldg(a.ctx_lens + r), 0);
+    q.ctx = (int32_t)min(ctx, cap);
+    q.length = (int32_t)min(ctx + q.nodes, cap);
+    q.tiles = (q.length + kTile - 1) / kTile;
+    const int64_t rows = (int64_t)q.nodes * (a.q_heads / a.kv_heads);
+    q.units = (int32_t)((rows + kUnitRows - 1) / kUnitRows);
+    q.work = (int64_t)q.units * q.tiles * a.kv_heads;
+    return q;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// The tiles of requests [0, r) and of all: every thread of the block calls it.
+template <int kBlock>
+__device__ __forceinline__ void tiles_before(const ple_tree_attention_args& a, int r,
+                                             int64_t* scratch, int64_t& before, int64_t& total) {
+    int64_t b = 0, t = 0;
+    for (int i = threadIdx.x; i < a.num_requests; i += kBlock) {
+        const int64_t w = request_of(a, i).work;
+        t += w;
+        if (i < r) b += w;
+    }
+    b = warp_sum(b);
+    t = warp_sum(t);
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+        scratch[2 * warp] = b;
+        scratch[2 * warp + 1] = t;
+    }
+    __syncthreads();
+    before = total = 0;
+    for (int w = 0; w < kBlock / 32; ++w) {
+        before += scratch[2 * w];
+        total += scratch[2 * w + 1];
+    }
+}
+
+// The request that owns tile `at`, and the tiles before it.  Every thread of the
+// block calls it; the owner's thread writes the answer.
+template <int kBlock>
+__device__ __forceinline__ void find_tile(const ple_tree_attention_args& a, int64_t at,
+                                          int64_t* scratch, int64_t* found) {
+    int64_t base = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int first = 0; first < a.num_requests; first += kBlock) {
+        const int r = first + threadIdx.x;
+        const int64_t w = r < a.num_requests ? request_of(a, r).work : 0;
+        int64_t upto = w;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        __syncthreads();
+        if (lane == 31) scratch[warp] = upto;
+        __syncthreads();
+        int64_t before = base, all = base;
+        for (int k = 0; k < kBlock / 32; ++k) {
+            if (k < warp) before += scratch[k];
+            all += scratch[k];
+        }
+        if (w > 0 && before + upto - w <= at && at < before + upto) {
+            found[0] = r;
+            found[1] = before + upto - w;
+        }
+        base = all;
+        if (at < base) break;
+    }
+    __syncthreads();
+}
+
+// A block's piece of one unit: keys tiles [k0, k1) of `tiles`.
+struct Segment {
+    Request q;
+    int32_t head, unit;
+    int32_t k0, k1;
+    int32_t rows;     // of the unit, at most kUnitRows
+    bool pair;        // more than 128 rows: a group each
+};
+
+// The block's segments in order; every role walks them alike.
+struct Walk {
+    const ple_tree_attention_args& a;
+    int64_t at, end;     // tiles still to do
+    int64_t base;        // tiles before request r
+    int r;
+    Request q;
+    __device__ __forceinline__ Walk(const ple_tree_attention_args& args, int64_t lo, int64_t hi,
+                                    int first, int64_t before)
+        : a(args), at(lo), end(hi), base(before), r(first) {
+        if (at < end) q = request_of(a, r);
+    }
+    __device__ __forceinline__ bool next(Segment& s) {
+        if (at >= end) return false;
+        while (at >= base + q.work) {
+            base += q.work;
+            q = request_of(a, ++r);
+        }
+        const int64_t rel = at - base;
+        const int32_t u = (int32_t)(rel / q.tiles);
+        s.q = q;
+        s.k0 = (int32_t)(rel - (int64_t)u * q.tiles);
+        s.k1 = (int32_t)min((int64_t)q.tiles, s.k0 + (end - at));
+        s.head = u / q.units;
+        s.unit = u - s.head * q.units;
+        s.rows = (int32_t)min((int64_t)kUnitRows,
+                              (int64_t)q.nodes * (a.q_heads / a.kv_heads) -
+                                  (int64_t)s.unit * kUnitRows);
+        s.pair = s.rows > kTile;
+        at += s.k1 - s.k0;
+        return true;
+    }
+};
+
+// First tile of share c, and the share of a tile.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int blocks) {
+    return total * c / blocks;
+}
+__device__ __forceinline__ int share_of(int64_t total, int64_t tile, int blocks) {
+    return (int)(((tile + 1) * blocks - 1) / total);
+}
+
+// The workspace: a failure flag for each block, then two states a block (0: a
+// unit begun before the block, 1: a unit that starts in it), each a pair (row
+// maximum in the exponent of 2, row sum) and D accumulators a row.
+__host__ __device__ __forceinline__ int64_t state_at(int64_t block, int slot, int rows_cap,
+                                                     int D) {
+    return kMaxBlocks + (block * 2 + slot) * (int64_t)rows_cap * (D + 2);
+}
+
+// K_j's and V_j's places in the order of copies K_0, K_1, V_0, K_2, V_1, ... of
+// a segment of n tiles: the order in which the issuing warp wants them.
+__device__ __forceinline__ int key_item(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int value_item(int j, int n) {
+    return j < n - 1 ? 2 * j + 2 : 2 * j + 1;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+    uint32_t v;
+    if constexpr (kBf16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
+// Which of 32 slots from `slot` on a node sees, as bits: all below ctx, above it
+// those of its mask.
+__device__ __forceinline__ uint32_t seen_bits(const unsigned long long* __restrict__ mask,
+                                              int words, int ctx, int length, int slot) {
+    const int b = slot - ctx;
+    if (b + 32 <= 0) return 0xffffffffu;
+    const int lo = max(b, 0);
+    const int limit = min(length - ctx, 64 * words);
+    if (lo >= limit) return b < 0 ? (1u << -b) - 1 : 0u;
+    const int w = lo >> 6, s = lo & 63;
+    uint64_t v = __ldg(mask + w) >> s;
+    if (s > 32 && w + 1 < words) v |= __ldg(mask + w + 1) << (64 - s);
+    uint32_t bits = (uint32_t)v;
+    if (limit - lo < 32) bits &= (1u << (limit - lo)) - 1;
+    return b < 0 ? bits << -b | ((1u << -b) - 1) : bits;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float widen16(uint32_t v) {
+    if constexpr (kBf16)
+        return __uint_as_float(v << 16);
+    else
+        return __half2float(__ushort_as_half((unsigned short)v));
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
+                         const __grid_constant__ CUtensorMap k_map,
+                         const __grid_constant__ CUtensorMap v_map) {
+    using S = Shape<D>;
+    const ple_tree_attention_args& a = args.a;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_full[2], pv_done[2], last;
+    __shared__ int64_t scratch[2 * (kThreads / 32)], found[2];
+    __shared__ uint32_t tmem_s;
+    __shared__ int failed_s;
+    __shared__ int bad_s[2];          // a segment's drafted values hold infinities or NaN
+    __shared__ float join_s[kTile][2];
+    volatile int* failed = &failed_s;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023) & ~1023u) - smem_addr(smem_raw));
+    uint8_t* q_tiles = smem;
+    uint8_t* ring = smem + 2 * S::kTileBytes;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&q_full[w], 128);
+            mbar_init(&s_full[w], 1);
+            mbar_init(&p_full[w], 4);
+            mbar_init(&pv_done[w], 1);
+            bad_s[w] = 0;
+        }
+        mbar_init(&q_empty, 1);
+        mbar_init(&last, 1);
+        failed_s = 0;
+        fence_barrier_init();
+    }
+    if (warp == kIssueWarp) tmem_alloc(&tmem_s, 512);
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_map(&k_map);
+        prefetch_map(&v_map);
+    }
+    wait_grid_before();
+
+    // this block's share of the tiles
+    int64_t unused, total;
+    tiles_before<kThreads>(a, 0, scratch, unused, total);
+    const int64_t lo = share_begin(total, blockIdx.x, args.blocks);
+    const int64_t hi = share_begin(total, blockIdx.x + 1, args.blocks);
+    if (lo < hi) find_tile<kThreads>(a, lo, scratch, found);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_s;
+    const int group = a.q_heads / a.kv_heads;
+    Walk walk(a, lo, hi, lo < hi ? (int)found[0] : 0, lo < hi ? found[1] : 0);
+    Segment s;
+
+    if (warp >= kCopyWarp) {
+        fewer_registers<kOtherRegisters>();
+        if (warp == kCopyWarp) {
+            // ------------------------------------------------------- copies
+            const int box = min(a.page_size, kTile);          // slots a box
+            const int boxes = kTile / box;
+            const int which = lane / S::kHalves, half = lane % S::kHalves;
+            const bool mine = which < boxes;
+            uint32_t items = 0;
+            while (walk.next(s)) {
+                const int n = s.k1 - s.k0;
+                const int32_t* table = a.page_table + (int64_t)walk.r * a.max_pages;
+                // a box past the tokens, or of a page outside the cache, is filled
+                // with zeros: its page number is outside the map
+                auto page_of = [&](int j) -> int {
+                    const int slot = (s.k0 + j) * kTile + which * box;
+                    if (!mine || j >= n || slot >= s.q.length) return (int)a.num_pages;
+                    const int p = __ldg(table + slot / a.page_size);
+                    return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
+                };
+                auto copy = [&](const CUtensorMap* map, uint32_t item, int j, int page) {
+                    const uint32_t slot = item % S::kSlots;
+                    const uint32_t round = item / S::kSlots;
+                    mbar_wait(&empty[slot], (round & 1) ^ 1, failed);
+                    if (lane == 0) mbar_arrive_expect(&full[slot], S::kTileBytes);
+                    __syncwarp();
+                    if (mine) {
+                        const uint32_t dst = smem_addr(ring) + slot * S::kTileBytes +
+                                             half * S::kHalfBytes + which * box * 128;
+                        copy_box(map, dst, &full[slot], half * 64,
+                                 ((s.k0 + j) * kTile + which * box) % a.page_size, s.head, page);
+                    }
+                };
+                int page = page_of(0), after = page_of(1);
+                copy(&k_map, items, 0, page);
+                for (int j = 0; j < n; ++j) {
+                    const int then = page_of(j + 2);
+                    if (j + 1 < n) copy(&k_map, items + key_item(j + 1), j + 1, after);
+                    copy(&v_map, items + value_item(j, n), j, page);
+                    page = after;
+                    after = then;
+                }
+                items += 2 * n;
+            }
+            if (*failed) {
+                // copies may be in flight: they end before the block does
+                for (uint32_t i = items > S::kSlots ? items - S::kSlots : 0; i < items; ++i) {
+                    const long long start = clock64();
+                    while (!mbar_try(&full[i % S::kSlots], i / S::kSlots & 1) &&
+                           clock64() - start < kWaitClocks) {
+                    }
+                }
+            }
+        } else if (warp == kIssueWarp) {
+            // -------------------------------------------- matrix instructions
+            constexpr uint32_t kScoreWord = mma_word(kBf16, false, kTile, kTile);
+            constexpr uint32_t kOutWord = mma_word(kBf16, true, kTile, D);
+            uint32_t items = 0;
+            uint32_t q_count[2] = {0, 0}, p_count[2] = {0, 0};
+            uint32_t seg = 0;
+            while (walk.next(s)) {
+                const int n = s.k1 - s.k0;
+                if (lane == 0) bad_s[seg & 1] = 0;
+                auto wait_item = [&](uint32_t item) {
+                    mbar_wait(&full[item % S::kSlots], item / S::kSlots & 1, failed);
+                };
+                auto slot_of = [&](uint32_t item) -> uint32_t {
+                    return smem_addr(ring) + item % S::kSlots * S::kTileBytes;
+                };
+                // a descriptor's address counts 16 bytes and stays below 2^14, so
+                // steps within a tile add to it
+                auto scores = [&](int w, uint32_t item) {
+                    if (lane == 0) {
+                        const uint64_t qd = operand_desc(
+                            smem_addr(q_tiles) + (s.pair ? w : 0) * S::kTileBytes, 16);
+                        const uint64_t kd = operand_desc(slot_of(item), 16);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t at = ((k / 4) * S::kHalfBytes + (k % 4) * 32) >> 4;
+                            mma_smem(tmem + w * S::kGroupColumns, qd + at, kd + at, kScoreWord,
+                                     k != 0);
+                        }
+                        mma_commit(&s_full[w]);
+                    }
+                    __syncwarp();
+                };
+                auto values = [&](int w, uint32_t item, bool accumulate) {
+                    if (lane == 0) {
+                        const uint64_t vd = operand_desc(slot_of(item), S::kHalfBytes);
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_tmem(tmem + w * S::kGroupColumns + S::kOut,
+                                     tmem + w * S::kGroupColumns + k * 8, vd + (k * 16 * 128 >> 4),
+                                     kOutWord, accumulate || k != 0);
+                        mma_commit(&pv_done[w]);
+                    }
+                    __syncwarp();
+                };
+                auto release = [&](uint32_t item) {
+                    if (lane == 0) mma_commit(&empty[item % S::kSlots]);
+                    __syncwarp();
+                };
+                auto wait_weights = [&](int w) {
+                    mbar_wait(&p_full[w], p_count[w]++ & 1, failed);
+                    tmem_fence_after();
+                };
+                // values past the request's tokens, and drafted ones that are not
+                // finite, are cleared before the product reads them
+                auto clean = [&](int j, uint32_t item) {
+                    const int first = (s.k0 + j) * kTile;
+                    if (first + kTile <= s.q.ctx) return;
+                    uint8_t* tile = ring + (item % S::kSlots) * S::kTileBytes;
+                    const int from = max(s.q.ctx - first, 0), upto = min(s.q.length - first, kTile);
+                    constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
+                    bool bad = false;
+                    for (int i = from * 8 + lane; i < kTile * 8; i += 32) {
+                        const bool live = i < upto * 8;
+#pragma unroll
+                        for (int h = 0; h < S::kHalves; ++h) {
+                            uint4* at = reinterpret_cast<uint4*>(tile + h * S::kHalfBytes) + i;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            bool change = !live;
+                            if (live) {
+                                v = *at;
+                                uint32_t* x = &v.x;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((x[e] & kExp) == kExp) {
+                                        x[e] &= 0xFFFF0000u;
+                                        change = bad = true;
+                                    }
+                                    if ((x[e] >> 16 & kExp) == kExp) {
+                                        x[e] &= 0xFFFFu;
+                                        change = bad = true;
+                                    }
+                                }
+                            }
+                            if (change) *at = v;
+                        }
+                    }
+                    if (bad) bad_s[seg & 1] = 1;
+                    __threadfence_block();
+                    fence_async_proxy();
+                    __syncwarp();
+                };
+
+                mbar_wait(&q_full[0], q_count[0]++ & 1, failed);
+                if (s.pair) mbar_wait(&q_full[1], q_count[1]++ & 1, failed);
+                tmem_fence_after();
+                if (s.pair) {
+                    wait_item(items);
+                    scores(0, items);
+                    scores(1, items);
+                    release(items);
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t v = items + value_item(j, n), k = items + key_item(j + 1);
+#pragma unroll 1
+                        for (int w = 0; w < 2; ++w) {
+                            wait_weights(w);
+                            if (w == 0) {
+                                wait_item(v);
+                                clean(j, v);
+                            }
+                            values(w, v, j > 0);
+                            if (w == 1) release(v);
+                            if (j + 1 < n) {
+                                if (w == 0) wait_item(k);
+                                scores(w, k);
+                                if (w == 1) release(k);
+                            }
+                        }
+                    }
+                } else {
+                    for (int w = 0; w < min(2, n); ++w) {
+                        const uint32_t k = items + key_item(w);
+                        wait_item(k);
+                        scores(w, k);
+                        release(k);
+                    }
+                    for (int j = 0; j < n; ++j) {
+                        const int w = j & 1;
+                        const uint32_t v = items + value_item(j, n);
+                        wait_weights(w);
+                        wait_item(v);
+                        clean(j, v);
+                        values(w, v, j > 1);
+                        release(v);
+                        if (j + 2 < n) {
+                            const uint32_t k = items + key_item(j + 2);
+                            wait_item(k);
+                            scores(w, k);
+                            release(k);
+                        }
+                    }
+                }
+                if (lane == 0) mma_commit(&q_empty);
+                __syncwarp();
+                items += 2 * n;
+                ++seg;
+            }
+            if (lane == 0) mma_commit(&last);
+            __syncwarp();
+            // also after a failure: nothing runs on past the block
+            const long long start = clock64();
+            while (!mbar_try(&last, 0) && clock64() - start < kWaitClocks) {
+            }
+        }
+    } else {
+        more_registers<kGroupRegisters>();
+        // ------------------------------------------------------- softmax
+        const int w = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + w * S::kGroupColumns + lanes;
+        const uint32_t o_at = s_at + S::kOut;
+        const float c = args.c;
+        uint32_t seg = 0, count = 0;
+        while (walk.next(s)) {
+            const int n = s.k1 - s.k0;
+            const int first_row = s.unit * kUnitRows + (s.pair ? w * kTile : 0);
+            const int rows = s.pair ? (w == 0 ? kTile : s.rows - kTile) : s.rows;
+            const bool active = (warp & 3) * 32 < rows;   // a warp with no row only keeps step
+            const bool here = row < rows;
+            const int node = (first_row + row) / group;
+            const int64_t token = s.q.begin + node;
+            const int64_t head = (int64_t)s.head * group + (first_row + row) - node * group;
+            const unsigned long long* mask =
+                reinterpret_cast<const unsigned long long*>(a.tree_mask) +
+                (here ? token : 0) * a.mask_words;
+
+            // this group's queries, rows of the unit, into swizzled shared memory
+            if (s.pair || w == 0) {
+                if (seg > 0) mbar_wait(&q_empty, (seg - 1) & 1, failed);
+                uint8_t* tile = q_tiles + (s.pair ? w : 0) * S::kTileBytes;
+                for (int i = row; i < rows * (D / 8); i += 128) {
+                    const int r = i / (D / 8), ch = i % (D / 8);
+                    const int nd = (first_row + r) / group;
+                    const int hd = s.head * group + (first_row + r) - nd * group;
+                    uint4 v = __ldg(reinterpret_cast<const uint4*>(
+                        static_cast<const unsigned short*>(a.q) +
+                        (int64_t)(s.q.begin + nd) * a.q_token + hd * a.q_head + ch * 8));
+                    v.x ^= args.flip;
+                    v.y ^= args.flip;
+                    v.z ^= args.flip;
+                    v.w ^= args.flip;
+                    *reinterpret_cast<uint4*>(tile + (ch / 8) * S::kHalfBytes + r * 128 +
+                                              (((ch & 7) ^ (r & 7)) << 4)) = v;
+                }
+                fence_async_proxy();
+                mbar_arrive(&q_full[w]);
+            }
+
+            float top = -INFINITY, sum = 0.f;
+            const int step = s.pair ? 1 : 2;
+            bool begun = false;
+            for (int j = s.pair ? 0 : w; j < n; j += step) {
+                mbar_wait(&s_full[w], count & 1, failed);
+                tmem_fence_after();
+                if (active) {
+                    uint32_t v[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_load(s_at + 32 * q, v[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_wait_load(v[q]);
+                    const int first = (s.k0 + j) * kTile;
+                    const bool masked = first + kTile > s.q.ctx;
+                    if (masked) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t bits =
+                                here ? seen_bits(mask, a.mask_words, s.q.ctx, s.q.length,
+                                                 first + 32 * q)
+                                     : 0u;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(bits >> i & 1)) v[q][i] = 0xFF800000u;  // -infinity
+                        }
+                    }
+                    float m4[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        m4[q] = __uint_as_float(v[q][0]);
+#pragma unroll
+                        for (int i = 1; i < 32; ++i) m4[q] = fmaxf(m4[q], __uint_as_float(v[q][i]));
+                    }
+                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    // a new maximum only where it grew by more than kLag
+                    const bool grow = here && (m - top) * c > kLag;
+                    const bool set = here && top == -INFINITY && m > -INFINITY;
+                    if (__any_sync(0xffffffffu, grow || set)) {
+                        const bool move = grow || set;
+                        const float f = move ? (set ? 0.f : exp2_fast((top - m) * c)) : 1.f;
+                        if (move) top = m;
+                        sum *= f;
+                        if (begun) {
+                            mbar_wait(&pv_done[w], (count - 1) & 1, failed);
+                            tmem_fence_after();
+#pragma unroll
+                            for (int q = 0; q < D / 32; ++q) {
+                                uint32_t o[32];
+                                tmem_load(o_at + 32 * q, o);
+                                tmem_wait_load(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_store(o_at + 32 * q, o);
+                            }
+                        }
+                    }
+                    // rows that have seen nothing yet have only -infinities:
+                    // exponents relative to 0 make zeros of them
+                    const float shift = top == -INFINITY ? 0.f : top * c;
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int q = 2 * h + i / 16, e = (2 * i) % 32;
+                            const float x0 = exp2_fast(fmaf(__uint_as_float(v[q][e]), c, -shift));
+                            const float x1 =
+                                exp2_fast(fmaf(__uint_as_float(v[q][e + 1]), c, -shift));
+                            part[i & 3] += x0 + x1;
+                            p[i] = round_pair<kBf16>(x0, x1);
+                        }
+                        tmem_store(s_at + 32 * h, p);
+                    }
+                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    tmem_wait_store();
+                }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[w]);
+                begun = true;
+                ++count;
+            }
+            if (begun) {
+                mbar_wait(&pv_done[w], (count - 1) & 1, failed);
+                tmem_fence_after();
+            }
+
+            // ------------------------------------ the segment's rows go out
+            const bool join = !s.pair && n > 1;   // both groups hold states of the same rows
+            float4* exchange = reinterpret_cast<float4*>(q_tiles);
+            if (join && w == 1) {
+                mbar_wait(&q_empty, seg & 1, failed);   // the queries have been read
+                if (active) {
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_load(o_at + 32 * q, o);
+                        tmem_wait_load(o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            exchange[(q * 8 + i) * kTile + row] = make_float4(
+                                __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    }
+                    join_s[row][0] = top;
+                    join_s[row][1] = sum;
+                }
+            }
+            if (join) named_barrier<256>(1);
+            if (s.pair || w == 0) {
+                float f0 = 1.f, f1 = 0.f;
+                if (join && here) {
+                    const float other = join_s[row][0];
+                    const float m = fmaxf(top, other);
+                    const float base = m == -INFINITY ? 0.f : m;
+                    f0 = exp2_fast((top - base) * c);
+                    f1 = exp2_fast((other - base) * c);
+                    if (top == -INFINITY) f0 = 0.f;
+                    if (other == -INFINITY) f1 = 0.f;
+                    sum = sum * f0 + join_s[row][1] * f1;
+                    top = m;
+                }
+                const bool whole = s.k0 == 0 && s.k1 == s.q.tiles;
+                const bool bad = bad_s[seg & 1] != 0;
+                const int64_t o_row = token * a.q_heads + head;
+                float* state = static_cast<float*>(a.workspace) +
+                               state_at(blockIdx.x, s.k0 == 0 ? 1 : 0, args.rows_cap, D);
+                const int state_row = (s.pair ? w * kTile : 0) + row;
+                float* pairs = state + 2 * state_row;
+                float* acc = state + 2 * args.rows_cap + (int64_t)state_row * D;
+                const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+                if (active) {
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        if (begun) {
+                            tmem_load(o_at + 32 * q, o);
+                            tmem_wait_load(o);
+                        }
+                        float x[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
+                        if (join) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 y = exchange[(q * 8 + i) * kTile + row];
+                                x[4 * i] = x[4 * i] * f0 + y.x * f1;
+                                x[4 * i + 1] = x[4 * i + 1] * f0 + y.y * f1;
+                                x[4 * i + 2] = x[4 * i + 2] * f0 + y.z * f1;
+                                x[4 * i + 3] = x[4 * i + 3] * f0 + y.w * f1;
+                            }
+                        }
+                        if (bad && here) {
+                            // the drafted values that were cleared, to the rows
+                            // that see them: infinities and NaN
+                            for (int slot = max(s.q.ctx, s.k0 * kTile);
+                                 slot < min(s.q.length, s.k1 * kTile); ++slot) {
+                                if (!(seen_bits(mask, a.mask_words, s.q.ctx, s.q.length, slot) & 1))
+                                    continue;
+                                const int64_t at = slot_offset(
+                                    a.page_table, a.max_pages, a.page_size, a.num_pages,
+                                    a.page_stride, a.slot_stride, walk.r, slot);
+                                if (at < 0) continue;
+                                const unsigned short* vrow =
+                                    static_cast<const unsigned short*>(a.v_cache) + at +
+                                    s.head * a.head_stride + 32 * q;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const float e = widen16<kBf16>(vrow[i]);
+                                    if (!isfinite(e)) x[i] += e;
+                                }
+                            }
+                        }
+                        if (here && whole) {
+                            uint4* dst = reinterpret_cast<uint4*>(
+                                static_cast<unsigned short*>(a.out) + o_row * D + 32 * q);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    y[e] = round_pair<kBf16>(x[8 * i + 2 * e] * inv,
+                                                             x[8 * i + 2 * e + 1] * inv);
+                                dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                        } else if (here) {
+                            float4* dst = reinterpret_cast<float4*>(acc + 32 * q);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2],
+                                                     x[4 * i + 3]);
+                        }
+                        __syncwarp();  // the next load is the whole warp's
+                    }
+                    if (here) {
+                        if (!whole) {
+                            pairs[0] = top == -INFINITY ? -INFINITY : top * c;
+                            pairs[1] = sum;
+                        } else if (a.lse != nullptr) {
+                            a.lse[o_row] = sum == 0.f ? -INFINITY
+                                                      : top * c * 0.69314718055994531f + logf(sum);
+                        }
+                    }
+                }
+            }
+            tmem_fence_before();
+            named_barrier<256>(2);
+            ++seg;
+        }
+    }
+
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (threadIdx.x == 0)
+        reinterpret_cast<int*>(a.workspace)[blockIdx.x] = failed_s;
+    if (warp == kIssueWarp) tmem_free(tmem, 512);
+}
+
+// ------------------------------------------------------------------- the join
+
+constexpr int kJoinThreads = 256;
+
+// The cut units' rows: for a row, the states of the blocks that share its unit,
+// in block order.  One block a token, one warp a row at a time, D / 32
+// accumulators a lane.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads)
+tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
+    const ple_tree_attention_args& a = args.a;
+    __shared__ int64_t scratch[2 * (kJoinThreads / 32)];
+    wait_grid_before();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = blockIdx.x;
+    const int r = warp_request(a.cu_seqlens, a.num_requests, t, lane);
+    int64_t before, total;
+    tiles_before<kJoinThreads>(a, r, scratch, before, total);
+    const Request q = request_of(a, r);
+    const int group = a.q_heads / a.kv_heads;
+    const int64_t node = t - q.begin;
+    if (node < 0 || node >= q.nodes) return;
+    const float* space = static_cast<const float*>(a.workspace);
+    for (int h = warp; h < a.q_heads; h += kJoinThreads / 32) {
+        const int head = h / group;
+        const int64_t row = node * group + (h - head * group);
+        const int64_t unit = row / kUnitRows;
+        const int local = (int)(row - unit * kUnitRows);
+        const int64_t first = before + (head * (int64_t)q.units + unit) * q.tiles;
+        const int c0 = share_of(total, first, args.blocks);
+        const int c1 = share_of(total, first + q.tiles - 1, args.blocks);
+        bool failed = false;
+        for (int c = c0; c <= c1; ++c) failed |= reinterpret_cast<const int*>(space)[c] != 0;
+        if (c0 == c1 && !failed) continue;  // the block wrote it
+        constexpr int E = D / 32;
+        float m = -INFINITY, sum = 0.f, acc[E] = {};
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t lo = share_begin(total, c, args.blocks);
+            if (lo == share_begin(total, c + 1, args.blocks)) continue;  // more shares than tiles
+            const float* state = space + state_at(c, lo <= first ? 1 : 0, args.rows_cap, D);
+            const float2 p = __ldcg(reinterpret_cast<const float2*>(state) + local);
+            float x[E];
+            const float* from = state + 2 * args.rows_cap + (int64_t)local * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = __ldcg(from + e);
+            // no maximum: nothing seen (zeros), or only NaN, which stays
+            const float now = fmaxf(m, p.x);
+            const float f = m == -INFINITY ? 1.f : exp2_fast(m - now);
+            const float g = p.x == -INFINITY ? 1.f : exp2_fast(p.x - now);
+            sum = sum * f + p.y * g;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + x[e] * g;
+            m = now;
+        }
+        if (failed) sum = __int_as_float(0x7FC00000);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t o = t * a.q_heads + h;
+        unsigned short* dst = static_cast<unsigned short*>(a.out) + o * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) =
+                round_pair<kBf16>(acc[e] * inv, acc[e + 1] * inv);
+        if (lane == 0 && a.lse != nullptr)
+            a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
+    }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A cache as a map of (element, slot, head, page); boxes of 64 elements by one
+// page's (or 128) slots.  Pages outside read as zeros.
+bool encode_cache(CUtensorMap* map, const ple_tree_attention_args& a, const void* cache) {
+    const EncodeTiled fn = encode_tiled();
+    if (fn == nullptr) return false;
+    auto stride = [](int64_t elements, int64_t n) {
+        return (cuuint64_t)(n == 1 ? 16 : elements * 2);
+    };
+    const cuuint64_t sizes[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.page_size,
+                                 (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {stride(a.slot_stride, a.page_size),
+                                   stride(a.head_stride, a.kv_heads),
+                                   stride(a.page_stride, a.num_pages)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(a.page_size < kTile ? a.page_size : kTile), 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return fn(map,
+              a.dtype == PLE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              4, const_cast<void*>(cache), sizes, strides, box, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int tc_blocks(const DeviceFacts& dev) {
+    return dev.sm_count < kMaxBlocks ? dev.sm_count : kMaxBlocks;
+}
+
+int tc_rows_cap(int64_t T, int32_t q_heads, int32_t kv_heads) {
+    const int64_t rows = T * (q_heads / kv_heads);
+    return (int)(rows < kUnitRows ? (rows + 3) / 4 * 4 : kUnitRows);  // 16-byte rows
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_tc(const TcArgs& args, const CUtensorMap& k, const CUtensorMap& v,
+                      cudaStream_t stream) {
+    auto* fn = tree_attention_tc_kernel<D, kBf16>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Shape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(fn, dim3((unsigned)args.blocks), dim3(kThreads), Shape<D>::kSmem, stream,
+                      programmatic_launch(), args, k, v);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(tree_attention_join_kernel<D, kBf16>, dim3((unsigned)args.a.num_tokens),
+                         dim3(kJoinThreads), 0, stream, programmatic_launch(), args);
+}
+
+}  // namespace
+
+int64_t tree_attention_tc_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D,
+                                    const DeviceFacts& dev) {
+    return 4 * state_at(tc_blocks(dev), 0, tc_rows_cap(T, q_heads, kv_heads), D);
+}
+
+// The shapes whose tiles are whole boxes of whole swizzle atoms.
+bool tree_attention_tc_fits(const ple_tree_attention_args& a) {
+    return (a.head_dim == 64 || a.head_dim == 128) && a.page_size % 8 == 0 &&
+           (kTile % a.page_size == 0 || a.page_size % kTile == 0);
+}
+
+// *taken: whether the tensor maps take the caches' strides (else nothing ran).
+cudaError_t launch_tree_attention_tc(const ple_tree_attention_args& a, const DeviceFacts& dev,
+                                     cudaStream_t stream, bool* taken) {
+    CUtensorMap k, v;
+    *taken = encode_cache(&k, a, a.k_cache) && encode_cache(&v, a, a.v_cache);
+    if (!*taken) return cudaSuccess;
+    TcArgs args;
+    args.a = a;
+    args.blocks = tc_blocks(dev);
+    args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads);
+    args.c = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
+    args.flip = a.scale < 0 ? 0x80008000u : 0u;
+    if (a.head_dim == 64)
+        return a.dtype == PLE_BF16 ? launch_tc<64, true>(args, k, v, stream)
+                                   : launch_tc<64, false>(args, k, v, stream);
+    return a.dtype == PLE_BF16 ? launch_tc<128, true>(args, k, v, stream)
+                               : launch_tc<128, false>(args, k, v, stream);
+}
+
+}  // namespace ple

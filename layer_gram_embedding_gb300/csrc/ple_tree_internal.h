@@ -36,5 +36,12 @@ int64_t tree_attention_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, i
                                  const DeviceFacts& dev);
 cudaError_t launch_tree_attention(const ple_tree_attention_args& a, const DeviceFacts& dev,
                                   cudaStream_t stream);
+// The tensor-core kernel (ple_tree_attention_tc.cu): which shapes it takes, the
+// states of split rows, its launches.
+bool tree_attention_tc_fits(const ple_tree_attention_args& a);
+int64_t tree_attention_tc_workspace(int64_t T, int32_t q_heads, int32_t kv_heads,
+                                    int32_t head_dim, const DeviceFacts& dev);
+cudaError_t launch_tree_attention_tc(const ple_tree_attention_args& a, const DeviceFacts& dev,
+                                     cudaStream_t stream, bool* taken);
 
 }  // namespace ple
