@@ -12,7 +12,7 @@
 // more than 8 in the exponent since it was last set: until then P stays below
 // 2^8 and the sum and O share the old maximum, so nothing is lost.
 //
-// Blocks.  One block an SM: a warp that copies key and value tiles into a ring
+// Blocks.  One block an SM: two warps that copy key and value tiles into a ring
 // of shared memory (tiled bulk copies, page by page, 128-byte swizzle), a warp
 // that issues the matrix instructions, and two groups of four warps that do the
 // softmax, one row a thread.  With more than 128 rows the two groups take 128
@@ -45,13 +45,8 @@ namespace {
 
 constexpr int kTile = 128;           // keys a tile, rows a matrix instruction
 constexpr int kUnitRows = 2 * kTile; // rows a unit
-constexpr int kThreads = 384;        // two groups of 128; a copying, an issuing, two idle warps
-// The softmax keeps a row's 128 scores in registers.  A block of 384 threads
-// starts with 168 a thread; 256 * 216 + 128 * 72 is the same sum.
-constexpr int kGroupRegisters = 216, kOtherRegisters = 72;
-static_assert(256 * kGroupRegisters + 128 * kOtherRegisters <= kThreads * 168,
-              "the shares come out of the block's registers");
-constexpr int kCopyWarp = 8, kIssueWarp = 9;
+constexpr int kThreads = 384;        // two groups of 128; two copying, an issuing, an idle warp
+constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10;
 constexpr int kMaxBlocks = 1024;     // blocks of a launch: an SM's number of them is far below
 constexpr float kLag = 8.0f;         // how far, in the exponent, a maximum may lag
 
@@ -210,7 +205,10 @@ struct Walk {
     }
 };
 
-// First tile of share c, and the share of a tile.
+// Shares that hold a tile, the first tile of share c, and the share of a tile.
+__device__ __forceinline__ int shares(int64_t total, int blocks) {
+    return (int)min(total, (int64_t)blocks);
+}
 __device__ __forceinline__ int64_t share_begin(int64_t total, int c, int blocks) {
     return total * c / blocks;
 }
@@ -219,8 +217,10 @@ __device__ __forceinline__ int share_of(int64_t total, int64_t tile, int blocks)
 }
 
 // The workspace: a failure flag for each block, then two states a block (0: a
-// unit begun before the block, 1: a unit that starts in it), each a pair (row
-// maximum in the exponent of 2, row sum) and D accumulators a row.
+// unit begun before the block, 1: a unit that starts in it).  A state is a pair
+// (row maximum in the exponent of 2, row sum) for each row, then the accumulators
+// as [D / 8][row][8]: neighbouring threads write, and a row's readers read, whole
+// 32-byte sectors.
 __host__ __device__ __forceinline__ int64_t state_at(int64_t block, int slot, int rows_cap,
                                                      int D) {
     return kMaxBlocks + (block * 2 + slot) * (int64_t)rows_cap * (D + 2);
@@ -237,6 +237,33 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float as_float(uint32_t v) { return __uint_as_float(v); }
+
+// Two 32-bit floats to a register pair: one instruction for both on sm_103a.
+__device__ __forceinline__ uint64_t pack_f32(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpack_f32(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float v;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+    return v;
 }
 
 template <bool kBf16>
@@ -314,7 +341,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
         fence_barrier_init();
     }
     if (warp == kIssueWarp) tmem_alloc(&tmem_s, 512);
-    if (warp == kCopyWarp && lane == 0) {
+    if (warp == kKeyWarp && lane == 0) {
         prefetch_map(&k_map);
         prefetch_map(&v_map);
     }
@@ -323,8 +350,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     // this block's share of the tiles
     int64_t unused, total;
     tiles_before<kThreads>(a, 0, scratch, unused, total);
-    const int64_t lo = share_begin(total, blockIdx.x, args.blocks);
-    const int64_t hi = share_begin(total, blockIdx.x + 1, args.blocks);
+    const int blocks = shares(total, args.blocks);
+    const int64_t lo = blockIdx.x < blocks ? share_begin(total, blockIdx.x, blocks) : total;
+    const int64_t hi = blockIdx.x < blocks ? share_begin(total, blockIdx.x + 1, blocks) : total;
     if (lo < hi) find_tile<kThreads>(a, lo, scratch, found);
     tmem_fence_before();
     __syncthreads();
@@ -334,10 +362,11 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     Walk walk(a, lo, hi, lo < hi ? (int)found[0] : 0, lo < hi ? found[1] : 0);
     Segment s;
 
-    if (warp >= kCopyWarp) {
-        fewer_registers<kOtherRegisters>();
-        if (warp == kCopyWarp) {
+    if (warp >= 8) {
+        if (warp == kKeyWarp || warp == kValueWarp) {
             // ------------------------------------------------------- copies
+            const bool keys = warp == kKeyWarp;
+            const CUtensorMap* map = keys ? &k_map : &v_map;
             const int box = min(a.page_size, kTile);          // slots a box
             const int boxes = kTile / box;
             const int which = lane / S::kHalves, half = lane % S::kHalves;
@@ -354,31 +383,25 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     const int p = __ldg(table + slot / a.page_size);
                     return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
                 };
-                auto copy = [&](const CUtensorMap* map, uint32_t item, int j, int page) {
+                int page = page_of(0);
+                for (int j = 0; j < n; ++j) {
+                    const int after = page_of(j + 1);
+                    const uint32_t item = items + (keys ? key_item(j) : value_item(j, n));
                     const uint32_t slot = item % S::kSlots;
-                    const uint32_t round = item / S::kSlots;
-                    mbar_wait(&empty[slot], (round & 1) ^ 1, failed);
+                    mbar_wait(&empty[slot], (item / S::kSlots & 1) ^ 1, failed);
                     if (lane == 0) mbar_arrive_expect(&full[slot], S::kTileBytes);
                     __syncwarp();
-                    if (mine) {
-                        const uint32_t dst = smem_addr(ring) + slot * S::kTileBytes +
-                                             half * S::kHalfBytes + which * box * 128;
-                        copy_box(map, dst, &full[slot], half * 64,
+                    if (mine)
+                        copy_box(map,
+                                 smem_addr(ring) + slot * S::kTileBytes + half * S::kHalfBytes +
+                                     which * box * 128,
+                                 &full[slot], half * 64,
                                  ((s.k0 + j) * kTile + which * box) % a.page_size, s.head, page);
-                    }
-                };
-                int page = page_of(0), after = page_of(1);
-                copy(&k_map, items, 0, page);
-                for (int j = 0; j < n; ++j) {
-                    const int then = page_of(j + 2);
-                    if (j + 1 < n) copy(&k_map, items + key_item(j + 1), j + 1, after);
-                    copy(&v_map, items + value_item(j, n), j, page);
                     page = after;
-                    after = then;
                 }
                 items += 2 * n;
             }
-            if (*failed) {
+            if (*failed && keys) {
                 // copies may be in flight: they end before the block does
                 for (uint32_t i = items > S::kSlots ? items - S::kSlots : 0; i < items; ++i) {
                     const long long start = clock64();
@@ -542,7 +565,6 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             }
         }
     } else {
-        more_registers<kGroupRegisters>();
         // ------------------------------------------------------- softmax
         const int w = warp >> 2;
         const int row = threadIdx.x & 127;
@@ -568,19 +590,31 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             if (s.pair || w == 0) {
                 if (seg > 0) mbar_wait(&q_empty, (seg - 1) & 1, failed);
                 uint8_t* tile = q_tiles + (s.pair ? w : 0) * S::kTileBytes;
-                for (int i = row; i < rows * (D / 8); i += 128) {
-                    const int r = i / (D / 8), ch = i % (D / 8);
-                    const int nd = (first_row + r) / group;
-                    const int hd = s.head * group + (first_row + r) - nd * group;
-                    uint4 v = __ldg(reinterpret_cast<const uint4*>(
-                        static_cast<const unsigned short*>(a.q) +
-                        (int64_t)(s.q.begin + nd) * a.q_token + hd * a.q_head + ch * 8));
-                    v.x ^= args.flip;
-                    v.y ^= args.flip;
-                    v.z ^= args.flip;
-                    v.w ^= args.flip;
-                    *reinterpret_cast<uint4*>(tile + (ch / 8) * S::kHalfBytes + r * 128 +
-                                              (((ch & 7) ^ (r & 7)) << 4)) = v;
+                // a thread's rows are 1024 / D apart; four loads in flight
+                constexpr int kPer = D / 8;
+                const int ch = row % kPer;
+                for (int r0 = row / kPer; r0 < rows; r0 += 4 * (128 / kPer)) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int r = r0 + u * (128 / kPer);
+                        if (r < rows) {
+                            const int nd = (int)((uint32_t)(first_row + r) / (uint32_t)group);
+                            const int hd = s.head * group + (first_row + r) - nd * group;
+                            x[u] = __ldg(reinterpret_cast<const uint4*>(
+                                static_cast<const unsigned short*>(a.q) +
+                                (int64_t)(s.q.begin + nd) * a.q_token + hd * a.q_head + ch * 8));
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int r = r0 + u * (128 / kPer);
+                        if (r < rows)
+                            *reinterpret_cast<uint4*>(tile + (ch / 8) * S::kHalfBytes + r * 128 +
+                                                      (((ch & 7) ^ (r & 7)) << 4)) =
+                                make_uint4(x[u].x ^ args.flip, x[u].y ^ args.flip,
+                                           x[u].z ^ args.flip, x[u].w ^ args.flip);
+                    }
                 }
                 fence_async_proxy();
                 mbar_arrive(&q_full[w]);
@@ -593,33 +627,47 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 mbar_wait(&s_full[w], count & 1, failed);
                 tmem_fence_after();
                 if (active) {
-                    uint32_t v[4][32];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_load(s_at + 32 * q, v[q]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_wait_load(v[q]);
                     const int first = (s.k0 + j) * kTile;
                     const bool masked = first + kTile > s.q.ctx;
+                    // The row's scores are read twice, 32 columns at a time and
+                    // the next ones on their way: for the maximum, then for
+                    // the weights.  Keeping all 128 between would not leave
+                    // registers for the rest.
+                    uint32_t bits[4];
                     if (masked) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t bits =
-                                here ? seen_bits(mask, a.mask_words, s.q.ctx, s.q.length,
-                                                 first + 32 * q)
-                                     : 0u;
+                        for (int q = 0; q < 4; ++q)
+                            bits[q] = here ? seen_bits(mask, a.mask_words, s.q.ctx, s.q.length,
+                                                       first + 32 * q)
+                                           : 0u;
+                        __syncwarp();
+                    }
+                    auto hide = [&](uint32_t (&x)[32], int q) {
+                        if (masked) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (!(bits >> i & 1)) v[q][i] = 0xFF800000u;  // -infinity
+                                if (!(bits[q] >> i & 1)) x[i] = 0xFF800000u;  // -infinity
                         }
-                    }
-                    float m4[4];
+                    };
+                    uint32_t v[2][32];
+                    float m = -INFINITY;
+                    tmem_load(s_at, v[0]);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        m4[q] = __uint_as_float(v[q][0]);
+                        uint32_t(&x)[32] = v[q & 1];
+                        tmem_wait_load(x);
+                        tmem_load(s_at + 32 * ((q + 1) & 3), v[(q + 1) & 1]);
+                        hide(x, q);
+                        float m0 = max3(m, as_float(x[0]), as_float(x[1]));
+                        float m1 = fmaxf(as_float(x[2]), as_float(x[3]));
 #pragma unroll
-                        for (int i = 1; i < 32; ++i) m4[q] = fmaxf(m4[q], __uint_as_float(v[q][i]));
+                        for (int i = 4; i < 32; i += 4) {
+                            m0 = max3(m0, as_float(x[i]), as_float(x[i + 1]));
+                            m1 = max3(m1, as_float(x[i + 2]), as_float(x[i + 3]));
+                        }
+                        m = fmaxf(m0, m1);
                     }
-                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    tmem_wait_load(v[0]);  // the first quarter again
                     // a new maximum only where it grew by more than kLag
                     const bool grow = here && (m - top) * c > kLag;
                     const bool set = here && top == -INFINITY && m > -INFINITY;
@@ -631,7 +679,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         if (begun) {
                             mbar_wait(&pv_done[w], (count - 1) & 1, failed);
                             tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int q = 0; q < D / 32; ++q) {
                                 uint32_t o[32];
                                 tmem_load(o_at + 32 * q, o);
@@ -646,22 +694,32 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     // rows that have seen nothing yet have only -infinities:
                     // exponents relative to 0 make zeros of them
                     const float shift = top == -INFINITY ? 0.f : top * c;
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t c2 = pack_f32(c, c), shift2 = pack_f32(-shift, -shift);
+                    uint64_t part[2] = {0, 0};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t p[32];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t(&x)[32] = v[q & 1];
+                        if (q > 0) tmem_wait_load(x);
+                        if (q < 3) tmem_load(s_at + 32 * (q + 1), v[(q + 1) & 1]);
+                        hide(x, q);
+                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int q = 2 * h + i / 16, e = (2 * i) % 32;
-                            const float x0 = exp2_fast(fmaf(__uint_as_float(v[q][e]), c, -shift));
-                            const float x1 =
-                                exp2_fast(fmaf(__uint_as_float(v[q][e + 1]), c, -shift));
-                            part[i & 3] += x0 + x1;
+                        for (int i = 0; i < 16; ++i) {
+                            float x0, x1;
+                            unpack_f32(fma_f32x2(pack_f32(as_float(x[2 * i]), as_float(x[2 * i + 1])),
+                                                 c2, shift2),
+                                       x0, x1);
+                            x0 = exp2_fast(x0);
+                            x1 = exp2_fast(x1);
+                            part[i & 1] = add_f32x2(part[i & 1], pack_f32(x0, x1));
                             p[i] = round_pair<kBf16>(x0, x1);
                         }
-                        tmem_store(s_at + 32 * h, p);
+                        // over columns whose scores have been read
+                        tmem_store(s_at + 16 * q, p);
                     }
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    float p0, p1;
+                    unpack_f32(add_f32x2(part[0], part[1]), p0, p1);
+                    sum += p0 + p1;
                     tmem_wait_store();
                 }
                 tmem_fence_before();
@@ -681,7 +739,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             if (join && w == 1) {
                 mbar_wait(&q_empty, seg & 1, failed);   // the queries have been read
                 if (active) {
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t o[32];
                         tmem_load(o_at + 32 * q, o);
@@ -717,10 +775,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                                state_at(blockIdx.x, s.k0 == 0 ? 1 : 0, args.rows_cap, D);
                 const int state_row = (s.pair ? w * kTile : 0) + row;
                 float* pairs = state + 2 * state_row;
-                float* acc = state + 2 * args.rows_cap + (int64_t)state_row * D;
+                float* acc = state + 2 * args.rows_cap + 8 * state_row;
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 if (active) {
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t o[32];
                         if (begun) {
@@ -774,11 +832,11 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                                 dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
                             }
                         } else if (here) {
-                            float4* dst = reinterpret_cast<float4*>(acc + 32 * q);
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2],
-                                                     x[4 * i + 3]);
+                                *reinterpret_cast<float4*>(
+                                    acc + (q * 4 + i / 2) * 8 * args.rows_cap + (i & 1) * 4) =
+                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                         }
                         __syncwarp();  // the next load is the whole warp's
                     }
@@ -812,66 +870,99 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
 constexpr int kJoinThreads = 256;
 
 // The cut units' rows: for a row, the states of the blocks that share its unit,
-// in block order.  One block a token, one warp a row at a time, D / 32
-// accumulators a lane.
+// in block order.  A warp takes a row: its lanes read up to 32 states' pairs at
+// once, then every lane D / 32 accumulators of each state, eight states' loads in
+// flight.  Blocks of eight rows of one token, so that one token's call spreads
+// over the device.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
 tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
+    constexpr int E = D / 32;
     const ple_tree_attention_args& a = args.a;
     __shared__ int64_t scratch[2 * (kJoinThreads / 32)];
     wait_grid_before();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = blockIdx.x;
+    const int h = blockIdx.y * (kJoinThreads / 32) + warp;
     const int r = warp_request(a.cu_seqlens, a.num_requests, t, lane);
     int64_t before, total;
     tiles_before<kJoinThreads>(a, r, scratch, before, total);
     const Request q = request_of(a, r);
     const int group = a.q_heads / a.kv_heads;
     const int64_t node = t - q.begin;
-    if (node < 0 || node >= q.nodes) return;
+    if (node < 0 || node >= q.nodes || h >= a.q_heads) return;
     const float* space = static_cast<const float*>(a.workspace);
-    for (int h = warp; h < a.q_heads; h += kJoinThreads / 32) {
-        const int head = h / group;
-        const int64_t row = node * group + (h - head * group);
-        const int64_t unit = row / kUnitRows;
-        const int local = (int)(row - unit * kUnitRows);
-        const int64_t first = before + (head * (int64_t)q.units + unit) * q.tiles;
-        const int c0 = share_of(total, first, args.blocks);
-        const int c1 = share_of(total, first + q.tiles - 1, args.blocks);
-        bool failed = false;
-        for (int c = c0; c <= c1; ++c) failed |= reinterpret_cast<const int*>(space)[c] != 0;
-        if (c0 == c1 && !failed) continue;  // the block wrote it
-        constexpr int E = D / 32;
-        float m = -INFINITY, sum = 0.f, acc[E] = {};
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t lo = share_begin(total, c, args.blocks);
-            if (lo == share_begin(total, c + 1, args.blocks)) continue;  // more shares than tiles
-            const float* state = space + state_at(c, lo <= first ? 1 : 0, args.rows_cap, D);
-            const float2 p = __ldcg(reinterpret_cast<const float2*>(state) + local);
-            float x[E];
-            const float* from = state + 2 * args.rows_cap + (int64_t)local * D + lane * E;
+    const int head = h / group;
+    const int64_t row = node * group + (h - head * group);
+    const int64_t unit = row / kUnitRows;
+    const int local = (int)(row - unit * kUnitRows);
+    const int64_t first = before + (head * (int64_t)q.units + unit) * q.tiles;
+    const int blocks = shares(total, args.blocks);
+    const int c0 = share_of(total, first, blocks);
+    const int c1 = share_of(total, first + q.tiles - 1, blocks);
+    float m = -INFINITY, sum = 0.f, acc[E] = {};
+    bool failed = false;
+    for (int from = c0; from <= c1; from += 32) {
+        const int c = from + lane;
+        const bool here = c <= c1;
+        if (here) failed |= reinterpret_cast<const int*>(space)[c] != 0;
+        if (c0 == c1) break;  // the block wrote the row
+        // the unit starts in the first of its blocks and is begun in the others
+        const int64_t mine = state_at(c, c == c0 ? 1 : 0, args.rows_cap, D);
+        float2 p = make_float2(-INFINITY, 0.f);
+        if (here) p = __ldcg(reinterpret_cast<const float2*>(space + mine) + local);
+        float now = fmaxf(m, p.x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = __ldcg(from + e);
-            // no maximum: nothing seen (zeros), or only NaN, which stays
-            const float now = fmaxf(m, p.x);
-            const float f = m == -INFINITY ? 1.f : exp2_fast(m - now);
-            const float g = p.x == -INFINITY ? 1.f : exp2_fast(p.x - now);
-            sum = sum * f + p.y * g;
+        for (int d = 16; d >= 1; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+        // no maximum: nothing seen (zeros), or only NaN, which stays
+        const float keep = m == -INFINITY ? 1.f : exp2_fast(m - now);
+        const float f = p.x == -INFINITY ? 1.f : exp2_fast(p.x - now);
+        float part = p.y * f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + x[e] * g;
-            m = now;
+        for (int d = 16; d >= 1; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+        sum = sum * keep + part;
+        m = now;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= keep;
+        const int n = min(32, c1 - from + 1);
+        const int64_t at = 2 * args.rows_cap +
+                           ((lane * E / 8) * (int64_t)args.rows_cap + local) * 8 + lane * E % 8;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float x[8][E];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t theirs = __shfl_sync(0xffffffffu, mine, i0 + i & 31);
+                if (i0 + i < n) {
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 y =
+                            __ldcg(reinterpret_cast<const float2*>(space + theirs + at + e));
+                        x[i][e] = y.x;
+                        x[i][e + 1] = y.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, i0 + i & 31);
+                if (i0 + i < n) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[i][e], g, acc[e]);
+                }
+            }
         }
-        if (failed) sum = __int_as_float(0x7FC00000);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t o = t * a.q_heads + h;
-        unsigned short* dst = static_cast<unsigned short*>(a.out) + o * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t*>(dst + e) =
-                round_pair<kBf16>(acc[e] * inv, acc[e + 1] * inv);
-        if (lane == 0 && a.lse != nullptr)
-            a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
     }
+    failed = __any_sync(0xffffffffu, failed);
+    if (c0 == c1 && !failed) return;
+    if (failed) sum = __int_as_float(0x7FC00000);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t o = t * a.q_heads + h;
+    unsigned short* dst = static_cast<unsigned short*>(a.out) + o * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = round_pair<kBf16>(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && a.lse != nullptr)
+        a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -935,8 +1026,11 @@ cudaError_t launch_tc(const TcArgs& args, const CUtensorMap& k, const CUtensorMa
     e = launch_kernel(fn, dim3((unsigned)args.blocks), dim3(kThreads), Shape<D>::kSmem, stream,
                       programmatic_launch(), args, k, v);
     if (e != cudaSuccess) return e;
-    return launch_kernel(tree_attention_join_kernel<D, kBf16>, dim3((unsigned)args.a.num_tokens),
-                         dim3(kJoinThreads), 0, stream, programmatic_launch(), args);
+    const int rows = kJoinThreads / 32;
+    return launch_kernel(
+        tree_attention_join_kernel<D, kBf16>,
+        dim3((unsigned)args.a.num_tokens, (unsigned)((args.a.q_heads + rows - 1) / rows)),
+        dim3(kJoinThreads), 0, stream, programmatic_launch(), args);
 }
 
 }  // namespace
