@@ -56,6 +56,18 @@ __device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, volati
     __syncwarp();
 }
 
+// A whole warp waits until *count has come to `least`, as mbar_wait does.
+__device__ __forceinline__ void count_wait(const volatile uint32_t* count, uint32_t least,
+                                           volatile int* failed) {
+    if ((int32_t)(*count - least) < 0) {
+        const long long start = clock64();
+        while ((int32_t)(*count - least) < 0 && !*failed) {
+            if (clock64() - start > kWaitClocks) *failed = 1;
+        }
+    }
+    __syncwarp();
+}
+
 __device__ __forceinline__ void fence_barrier_init() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -64,6 +76,16 @@ __device__ __forceinline__ void fence_barrier_init() {
 // instructions after it.
 __device__ __forceinline__ void fence_async_proxy() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// One lane of a whole warp, the same one every time, known as one to the
+// compiler (so operands of single-thread instructions stay uniform).
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t chosen;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(chosen));
+    return chosen != 0;
 }
 
 template <int kThreads>

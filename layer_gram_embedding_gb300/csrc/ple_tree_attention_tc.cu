@@ -13,9 +13,9 @@
 // 2^8 and the sum and O share the old maximum, so nothing is lost.
 //
 // Blocks.  One block an SM: two warps that copy key and value tiles into a ring
-// of shared memory (tiled bulk copies, page by page, 128-byte swizzle), a warp
-// that issues the matrix instructions, and two groups of four warps that do the
-// softmax, one row a thread.  With more than 128 rows the two groups take 128
+// of shared memory (tiled bulk copies, page by page, 128-byte swizzle), and two
+// groups of four warps that do the softmax, one row a thread, each with a warp
+// that issues its matrix instructions.  With more than 128 rows the two groups take 128
 // each over the same tiles, so that a key is read once for 256 rows; with fewer
 // they take the tiles in turn over the same rows and are joined in shared memory.
 // Either way one group's softmax runs while the tensor cores work for the other.
@@ -45,8 +45,8 @@ namespace {
 
 constexpr int kTile = 128;           // keys a tile, rows a matrix instruction
 constexpr int kUnitRows = 2 * kTile; // rows a unit
-constexpr int kThreads = 384;        // two groups of 128; two copying, an issuing, an idle warp
-constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10;
+constexpr int kThreads = 384;        // two groups of 128, two copying and two issuing warps
+constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10;  // and 11: the second group's issuing
 constexpr int kMaxBlocks = 1024;     // blocks of a launch: an SM's number of them is far below
 constexpr float kLag = 8.0f;         // how far, in the exponent, a maximum may lag
 
@@ -310,13 +310,20 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     const ple_tree_attention_args& a = args.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
-    __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_full[2], pv_done[2], last;
+    __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_full[2], pv_done[2];
+    __shared__ __align__(8) uint64_t cleaned, last;
+    // How often a slot was armed for a tile.  A barrier tells only the parity of
+    // its phase, and neither a copying warp nor an issuing one sees every tile
+    // of a slot: who waits for the slot's round r looks here first, where r (or
+    // r + 1, armed) says that all rounds before are over.
+    __shared__ uint32_t armed_s[S::kSlots];
     __shared__ int64_t scratch[2 * (kThreads / 32)], found[2];
     __shared__ uint32_t tmem_s;
     __shared__ int failed_s;
     __shared__ int bad_s[2];          // a segment's drafted values hold infinities or NaN
     __shared__ float join_s[kTile][2];
     volatile int* failed = &failed_s;
+    volatile uint32_t* armed = armed_s;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023) & ~1023u) - smem_addr(smem_raw));
@@ -326,7 +333,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);
+            armed_s[i] = 0;
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&q_full[w], 128);
@@ -335,8 +343,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             mbar_init(&pv_done[w], 1);
             bad_s[w] = 0;
         }
-        mbar_init(&q_empty, 1);
-        mbar_init(&last, 1);
+        mbar_init(&q_empty, 2);
+        mbar_init(&cleaned, 1);
+        mbar_init(&last, 2);
         failed_s = 0;
         fence_barrier_init();
     }
@@ -387,9 +396,14 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 for (int j = 0; j < n; ++j) {
                     const int after = page_of(j + 1);
                     const uint32_t item = items + (keys ? key_item(j) : value_item(j, n));
-                    const uint32_t slot = item % S::kSlots;
-                    mbar_wait(&empty[slot], (item / S::kSlots & 1) ^ 1, failed);
-                    if (lane == 0) mbar_arrive_expect(&full[slot], S::kTileBytes);
+                    const uint32_t slot = item % S::kSlots, round = item / S::kSlots;
+                    count_wait(&armed[slot], round, failed);
+                    mbar_wait(&empty[slot], (round & 1) ^ 1, failed);
+                    if (__any_sync(0xffffffffu, *failed)) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect(&full[slot], S::kTileBytes);
+                        armed[slot] = round + 1;
+                    }
                     __syncwarp();
                     if (mine)
                         copy_box(map,
@@ -401,74 +415,64 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 items += 2 * n;
             }
-            if (*failed && keys) {
+            if (*failed) {
                 // copies may be in flight: they end before the block does
-                for (uint32_t i = items > S::kSlots ? items - S::kSlots : 0; i < items; ++i) {
+                for (int i = 0; i < S::kSlots; ++i) {
+                    const uint32_t rounds = armed[i];
                     const long long start = clock64();
-                    while (!mbar_try(&full[i % S::kSlots], i / S::kSlots & 1) &&
+                    while (rounds != 0 && !mbar_try(&full[i], (rounds - 1) & 1) &&
                            clock64() - start < kWaitClocks) {
                     }
                 }
+                __syncwarp();
             }
-        } else if (warp == kIssueWarp) {
+        } else {
             // -------------------------------------------- matrix instructions
+            // one warp a group, so that neither group waits in the other's
+            // order; one lane issues (tcgen05 work of one thread stays in order:
+            // a group's next scores follow the product that reads its weights)
             constexpr uint32_t kScoreWord = mma_word(kBf16, false, kTile, kTile);
             constexpr uint32_t kOutWord = mma_word(kBf16, true, kTile, D);
-            uint32_t items = 0;
-            uint32_t q_count[2] = {0, 0}, p_count[2] = {0, 0};
-            uint32_t seg = 0;
+            const int w = warp == kIssueWarp ? 0 : 1;
+            const bool elected = elect_lane();
+            const uint32_t s_at = tmem + w * S::kGroupColumns, o_at = s_at + S::kOut;
+            const uint32_t ring_at = smem_addr(ring);
+            uint32_t items = 0, p_count = 0, pairs = 0, cleanings = 0, seg = 0;
             while (walk.next(s)) {
                 const int n = s.k1 - s.k0;
-                if (lane == 0) bad_s[seg & 1] = 0;
-                auto wait_item = [&](uint32_t item) {
-                    mbar_wait(&full[item % S::kSlots], item / S::kSlots & 1, failed);
+                auto wait_item = [&](uint32_t item) -> uint32_t {
+                    const uint32_t slot = item % S::kSlots, round = item / S::kSlots;
+                    count_wait(&armed[slot], round + 1, failed);
+                    mbar_wait(&full[slot], round & 1, failed);
+                    return slot;
                 };
-                auto slot_of = [&](uint32_t item) -> uint32_t {
-                    return smem_addr(ring) + item % S::kSlots * S::kTileBytes;
+                // a tile is free when both groups are done with it; where the
+                // groups take tiles in turn its only user says so twice
+                auto release = [&](uint32_t slot) {
+                    mma_commit(&empty[slot]);
+                    if (!s.pair) mma_commit(&empty[slot]);
                 };
                 // a descriptor's address counts 16 bytes and stays below 2^14, so
                 // steps within a tile add to it
-                auto scores = [&](int w, uint32_t item) {
-                    if (lane == 0) {
-                        const uint64_t qd = operand_desc(
-                            smem_addr(q_tiles) + (s.pair ? w : 0) * S::kTileBytes, 16);
-                        const uint64_t kd = operand_desc(slot_of(item), 16);
+                const uint64_t qd =
+                    operand_desc(smem_addr(q_tiles) + (s.pair ? w : 0) * S::kTileBytes, 16);
+                auto scores = [&](uint32_t item) {
+                    const uint32_t slot = wait_item(item);
+                    const uint64_t kd = operand_desc(ring_at + slot * S::kTileBytes, 16);
+                    if (elected) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             const uint32_t at = ((k / 4) * S::kHalfBytes + (k % 4) * 32) >> 4;
-                            mma_smem(tmem + w * S::kGroupColumns, qd + at, kd + at, kScoreWord,
-                                     k != 0);
+                            mma_smem(s_at, qd + at, kd + at, kScoreWord, k != 0);
                         }
                         mma_commit(&s_full[w]);
+                        release(slot);
                     }
                     __syncwarp();
-                };
-                auto values = [&](int w, uint32_t item, bool accumulate) {
-                    if (lane == 0) {
-                        const uint64_t vd = operand_desc(slot_of(item), S::kHalfBytes);
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_tmem(tmem + w * S::kGroupColumns + S::kOut,
-                                     tmem + w * S::kGroupColumns + k * 8, vd + (k * 16 * 128 >> 4),
-                                     kOutWord, accumulate || k != 0);
-                        mma_commit(&pv_done[w]);
-                    }
-                    __syncwarp();
-                };
-                auto release = [&](uint32_t item) {
-                    if (lane == 0) mma_commit(&empty[item % S::kSlots]);
-                    __syncwarp();
-                };
-                auto wait_weights = [&](int w) {
-                    mbar_wait(&p_full[w], p_count[w]++ & 1, failed);
-                    tmem_fence_after();
                 };
                 // values past the request's tokens, and drafted ones that are not
                 // finite, are cleared before the product reads them
-                auto clean = [&](int j, uint32_t item) {
-                    const int first = (s.k0 + j) * kTile;
-                    if (first + kTile <= s.q.ctx) return;
-                    uint8_t* tile = ring + (item % S::kSlots) * S::kTileBytes;
+                auto clean = [&](int first, uint8_t* tile) {
                     const int from = max(s.q.ctx - first, 0), upto = min(s.q.length - first, kTile);
                     constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
                     bool bad = false;
@@ -503,66 +507,49 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     __syncwarp();
                 };
 
-                mbar_wait(&q_full[0], q_count[0]++ & 1, failed);
-                if (s.pair) mbar_wait(&q_full[1], q_count[1]++ & 1, failed);
+                mbar_wait(&q_full[0], seg & 1, failed);
+                if (s.pair && w == 1) mbar_wait(&q_full[1], pairs & 1, failed);
+                if (s.pair) ++pairs;
                 tmem_fence_after();
-                if (s.pair) {
-                    wait_item(items);
-                    scores(0, items);
-                    scores(1, items);
-                    release(items);
-                    for (int j = 0; j < n; ++j) {
-                        const uint32_t v = items + value_item(j, n), k = items + key_item(j + 1);
-#pragma unroll 1
-                        for (int w = 0; w < 2; ++w) {
-                            wait_weights(w);
-                            if (w == 0) {
-                                wait_item(v);
-                                clean(j, v);
-                            }
-                            values(w, v, j > 0);
-                            if (w == 1) release(v);
-                            if (j + 1 < n) {
-                                if (w == 0) wait_item(k);
-                                scores(w, k);
-                                if (w == 1) release(k);
-                            }
+                const int from = s.pair ? 0 : w, step = s.pair ? 1 : 2;
+                if (from < n) scores(items + key_item(from));
+                for (int j = from; j < n; j += step) {
+                    mbar_wait(&p_full[w], p_count++ & 1, failed);
+                    tmem_fence_after();
+                    const uint32_t slot = wait_item(items + value_item(j, n));
+                    const int first = (s.k0 + j) * kTile;
+                    if (first + kTile > s.q.ctx) {
+                        if (!s.pair || w == 0) clean(first, ring + slot * S::kTileBytes);
+                        if (s.pair) {
+                            if (w == 0 && lane == 0) mbar_arrive(&cleaned);
+                            mbar_wait(&cleaned, cleanings++ & 1, failed);
                         }
                     }
-                } else {
-                    for (int w = 0; w < min(2, n); ++w) {
-                        const uint32_t k = items + key_item(w);
-                        wait_item(k);
-                        scores(w, k);
-                        release(k);
+                    if (__any_sync(0xffffffffu, *failed)) break;
+                    const uint64_t vd = operand_desc(ring_at + slot * S::kTileBytes, S::kHalfBytes);
+                    if (elected) {
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_tmem(o_at, s_at + k * 8, vd + (k * 16 * 128 >> 4), kOutWord,
+                                     j != from || k != 0);
+                        mma_commit(&pv_done[w]);
+                        release(slot);
                     }
-                    for (int j = 0; j < n; ++j) {
-                        const int w = j & 1;
-                        const uint32_t v = items + value_item(j, n);
-                        wait_weights(w);
-                        wait_item(v);
-                        clean(j, v);
-                        values(w, v, j > 1);
-                        release(v);
-                        if (j + 2 < n) {
-                            const uint32_t k = items + key_item(j + 2);
-                            wait_item(k);
-                            scores(w, k);
-                            release(k);
-                        }
-                    }
+                    __syncwarp();
+                    if (j + step < n) scores(items + key_item(j + step));
                 }
-                if (lane == 0) mma_commit(&q_empty);
+                if (elected) mma_commit(&q_empty);
                 __syncwarp();
                 items += 2 * n;
                 ++seg;
             }
-            if (lane == 0) mma_commit(&last);
+            // everything issued is done before the block ends, also after a failure
+            if (elected) mma_commit(&last);
             __syncwarp();
-            // also after a failure: nothing runs on past the block
             const long long start = clock64();
             while (!mbar_try(&last, 0) && clock64() - start < kWaitClocks) {
             }
+            __syncwarp();
         }
     } else {
         // ------------------------------------------------------- softmax
@@ -589,6 +576,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             // this group's queries, rows of the unit, into swizzled shared memory
             if (s.pair || w == 0) {
                 if (seg > 0) mbar_wait(&q_empty, (seg - 1) & 1, failed);
+                if (w == 0 && row == 0) bad_s[seg & 1] = 0;
                 uint8_t* tile = q_tiles + (s.pair ? w : 0) * S::kTileBytes;
                 // a thread's rows are 1024 / D apart; four loads in flight
                 constexpr int kPer = D / 8;
@@ -625,6 +613,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             bool begun = false;
             for (int j = s.pair ? 0 : w; j < n; j += step) {
                 mbar_wait(&s_full[w], count & 1, failed);
+                if (__any_sync(0xffffffffu, *failed)) break;
                 tmem_fence_after();
                 if (active) {
                     const int first = (s.k0 + j) * kTile;
@@ -728,10 +717,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 begun = true;
                 ++count;
             }
-            if (begun) {
-                mbar_wait(&pv_done[w], (count - 1) & 1, failed);
-                tmem_fence_after();
-            }
+            if (begun) mbar_wait(&pv_done[w], (count - 1) & 1, failed);
+            tmem_fence_after();
 
             // ------------------------------------ the segment's rows go out
             const bool join = !s.pair && n > 1;   // both groups hold states of the same rows
@@ -1056,7 +1043,9 @@ cudaError_t launch_tree_attention_tc(const ple_tree_attention_args& a, const Dev
     args.a = a;
     args.blocks = tc_blocks(dev);
     args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads);
-    args.c = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
+    // a scale of 0 as the least normal number: every exponent still rounds to 0,
+    // and a hidden score stays -infinity
+    args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     args.flip = a.scale < 0 ? 0x80008000u : 0u;
     if (a.head_dim == 64)
         return a.dtype == PLE_BF16 ? launch_tc<64, true>(args, k, v, stream)

@@ -379,6 +379,12 @@ ATTENTION_CASES = [
     ([4] * 37, list(range(0, 370, 10)), 4, 2, 64, 16, "phsd"),
     ([2], [5000], 4, 1, 128, 64, "phsd"),
     ([512], [130], 2, 1, 64, 64, "phsd"),
+    # more tiles than the device has SMs: shares of many tiles and requests
+    ([2] * 40, [100 + 19 * i for i in range(40)], 16, 8, 128, 16, "phsd"),
+    ([3, 0, 1, 30] * 12, [37 * i for i in range(48)], 16, 4, 64, 64, "phsd"),
+    ([40, 64, 33], [2500, 900, 3000], 32, 4, 64, 32, "phsd"),
+    ([18], [9001], 32, 4, 128, 64, "phsd"),
+    ([1, 1], [20000, 11], 4, 2, 128, 128, "phsd"),
 ]
 
 
@@ -450,6 +456,15 @@ def test_nothing_unseen_has_an_effect(D):
         out[sees] = plain[sees]
         assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
         cache.v[int(p), :, s] = old
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0])
+@pytest.mark.parametrize("D", [64, 96])
+def test_attention_scales(D, scale):
+    rng = np.random.default_rng(19)
+    q, cache, ctx, cu, masks = attention_inputs(rng, [5, 70], [200, 31], 4, 2, D, 16,
+                                                torch.bfloat16)
+    check_attention(q, cache, ctx, cu, masks, scale=scale)
 
 
 def test_attention_masks_bits_past_the_nodes_are_ignored():
