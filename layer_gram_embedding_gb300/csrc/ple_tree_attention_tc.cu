@@ -97,47 +97,43 @@ __device__ __forceinline__ Request request_of(const ple_tree_attention_args& a, 
     return q;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
+// First tile of share c of `shares`, and the share of a tile.
+__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int shares) {
+    return total * c / shares;
+}
+__device__ __forceinline__ int share_of(int64_t total, int64_t tile, int shares) {
+    return (int)(((tile + 1) * shares - 1) / total);
 }
 
-// The tiles of requests [0, r) and of all: every thread of the block calls it.
-template <int kBlock>
-__device__ __forceinline__ void tiles_before(const ple_tree_attention_args& a, int r,
-                                             int64_t* scratch, int64_t& before, int64_t& total) {
-    int64_t b = 0, t = 0;
-    for (int i = threadIdx.x; i < a.num_requests; i += kBlock) {
-        const int64_t w = request_of(a, i).work;
-        t += w;
-        if (i < r) b += w;
-    }
-    b = warp_sum(b);
-    t = warp_sum(t);
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) {
-        scratch[2 * warp] = b;
-        scratch[2 * warp + 1] = t;
-    }
-    __syncthreads();
-    before = total = 0;
-    for (int w = 0; w < kBlock / 32; ++w) {
-        before += scratch[2 * w];
-        total += scratch[2 * w + 1];
-    }
-}
+// A block's tiles [lo, hi) of `total`, the request that owns the first one, and
+// the tiles before that request.  Not more shares than tiles.
+struct Share {
+    int64_t lo, hi, total, before;
+    int32_t first, shares;
+};
 
-// The request that owns tile `at`, and the tiles before it.  Every thread of the
-// block calls it; the owner's thread writes the answer.
+// Every thread of the block calls it; the answer is in *share.  Requests are
+// scanned a block's width at a time: once where they fit, else once for the
+// total and once for the owner.
 template <int kBlock>
-__device__ __forceinline__ void find_tile(const ple_tree_attention_args& a, int64_t at,
-                                          int64_t* scratch, int64_t* found) {
-    int64_t base = 0;
+__device__ __forceinline__ void find_share(const ple_tree_attention_args& a, int blocks,
+                                           int64_t* scratch, Share* share) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int first = 0; first < a.num_requests; first += kBlock) {
-        const int r = first + threadIdx.x;
-        const int64_t w = r < a.num_requests ? request_of(a, r).work : 0;
+    const int B = a.num_requests;
+    int64_t total = 0;
+    if (B > kBlock) {
+        int64_t mine = 0;
+        for (int r = threadIdx.x; r < B; r += kBlock) mine += request_of(a, r).work;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+        if (lane == 0) scratch[warp] = mine;
+        __syncthreads();
+        for (int k = 0; k < kBlock / 32; ++k) total += scratch[k];
+    }
+    int64_t base = 0;
+    for (int from = 0; from < B; from += kBlock) {
+        const int r = from + threadIdx.x;
+        const int64_t w = r < B ? request_of(a, r).work : 0;
         int64_t upto = w;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -148,18 +144,27 @@ __device__ __forceinline__ void find_tile(const ple_tree_attention_args& a, int6
         if (lane == 31) scratch[warp] = upto;
         __syncthreads();
         int64_t before = base, all = base;
+#pragma unroll
         for (int k = 0; k < kBlock / 32; ++k) {
-            if (k < warp) before += scratch[k];
-            all += scratch[k];
+            const int64_t x = scratch[k];
+            if (k < warp) before += x;
+            all += x;
         }
-        if (w > 0 && before + upto - w <= at && at < before + upto) {
-            found[0] = r;
-            found[1] = before + upto - w;
+        if (B <= kBlock) total = all;
+        const int shares = (int)min(total, (int64_t)blocks);
+        const bool none = (int)blockIdx.x >= shares;
+        const int64_t lo = none ? total : share_begin(total, blockIdx.x, shares);
+        if (none ? r == 0 : (w > 0 && before + upto - w <= lo && lo < before + upto)) {
+            share->lo = lo;
+            share->hi = none ? total : share_begin(total, blockIdx.x + 1, shares);
+            share->total = total;
+            share->before = before + upto - w;
+            share->first = r;
+            share->shares = shares;
         }
         base = all;
-        if (at < base) break;
+        if (lo < base) break;
     }
-    __syncthreads();
 }
 
 // A block's piece of one unit: keys tiles [k0, k1) of `tiles`.
@@ -178,9 +183,8 @@ struct Walk {
     int64_t base;        // tiles before request r
     int r;
     Request q;
-    __device__ __forceinline__ Walk(const ple_tree_attention_args& args, int64_t lo, int64_t hi,
-                                    int first, int64_t before)
-        : a(args), at(lo), end(hi), base(before), r(first) {
+    __device__ __forceinline__ Walk(const ple_tree_attention_args& args, const Share& share)
+        : a(args), at(share.lo), end(share.hi), base(share.before), r(share.first) {
         if (at < end) q = request_of(a, r);
     }
     __device__ __forceinline__ bool next(Segment& s) {
@@ -205,25 +209,34 @@ struct Walk {
     }
 };
 
-// Shares that hold a tile, the first tile of share c, and the share of a tile.
-__device__ __forceinline__ int shares(int64_t total, int blocks) {
-    return (int)min(total, (int64_t)blocks);
-}
-__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int blocks) {
-    return total * c / blocks;
-}
-__device__ __forceinline__ int share_of(int64_t total, int64_t tile, int blocks) {
-    return (int)(((tile + 1) * blocks - 1) / total);
+// The offset of the query of a key head's row.
+__device__ __forceinline__ int64_t query_row(const ple_tree_attention_args& a, const Segment& s,
+                                             int row) {
+    const uint32_t group = a.q_heads / a.kv_heads;
+    const uint32_t node = (uint32_t)row / group;
+    return (s.q.begin + (int64_t)node) * a.q_token +
+           (int64_t)(s.head * group + (row - node * group)) * a.q_head;
 }
 
-// The workspace: a failure flag for each block, then two states a block (0: a
-// unit begun before the block, 1: a unit that starts in it).  A state is a pair
+// The unit that a block starts and leaves unfinished: what the join has to know.
+struct Cut {
+    int32_t last;          // the block that finishes it; below the first one: there is none
+    int32_t rows;
+    int32_t begin;         // the request's first token
+    int32_t first_row;     // the unit's among the key head's rows
+    int32_t head;
+    int32_t unused[3];
+};
+
+// The workspace: each block's cut, then two states a block (0: a unit begun
+// before the block, 1: a unit that starts in it).  A state is a pair
 // (row maximum in the exponent of 2, row sum) for each row, then the accumulators
 // as [D / 8][row][8]: neighbouring threads write, and a row's readers read, whole
 // 32-byte sectors.
 __host__ __device__ __forceinline__ int64_t state_at(int64_t block, int slot, int rows_cap,
                                                      int D) {
-    return kMaxBlocks + (block * 2 + slot) * (int64_t)rows_cap * (D + 2);
+    return kMaxBlocks * (int64_t)(sizeof(Cut) / 4) +
+           (block * 2 + slot) * (int64_t)rows_cap * (D + 2);
 }
 
 // K_j's and V_j's places in the order of copies K_0, K_1, V_0, K_2, V_1, ... of
@@ -317,7 +330,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     // of a slot: who waits for the slot's round r looks here first, where r (or
     // r + 1, armed) says that all rounds before are over.
     __shared__ uint32_t armed_s[S::kSlots];
-    __shared__ int64_t scratch[2 * (kThreads / 32)], found[2];
+    __shared__ int64_t scratch[kThreads / 32];
+    __shared__ Share share_s;
     __shared__ uint32_t tmem_s;
     __shared__ int failed_s;
     __shared__ int bad_s[2];          // a segment's drafted values hold infinities or NaN
@@ -356,19 +370,13 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     }
     wait_grid_before();
 
-    // this block's share of the tiles
-    int64_t unused, total;
-    tiles_before<kThreads>(a, 0, scratch, unused, total);
-    const int blocks = shares(total, args.blocks);
-    const int64_t lo = blockIdx.x < blocks ? share_begin(total, blockIdx.x, blocks) : total;
-    const int64_t hi = blockIdx.x < blocks ? share_begin(total, blockIdx.x + 1, blocks) : total;
-    if (lo < hi) find_tile<kThreads>(a, lo, scratch, found);
+    find_share<kThreads>(a, args.blocks, scratch, &share_s);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_s;
     const int group = a.q_heads / a.kv_heads;
-    Walk walk(a, lo, hi, lo < hi ? (int)found[0] : 0, lo < hi ? found[1] : 0);
+    Walk walk(a, share_s);
     Segment s;
 
     if (warp >= 8) {
@@ -392,6 +400,17 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     const int p = __ldg(table + slot / a.page_size);
                     return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
                 };
+                // this warp is some tiles ahead: the queries come to the L2 cache
+                // before the groups read them
+                if (!keys) {
+                    const int first_row = s.unit * kUnitRows;
+                    for (int r = lane; r < s.rows; r += 32) {
+                        const unsigned short* at = static_cast<const unsigned short*>(a.q) +
+                                                   query_row(a, s, first_row + r);
+#pragma unroll
+                        for (int h = 0; h < S::kHalves; ++h) prefetch_l2(at + 64 * h);
+                    }
+                }
                 int page = page_of(0);
                 for (int j = 0; j < n; ++j) {
                     const int after = page_of(j + 1);
@@ -560,6 +579,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
         const uint32_t o_at = s_at + S::kOut;
         const float c = args.c;
         uint32_t seg = 0, count = 0;
+        Cut cut = {};
+        cut.last = -1;
         while (walk.next(s)) {
             const int n = s.k1 - s.k0;
             const int first_row = s.unit * kUnitRows + (s.pair ? w * kTile : 0);
@@ -578,30 +599,22 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 if (seg > 0) mbar_wait(&q_empty, (seg - 1) & 1, failed);
                 if (w == 0 && row == 0) bad_s[seg & 1] = 0;
                 uint8_t* tile = q_tiles + (s.pair ? w : 0) * S::kTileBytes;
-                // a thread's rows are 1024 / D apart; four loads in flight
+                // 16-byte pieces copied without a register, all in flight at once
                 constexpr int kPer = D / 8;
                 const int ch = row % kPer;
-                for (int r0 = row / kPer; r0 < rows; r0 += 4 * (128 / kPer)) {
-                    uint4 x[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int r = r0 + u * (128 / kPer);
-                        if (r < rows) {
-                            const int nd = (int)((uint32_t)(first_row + r) / (uint32_t)group);
-                            const int hd = s.head * group + (first_row + r) - nd * group;
-                            x[u] = __ldg(reinterpret_cast<const uint4*>(
-                                static_cast<const unsigned short*>(a.q) +
-                                (int64_t)(s.q.begin + nd) * a.q_token + hd * a.q_head + ch * 8));
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int r = r0 + u * (128 / kPer);
-                        if (r < rows)
-                            *reinterpret_cast<uint4*>(tile + (ch / 8) * S::kHalfBytes + r * 128 +
-                                                      (((ch & 7) ^ (r & 7)) << 4)) =
-                                make_uint4(x[u].x ^ args.flip, x[u].y ^ args.flip,
-                                           x[u].z ^ args.flip, x[u].w ^ args.flip);
+                const uint32_t to = smem_addr(tile) + (ch / 8) * S::kHalfBytes;
+                const unsigned short* from = static_cast<const unsigned short*>(a.q) + ch * 8;
+#pragma unroll 4
+                for (int r = row / kPer; r < rows; r += 128 / kPer)
+                    copy16(to + r * 128 + (((ch & 7) ^ (r & 7)) << 4), from + query_row(a, s, first_row + r));
+                copy16_wait();
+                if (args.flip != 0) {
+                    for (int r = row / kPer; r < rows; r += 128 / kPer) {
+                        uint4* at = reinterpret_cast<uint4*>(tile + (ch / 8) * S::kHalfBytes + r * 128 +
+                                                             (((ch & 7) ^ (r & 7)) << 4));
+                        const uint4 x = *at;
+                        *at = make_uint4(x.x ^ args.flip, x.y ^ args.flip, x.z ^ args.flip,
+                                         x.w ^ args.flip);
                     }
                 }
                 fence_async_proxy();
@@ -756,6 +769,14 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     top = m;
                 }
                 const bool whole = s.k0 == 0 && s.k1 == s.q.tiles;
+                if (threadIdx.x == 0 && s.k0 == 0 && !whole) {
+                    cut.last = share_of(share_s.total, walk.at - 1 + (s.q.tiles - s.k1), share_s.shares);
+                    cut.rows = s.rows;
+                    cut.begin = s.q.begin;
+                    cut.first_row = s.unit * kUnitRows;
+                    cut.head = s.head;
+                }
+                if (*failed) sum = __int_as_float(0x7FC00000);  // NaN, not an unfinished sum
                 const bool bad = bad_s[seg & 1] != 0;
                 const int64_t o_row = token * a.q_heads + head;
                 float* state = static_cast<float*>(a.workspace) +
@@ -842,114 +863,103 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             named_barrier<256>(2);
             ++seg;
         }
+        if (threadIdx.x == 0) static_cast<Cut*>(a.workspace)[blockIdx.x] = cut;
     }
 
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    if (threadIdx.x == 0)
-        reinterpret_cast<int*>(a.workspace)[blockIdx.x] = failed_s;
     if (warp == kIssueWarp) tmem_free(tmem, 512);
 }
 
 // ------------------------------------------------------------------- the join
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 2 * (kJoinThreads / 32);  // rows a block
 
 // The cut units' rows: for a row, the states of the blocks that share its unit,
-// in block order.  A warp takes a row: its lanes read up to 32 states' pairs at
-// once, then every lane D / 32 accumulators of each state, eight states' loads in
-// flight.  Blocks of eight rows of one token, so that one token's call spreads
-// over the device.
+// in block order.  The first grid dimension is the block that started a unit, the
+// second its rows, two a warp.  For a row the lanes read up to 32 states' pairs at
+// once, then every lane D / 32 accumulators of each state, eight states' loads
+// in flight.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
 tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
     constexpr int E = D / 32;
     const ple_tree_attention_args& a = args.a;
-    __shared__ int64_t scratch[2 * (kJoinThreads / 32)];
     wait_grid_before();
+    const int c0 = blockIdx.x;
+    const int4* told = reinterpret_cast<const int4*>(static_cast<const Cut*>(a.workspace) + c0);
+    const int4 cut = __ldcg(told);
+    const int cut_head = __ldcg(&told[1].x);
+    const int c1 = cut.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y * (kJoinThreads / 32) + warp;
-    const int r = warp_request(a.cu_seqlens, a.num_requests, t, lane);
-    int64_t before, total;
-    tiles_before<kJoinThreads>(a, r, scratch, before, total);
-    const Request q = request_of(a, r);
     const int group = a.q_heads / a.kv_heads;
-    const int64_t node = t - q.begin;
-    if (node < 0 || node >= q.nodes || h >= a.q_heads) return;
     const float* space = static_cast<const float*>(a.workspace);
-    const int head = h / group;
-    const int64_t row = node * group + (h - head * group);
-    const int64_t unit = row / kUnitRows;
-    const int local = (int)(row - unit * kUnitRows);
-    const int64_t first = before + (head * (int64_t)q.units + unit) * q.tiles;
-    const int blocks = shares(total, args.blocks);
-    const int c0 = share_of(total, first, blocks);
-    const int c1 = share_of(total, first + q.tiles - 1, blocks);
-    float m = -INFINITY, sum = 0.f, acc[E] = {};
-    bool failed = false;
-    for (int from = c0; from <= c1; from += 32) {
-        const int c = from + lane;
-        const bool here = c <= c1;
-        if (here) failed |= reinterpret_cast<const int*>(space)[c] != 0;
-        if (c0 == c1) break;  // the block wrote the row
-        // the unit starts in the first of its blocks and is begun in the others
-        const int64_t mine = state_at(c, c == c0 ? 1 : 0, args.rows_cap, D);
-        float2 p = make_float2(-INFINITY, 0.f);
-        if (here) p = __ldcg(reinterpret_cast<const float2*>(space + mine) + local);
-        float now = fmaxf(m, p.x);
+    if (c1 <= c0) return;
+#pragma unroll 1
+    for (int local = blockIdx.y * kJoinRows + warp;
+         local < min(cut.y, (blockIdx.y + 1) * kJoinRows); local += kJoinThreads / 32) {
+        float m = -INFINITY, sum = 0.f, acc[E] = {};
+        for (int from = c0; from <= c1; from += 32) {
+            const int c = from + lane;
+            // the unit starts in the first of its blocks and is begun in the others
+            const int64_t mine = state_at(c, c == c0 ? 1 : 0, args.rows_cap, D);
+            float2 p = make_float2(-INFINITY, 0.f);
+            if (c <= c1) p = __ldcg(reinterpret_cast<const float2*>(space + mine) + local);
+            float now = fmaxf(m, p.x);
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-        // no maximum: nothing seen (zeros), or only NaN, which stays
-        const float keep = m == -INFINITY ? 1.f : exp2_fast(m - now);
-        const float f = p.x == -INFINITY ? 1.f : exp2_fast(p.x - now);
-        float part = p.y * f;
+            for (int d = 16; d >= 1; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+            // no maximum: nothing seen (zeros), or only NaN, which stays
+            const float keep = m == -INFINITY ? 1.f : exp2_fast(m - now);
+            const float f = p.x == -INFINITY ? 1.f : exp2_fast(p.x - now);
+            float part = p.y * f;
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-        sum = sum * keep + part;
-        m = now;
+            for (int d = 16; d >= 1; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+            sum = sum * keep + part;
+            m = now;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= keep;
-        const int n = min(32, c1 - from + 1);
-        const int64_t at = 2 * args.rows_cap +
-                           ((lane * E / 8) * (int64_t)args.rows_cap + local) * 8 + lane * E % 8;
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            float x[8][E];
+            for (int e = 0; e < E; ++e) acc[e] *= keep;
+            const int n = min(32, c1 - from + 1);
+            const int64_t at = 2 * args.rows_cap +
+                               ((lane * E / 8) * (int64_t)args.rows_cap + local) * 8 + lane * E % 8;
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float x[8][E];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t theirs = __shfl_sync(0xffffffffu, mine, i0 + i & 31);
-                if (i0 + i < n) {
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t theirs = __shfl_sync(0xffffffffu, mine, i0 + i & 31);
+                    if (i0 + i < n) {
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float2 y =
-                            __ldcg(reinterpret_cast<const float2*>(space + theirs + at + e));
-                        x[i][e] = y.x;
-                        x[i][e + 1] = y.y;
+                        for (int e = 0; e < E; e += 2) {
+                            const float2 y =
+                                __ldcg(reinterpret_cast<const float2*>(space + theirs + at + e));
+                            x[i][e] = y.x;
+                            x[i][e + 1] = y.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float g = __shfl_sync(0xffffffffu, f, i0 + i & 31);
+                    if (i0 + i < n) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[e] = fmaf(x[i][e], g, acc[e]);
                     }
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float g = __shfl_sync(0xffffffffu, f, i0 + i & 31);
-                if (i0 + i < n) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[i][e], g, acc[e]);
-                }
-            }
         }
-    }
-    failed = __any_sync(0xffffffffu, failed);
-    if (c0 == c1 && !failed) return;
-    if (failed) sum = __int_as_float(0x7FC00000);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t o = t * a.q_heads + h;
-    unsigned short* dst = static_cast<unsigned short*>(a.out) + o * D + lane * E;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int row = cut.w + local;
+        const int node = row / group;
+        const int64_t o = (cut.z + (int64_t)node) * a.q_heads + cut_head * group + row - node * group;
+        unsigned short* dst = static_cast<unsigned short*>(a.out) + o * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = round_pair<kBf16>(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0 && a.lse != nullptr)
-        a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) =
+                round_pair<kBf16>(acc[e] * inv, acc[e + 1] * inv);
+        if (lane == 0 && a.lse != nullptr)
+            a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
+    }
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1013,10 +1023,9 @@ cudaError_t launch_tc(const TcArgs& args, const CUtensorMap& k, const CUtensorMa
     e = launch_kernel(fn, dim3((unsigned)args.blocks), dim3(kThreads), Shape<D>::kSmem, stream,
                       programmatic_launch(), args, k, v);
     if (e != cudaSuccess) return e;
-    const int rows = kJoinThreads / 32;
     return launch_kernel(
         tree_attention_join_kernel<D, kBf16>,
-        dim3((unsigned)args.a.num_tokens, (unsigned)((args.a.q_heads + rows - 1) / rows)),
+        dim3((unsigned)args.blocks, (unsigned)((args.rows_cap + kJoinRows - 1) / kJoinRows)),
         dim3(kJoinThreads), 0, stream, programmatic_launch(), args);
 }
 
