@@ -13,9 +13,9 @@
 // 2^8 and the sum and O share the old maximum, so nothing is lost.
 //
 // Blocks.  One block an SM: two warps that copy key and value tiles into a ring
-// of shared memory (tiled bulk copies, page by page, 128-byte swizzle), and two
-// groups of four warps that do the softmax, one row a thread, each with a warp
-// that issues its matrix instructions.  With more than 128 rows the two groups take 128
+// of shared memory (tiled bulk copies, page by page, 128-byte swizzle), a warp
+// that issues the matrix instructions, and two groups of four warps that do the
+// softmax, one row a thread.  With more than 128 rows the two groups take 128
 // each over the same tiles, so that a key is read once for 256 rows; with fewer
 // they take the tiles in turn over the same rows and are joined in shared memory.
 // Either way one group's softmax runs while the tensor cores work for the other.
@@ -45,8 +45,8 @@ namespace {
 
 constexpr int kTile = 128;           // keys a tile, rows a matrix instruction
 constexpr int kUnitRows = 2 * kTile; // rows a unit
-constexpr int kThreads = 384;        // two groups of 128, two copying and two issuing warps
-constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10;  // and 11: the second group's issuing
+constexpr int kThreads = 352;        // two groups of 128, two copying warps, an issuing one
+constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10;
 constexpr int kMaxBlocks = 1024;     // blocks of a launch: an SM's number of them is far below
 constexpr float kLag = 8.0f;         // how far, in the exponent, a maximum may lag
 
@@ -324,11 +324,11 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
     __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_full[2], pv_done[2];
-    __shared__ __align__(8) uint64_t cleaned, last;
+    __shared__ __align__(8) uint64_t last;
     // How often a slot was armed for a tile.  A barrier tells only the parity of
-    // its phase, and neither a copying warp nor an issuing one sees every tile
-    // of a slot: who waits for the slot's round r looks here first, where r (or
-    // r + 1, armed) says that all rounds before are over.
+    // its phase, and neither copying warp sees every tile of a slot: before it
+    // waits for the end of the slot's round r - 1 it waits here for r, which says
+    // that all rounds before are over.
     __shared__ uint32_t armed_s[S::kSlots];
     __shared__ int64_t scratch[kThreads / 32];
     __shared__ Share share_s;
@@ -347,7 +347,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 2);
+            mbar_init(&empty[i], 1);
             armed_s[i] = 0;
         }
         for (int w = 0; w < 2; ++w) {
@@ -357,9 +357,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             mbar_init(&pv_done[w], 1);
             bad_s[w] = 0;
         }
-        mbar_init(&q_empty, 2);
-        mbar_init(&cleaned, 1);
-        mbar_init(&last, 2);
+        mbar_init(&q_empty, 1);
+        mbar_init(&last, 1);
         failed_s = 0;
         fence_barrier_init();
     }
@@ -445,53 +444,64 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 __syncwarp();
             }
-        } else {
+        } else if (warp == kIssueWarp) {
             // -------------------------------------------- matrix instructions
-            // one warp a group, so that neither group waits in the other's
-            // order; one lane issues (tcgen05 work of one thread stays in order:
-            // a group's next scores follow the product that reads its weights)
+            // one lane issues for both groups (tcgen05 work of one thread stays
+            // in order: a group's next scores follow the product that reads its
+            // weights).  A second issuing warp, one a group, measured slower: the
+            // two groups' instructions then interleave one by one (256 rows over
+            // 32 x 16384 slots: 515 us against 597)
             constexpr uint32_t kScoreWord = mma_word(kBf16, false, kTile, kTile);
             constexpr uint32_t kOutWord = mma_word(kBf16, true, kTile, D);
-            const int w = warp == kIssueWarp ? 0 : 1;
             const bool elected = elect_lane();
-            const uint32_t s_at = tmem + w * S::kGroupColumns, o_at = s_at + S::kOut;
-            const uint32_t ring_at = smem_addr(ring);
-            uint32_t items = 0, p_count = 0, pairs = 0, cleanings = 0, seg = 0;
+            const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(q_tiles);
+            uint32_t items = 0, p_count[2] = {0, 0}, pairs = 0, seg = 0;
+            auto wait_item = [&](uint32_t item) -> uint32_t {
+                const uint32_t slot = item % S::kSlots;
+                mbar_wait(&full[slot], item / S::kSlots & 1, failed);
+                return slot;
+            };
+            // a descriptor's address counts 16 bytes and stays below 2^14, so
+            // steps within a tile add to it
+            auto scores = [&](int w, uint32_t slot, uint32_t q_tile, bool free) {
+                const uint64_t qd = operand_desc(q_at + q_tile * S::kTileBytes, 16);
+                const uint64_t kd = operand_desc(ring_at + slot * S::kTileBytes, 16);
+                if (elected) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = ((k / 4) * S::kHalfBytes + (k % 4) * 32) >> 4;
+                        mma_smem(tmem + w * S::kGroupColumns, qd + at, kd + at, kScoreWord, k != 0);
+                    }
+                    mma_commit(&s_full[w]);
+                    if (free) mma_commit(&empty[slot]);
+                }
+                __syncwarp();
+            };
+            auto values = [&](int w, uint32_t slot, bool accumulate, bool free) {
+                const uint64_t vd = operand_desc(ring_at + slot * S::kTileBytes, S::kHalfBytes);
+                if (elected) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_tmem(tmem + w * S::kGroupColumns + S::kOut,
+                                 tmem + w * S::kGroupColumns + k * 8, vd + (k * 16 * 128 >> 4),
+                                 kOutWord, accumulate || k != 0);
+                    mma_commit(&pv_done[w]);
+                    if (free) mma_commit(&empty[slot]);
+                }
+                __syncwarp();
+            };
+            auto wait_weights = [&](int w) {
+                mbar_wait(&p_full[w], p_count[w]++ & 1, failed);
+                tmem_fence_after();
+            };
             while (walk.next(s)) {
                 const int n = s.k1 - s.k0;
-                auto wait_item = [&](uint32_t item) -> uint32_t {
-                    const uint32_t slot = item % S::kSlots, round = item / S::kSlots;
-                    count_wait(&armed[slot], round + 1, failed);
-                    mbar_wait(&full[slot], round & 1, failed);
-                    return slot;
-                };
-                // a tile is free when both groups are done with it; where the
-                // groups take tiles in turn its only user says so twice
-                auto release = [&](uint32_t slot) {
-                    mma_commit(&empty[slot]);
-                    if (!s.pair) mma_commit(&empty[slot]);
-                };
-                // a descriptor's address counts 16 bytes and stays below 2^14, so
-                // steps within a tile add to it
-                const uint64_t qd =
-                    operand_desc(smem_addr(q_tiles) + (s.pair ? w : 0) * S::kTileBytes, 16);
-                auto scores = [&](uint32_t item) {
-                    const uint32_t slot = wait_item(item);
-                    const uint64_t kd = operand_desc(ring_at + slot * S::kTileBytes, 16);
-                    if (elected) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t at = ((k / 4) * S::kHalfBytes + (k % 4) * 32) >> 4;
-                            mma_smem(s_at, qd + at, kd + at, kScoreWord, k != 0);
-                        }
-                        mma_commit(&s_full[w]);
-                        release(slot);
-                    }
-                    __syncwarp();
-                };
                 // values past the request's tokens, and drafted ones that are not
                 // finite, are cleared before the product reads them
-                auto clean = [&](int first, uint8_t* tile) {
+                auto clean = [&](int j, uint32_t slot) {
+                    const int first = (s.k0 + j) * kTile;
+                    if (first + kTile <= s.q.ctx) return;
+                    uint8_t* tile = ring + slot * S::kTileBytes;
                     const int from = max(s.q.ctx - first, 0), upto = min(s.q.length - first, kTile);
                     constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
                     bool bad = false;
@@ -527,35 +537,39 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 };
 
                 mbar_wait(&q_full[0], seg & 1, failed);
-                if (s.pair && w == 1) mbar_wait(&q_full[1], pairs & 1, failed);
-                if (s.pair) ++pairs;
+                if (s.pair) mbar_wait(&q_full[1], pairs++ & 1, failed);
                 tmem_fence_after();
-                const int from = s.pair ? 0 : w, step = s.pair ? 1 : 2;
-                if (from < n) scores(items + key_item(from));
-                for (int j = from; j < n; j += step) {
-                    mbar_wait(&p_full[w], p_count++ & 1, failed);
-                    tmem_fence_after();
-                    const uint32_t slot = wait_item(items + value_item(j, n));
-                    const int first = (s.k0 + j) * kTile;
-                    if (first + kTile > s.q.ctx) {
-                        if (!s.pair || w == 0) clean(first, ring + slot * S::kTileBytes);
-                        if (s.pair) {
-                            if (w == 0 && lane == 0) mbar_arrive(&cleaned);
-                            mbar_wait(&cleaned, cleanings++ & 1, failed);
+                if (s.pair) {
+                    uint32_t k = wait_item(items);
+                    scores(0, k, 0, false);
+                    scores(1, k, 1, true);
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        wait_weights(0);
+                        const uint32_t v = wait_item(items + value_item(j, n));
+                        if (__any_sync(0xffffffffu, *failed)) break;
+                        clean(j, v);
+                        values(0, v, j > 0, false);
+                        if (more) {
+                            k = wait_item(items + key_item(j + 1));
+                            scores(0, k, 0, false);
                         }
+                        wait_weights(1);
+                        values(1, v, j > 0, true);
+                        if (more) scores(1, k, 1, true);
                     }
-                    if (__any_sync(0xffffffffu, *failed)) break;
-                    const uint64_t vd = operand_desc(ring_at + slot * S::kTileBytes, S::kHalfBytes);
-                    if (elected) {
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_tmem(o_at, s_at + k * 8, vd + (k * 16 * 128 >> 4), kOutWord,
-                                     j != from || k != 0);
-                        mma_commit(&pv_done[w]);
-                        release(slot);
+                } else {
+                    for (int w = 0; w < min(2, n); ++w)
+                        scores(w, wait_item(items + key_item(w)), 0, true);
+                    for (int j = 0; j < n; ++j) {
+                        const int w = j & 1;
+                        wait_weights(w);
+                        const uint32_t v = wait_item(items + value_item(j, n));
+                        if (__any_sync(0xffffffffu, *failed)) break;
+                        clean(j, v);
+                        values(w, v, j > 1, true);
+                        if (j + 2 < n) scores(w, wait_item(items + key_item(j + 2)), 0, true);
                     }
-                    __syncwarp();
-                    if (j + step < n) scores(items + key_item(j + step));
                 }
                 if (elected) mma_commit(&q_empty);
                 __syncwarp();
@@ -874,18 +888,19 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
 
 // ------------------------------------------------------------------- the join
 
-constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 2 * (kJoinThreads / 32);  // rows a block
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = kJoinThreads / 16;  // rows a block
 
 // The cut units' rows: for a row, the states of the blocks that share its unit,
 // in block order.  The first grid dimension is the block that started a unit, the
-// second its rows, two a warp.  For a row the lanes read up to 32 states' pairs at
-// once, then every lane D / 32 accumulators of each state, eight states' loads
-// in flight.
+// second its rows.  Sixteen lanes take a row: they read up to 16 states' pairs at
+// once, then every lane D / 16 accumulators of each state, four states' loads
+// in flight (a unit is mostly cut into two or three).  The work is a few bytes
+// a row behind three dependent reads, so it is spread thin and wide.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 8)
 tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
-    constexpr int E = D / 32;
+    constexpr int E = D / 16;
     const ple_tree_attention_args& a = args.a;
     wait_grid_before();
     const int c0 = blockIdx.x;
@@ -893,73 +908,79 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
     const int4 cut = __ldcg(told);
     const int cut_head = __ldcg(&told[1].x);
     const int c1 = cut.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = a.q_heads / a.kv_heads;
+    const int local = blockIdx.y * kJoinRows + threadIdx.x / 16;
+    const int lane = threadIdx.x & 15;
+    if (c1 <= c0 || local - (threadIdx.x & 31) / 16 >= cut.y) return;
+    const bool live = local < cut.y;  // the warp's other row may be there alone
     const float* space = static_cast<const float*>(a.workspace);
-    if (c1 <= c0) return;
-#pragma unroll 1
-    for (int local = blockIdx.y * kJoinRows + warp;
-         local < min(cut.y, (blockIdx.y + 1) * kJoinRows); local += kJoinThreads / 32) {
-        float m = -INFINITY, sum = 0.f, acc[E] = {};
-        for (int from = c0; from <= c1; from += 32) {
-            const int c = from + lane;
-            // the unit starts in the first of its blocks and is begun in the others
-            const int64_t mine = state_at(c, c == c0 ? 1 : 0, args.rows_cap, D);
-            float2 p = make_float2(-INFINITY, 0.f);
-            if (c <= c1) p = __ldcg(reinterpret_cast<const float2*>(space + mine) + local);
-            float now = fmaxf(m, p.x);
+    float m = -INFINITY, sum = 0.f, acc[E] = {};
+    for (int from = c0; from <= c1; from += 16) {
+        const int c = from + lane;
+        // the unit starts in the first of its blocks and is begun in the others
+        const int64_t mine = state_at(c, c == c0 ? 1 : 0, args.rows_cap, D);
+        float2 p = make_float2(-INFINITY, 0.f);
+        if (c <= c1 && live) p = __ldcg(reinterpret_cast<const float2*>(space + mine) + local);
+        float now = fmaxf(m, p.x);
 #pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-            // no maximum: nothing seen (zeros), or only NaN, which stays
-            const float keep = m == -INFINITY ? 1.f : exp2_fast(m - now);
-            const float f = p.x == -INFINITY ? 1.f : exp2_fast(p.x - now);
-            float part = p.y * f;
+        for (int d = 8; d >= 1; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+        // no maximum: nothing seen (zeros), or only NaN, which stays
+        const float keep = m == -INFINITY ? 1.f : exp2_fast(m - now);
+        const float f = p.x == -INFINITY ? 1.f : exp2_fast(p.x - now);
+        float part = p.y * f;
 #pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-            sum = sum * keep + part;
-            m = now;
+        for (int d = 8; d >= 1; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+        sum = sum * keep + part;
+        m = now;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= keep;
-            const int n = min(32, c1 - from + 1);
-            const int64_t at = 2 * args.rows_cap +
-                               ((lane * E / 8) * (int64_t)args.rows_cap + local) * 8 + lane * E % 8;
-            for (int i0 = 0; i0 < n; i0 += 8) {
-                float x[8][E];
+        for (int e = 0; e < E; ++e) acc[e] *= keep;
+        const int n = min(16, c1 - from + 1);
+        const int at = 2 * args.rows_cap + ((lane * E / 8) * args.rows_cap + local) * 8 + lane * E % 8;
+        for (int i0 = 0; i0 < n; i0 += 4) {
+            float4 x[4][E / 4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t theirs = __shfl_sync(0xffffffffu, mine, i0 + i & 31);
-                    if (i0 + i < n) {
+            for (int i = 0; i < 4; ++i) {
+                if (i0 + i < n && live) {
+                    const float* theirs =
+                        space + at +
+                        state_at(from + i0 + i, from + i0 + i == c0 ? 1 : 0, args.rows_cap, D);
 #pragma unroll
-                        for (int e = 0; e < E; e += 2) {
-                            const float2 y =
-                                __ldcg(reinterpret_cast<const float2*>(space + theirs + at + e));
-                            x[i][e] = y.x;
-                            x[i][e + 1] = y.y;
-                        }
-                    }
+                    for (int e = 0; e < E / 4; ++e)
+                        x[i][e] = __ldcg(reinterpret_cast<const float4*>(theirs) + e);
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float g = __shfl_sync(0xffffffffu, f, i0 + i & 31);
-                    if (i0 + i < n) {
+            for (int i = 0; i < 4; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, (i0 + i) & 15, 16);
+                if (i0 + i < n && live) {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) acc[e] = fmaf(x[i][e], g, acc[e]);
+                    for (int e = 0; e < E / 4; ++e) {
+                        acc[4 * e] = fmaf(x[i][e].x, g, acc[4 * e]);
+                        acc[4 * e + 1] = fmaf(x[i][e].y, g, acc[4 * e + 1]);
+                        acc[4 * e + 2] = fmaf(x[i][e].z, g, acc[4 * e + 2]);
+                        acc[4 * e + 3] = fmaf(x[i][e].w, g, acc[4 * e + 3]);
                     }
                 }
             }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int row = cut.w + local;
-        const int node = row / group;
-        const int64_t o = (cut.z + (int64_t)node) * a.q_heads + cut_head * group + row - node * group;
-        unsigned short* dst = static_cast<unsigned short*>(a.out) + o * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t*>(dst + e) =
-                round_pair<kBf16>(acc[e] * inv, acc[e + 1] * inv);
-        if (lane == 0 && a.lse != nullptr)
-            a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
     }
+    if (!live) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const uint32_t group = a.q_heads / a.kv_heads;
+    const uint32_t row = cut.w + local;
+    const uint32_t node = row / group;
+    const int64_t o = (cut.z + (int64_t)node) * a.q_heads + cut_head * group + row - node * group;
+    uint32_t y[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e)
+        y[e] = round_pair<kBf16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned short*>(a.out) + o * D) +
+                    lane * (E / 2);
+    if constexpr (E == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+    else
+        *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    if (lane == 0 && a.lse != nullptr)
+        a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
