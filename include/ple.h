@@ -478,7 +478,7 @@ ple_status ple_build_tree_index(const int32_t* parent, const int32_t* cu_seqlens
  * id of the node's s-th ancestor, and behind the branch's root the carried
  * context, newest id first.  A tree that is a chain gives the row ids of the
  * same tokens as a prefill.  Arguments, arithmetic and checks as
- * ple_row_ids_ex; parent and cu_seqlens as above.
+ * ple_row_ids_ex, with at most 65535 layers; parent and cu_seqlens as above.
  *
  * Errors: as ple_row_ids_ex.  One kernel launch.
  */

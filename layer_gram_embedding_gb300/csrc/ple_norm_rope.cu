@@ -55,92 +55,139 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <typename E>
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<E>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-
-template <typename E>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack2<E>(x[0], x[1]), pack2<E>(x[2], x[3]), pack2<E>(x[4], x[5]),
-                      pack2<E>(x[6], x[7]));
-}
-
 // How a pair's two elements lie: side by side, half the rotary part apart with
 // both in whole lanes (R / 2 a multiple of 8), or half of it apart anyhow.
 enum PairLayout { kPairsInterleaved = 0, kPairsHalves = 1, kPairsAnyHalves = 2 };
 
-// Pair p's (cos, sin) is float2 number (2 * ((p % 8) / 2) + ...) of four planes:
-// plane k holds, for every chunk of eight pairs, pairs 2k and 2k + 1, so that
-// the lanes of a row read consecutive 16-byte words.
-__device__ __forceinline__ int pair_slot(int p, int chunks) {
-    return (((p & 7) >> 1) * chunks + (p >> 3)) * 2 + (p & 1);
+// The table of a token's angles.  Pairs 2m and 2m + 1 make one 16-byte word
+// (cos, cos, sin, sin), ready for paired arithmetic; word m of a chunk of eight
+// pairs lies in plane m % 4, so that the lanes of a row read consecutive words.
+__device__ __forceinline__ int turn_word(int pair, int chunks) {
+    return ((pair & 7) >> 1) * chunks + (pair >> 3);
 }
 
+// Two 32-bit floats to a register pair: one instruction for both on sm_103a.
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair make_pair(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(Pair a, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma_pair(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+template <typename E>
+__device__ __forceinline__ void unpack_row(uint4 v, Pair (&x)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<E>(w[i]);
+        x[i] = make_pair(f.x, f.y);
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ uint4 pack_row(const Pair (&x)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        split(x[i], lo, hi);
+        w[i] = pack2<E>(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// How the block's warps meet the rows: `abreast` tokens at a time with
+// 8 / abreast warps each, a warp taking every (8 / abreast)-th group of rows.
+struct RowPlan {
+    int32_t tokens;   // of a block, at most kNormTokens
+    int32_t abreast;
+    int32_t groups;   // of 32 / lanes-a-row rows, of a token
+};
+
 template <typename E, int LPR, int kLayout>
-__global__ void __launch_bounds__(kNormThreads)
-qk_norm_rope_kernel(const ple_qk_norm_rope_args a, const int tokens) {
-    constexpr int RPW = 32 / LPR;                      // rows a warp
-    constexpr int RPB = RPW * (kNormThreads / 32);     // rows a block and step
-    constexpr int U = 3;                               // steps whose loads are in flight
-    __shared__ __align__(16) float2 turn[kNormTokens][kMaxPairs + 8];
+__global__ void __launch_bounds__(kNormThreads, 4)
+qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPlan plan) {
+    constexpr int RPW = 32 / LPR;     // rows a warp
+    constexpr int kWarps = kNormThreads / 32;
+    constexpr int U = 3;              // rows whose loads are in flight, a lane
+    // cosines with sines, and with negated sines for the first half's elements
+    __shared__ __align__(16) float4 turn[2][kNormTokens][kMaxPairs / 2];
     __shared__ int64_t dst_s[kNormTokens];
     __shared__ float row_s[kLayout == kPairsAnyHalves ? kNormThreads * 8 : 1];
 
     wait_grid_before();
-    const int64_t t0 = (int64_t)blockIdx.x * tokens;
-    const int nt = (int)min((int64_t)tokens, a.num_tokens - t0);
+    const int64_t t0 = (int64_t)blockIdx.x * plan.tokens;
+    const int nt = (int)min((int64_t)plan.tokens, a.num_tokens - t0);
     const bool cached = a.k_cache != nullptr;
-    const int heads = a.q_heads + a.kv_heads * (cached ? 2 : 1);
-    const int rows = nt * heads;
+    const int qk_heads = a.q_heads + a.kv_heads;
+    const int heads = qk_heads + (cached ? a.kv_heads : 0);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
-    const int D = a.head_dim;
-    const bool live = sub * 8 < D;
-    const int R = a.rotary_dim;
-    const int pairs = R >> 1;
+    const int in_group = lane / LPR;
+    const bool live = sub * 8 < a.head_dim;
+    const int pairs = a.rotary_dim >> 1;
     const int chunks = (pairs + 7) >> 3;
+    const int per_token = kWarps / plan.abreast;   // warps of a token
+    const int group0 = warp % per_token;
 
+    // a row's elements of this lane; q, k and v rows follow one another
+    auto load = [&](int tok, int group) -> uint4 {
+        const int head = group * RPW + in_group;
+        if (head >= heads || !live) return make_uint4(0, 0, 0, 0);
+        const bool is_q = head < a.q_heads, is_k = head < qk_heads;
+        const unsigned short* base =
+            static_cast<const unsigned short*>(is_q ? a.q : is_k ? a.k : a.v);
+        const int64_t at = (t0 + tok) * (is_q ? a.q_token : is_k ? a.k_token : a.v_token) +
+                           (head - (is_q ? 0 : is_k ? a.q_heads : qk_heads)) *
+                               (is_q ? a.q_head : is_k ? a.k_head : a.v_head);
+        return __ldcs(reinterpret_cast<const uint4*>(base + at) + sub);
+    };
     // the rows' loads first: they are in flight while the angles are computed
-    auto source = [&](int row, int& tok, int& head) -> const uint4* {
-        tok = row / heads;
-        head = row - tok * heads;
-        const int64_t t = t0 + tok;
-        const unsigned short* base;
-        int64_t at;
-        if (head < a.q_heads) {
-            base = static_cast<const unsigned short*>(a.q);
-            at = t * a.q_token + head * a.q_head;
-        } else if (head < a.q_heads + a.kv_heads) {
-            base = static_cast<const unsigned short*>(a.k);
-            at = t * a.k_token + (head - a.q_heads) * a.k_head;
-        } else {
-            base = static_cast<const unsigned short*>(a.v);
-            at = t * a.v_token + (head - a.q_heads - a.kv_heads) * a.v_head;
+    int ltok = warp / per_token, lgroup = group0;
+    auto next = [&](int& tok, int& group) {
+        group += per_token;
+        if (group >= plan.groups) {
+            group = group0;
+            tok += plan.abreast;
         }
-        return reinterpret_cast<const uint4*>(base + at) + sub;
     };
-    const int row0 = warp * RPW + lane / LPR;
+    int tok = ltok, group = lgroup;
     uint4 raw[U];
-    int tok[U], head[U];
-    auto fetch = [&](int first) {
+    const bool any = group0 < plan.groups;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int row = first + u * RPB;
-            if (row < rows && live) raw[u] = *source(row, tok[u], head[u]);
+    for (int u = 0; u < U; ++u) {
+        if (any && ltok < nt) raw[u] = load(ltok, lgroup);
+        next(ltok, lgroup);
+    }
+    Pair qw[4], kw[4];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const uint4* from = static_cast<const uint4*>(side == 0 ? a.q_weight : a.k_weight);
+        Pair(&w)[4] = side == 0 ? qw : kw;
+        if (from != nullptr && live) {
+            unpack_row<E>(__ldg(from + sub), w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = make_pair(1.f, 1.f);
         }
-    };
-    fetch(row0);
-    uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
-    if (a.q_weight != nullptr && live) qw = __ldg(static_cast<const uint4*>(a.q_weight) + sub);
-    if (a.k_weight != nullptr && live) kw = __ldg(static_cast<const uint4*>(a.k_weight) + sub);
+    }
+    const bool norms = a.q_weight != nullptr || a.k_weight != nullptr;
 
     for (int i = threadIdx.x; i < nt * pairs; i += kNormThreads) {
         const int k = i / pairs;
@@ -151,10 +198,15 @@ qk_norm_rope_kernel(const ple_qk_norm_rope_args a, const int tokens) {
         const float half_turns = (float)(int32_t)(uint32_t)(phase >> 32) * 0x1p-31f;
         float sn, cs;
         sincospif(half_turns, &sn, &cs);
-        turn[k][pair_slot(p, chunks)] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            float* word = reinterpret_cast<float*>(&turn[side][k][turn_word(p, chunks)]);
+            word[p & 1] = cs * a.rope_scale;
+            word[2 + (p & 1)] = side == 0 ? sn * a.rope_scale : -sn * a.rope_scale;
+        }
     }
     if (cached) {
-        for (int k = warp; k < nt; k += kNormThreads / 32) {
+        for (int k = warp; k < nt; k += kWarps) {
             const int r = warp_request(a.cu_seqlens, a.num_requests, t0 + k, lane);
             if (lane == 0) {
                 const int64_t place = t0 + k - max(__ldg(a.cu_seqlens + r), 0);
@@ -166,100 +218,115 @@ qk_norm_rope_kernel(const ple_qk_norm_rope_args a, const int tokens) {
         }
     }
     __syncthreads();
+    if (!any) return;
 
-    const float inv_d = 1.0f / (float)D;
-    for (int first = row0; first - lane / LPR < rows; first += U * RPB) {
-        if (first != row0) fetch(first);
+    const float inv_d = 1.0f / (float)a.head_dim;
+    while (tok < nt) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int row = first + u * RPB;
-            // a warp's rows go on together: its shuffles need every lane
-            if (row - lane / LPR >= rows) break;
-            const bool here = row < rows && live;
-            const bool is_q = here && head[u] < a.q_heads;
-            const bool is_v = here && head[u] >= a.q_heads + a.kv_heads;
-            float x[8];
+            if (tok >= nt) break;  // a warp's rows go on together
+            const int head = group * RPW + in_group;
+            const uint4 mine = raw[u];
+            if (ltok < nt) raw[u] = load(ltok, lgroup);
+            next(ltok, lgroup);
+            const bool here = head < heads && live;
+            const bool is_q = head < a.q_heads;
+            uint4 y = mine;
+            if (group * RPW < qk_heads) {  // else value rows alone
+                Pair x[4];
+                unpack_row<E>(mine, x);
+                if (norms) {
+                    Pair sq = x[0] * x[0];
+#pragma unroll
+                    for (int i = 1; i < 4; ++i) sq = fma_pair(x[i], x[i], sq);
+                    float lo, hi;
+                    split(sq, lo, hi);
+                    lo += hi;
+#pragma unroll
+                    for (int m = LPR / 2; m >= 1; m >>= 1)
+                        lo += __shfl_xor_sync(0xffffffffu, lo, m);
+                    // rows with a norm and rows without may share a warp
+                    const bool norm = (is_q ? a.q_weight : a.k_weight) != nullptr;
+                    const float inv = norm ? rsqrtf(fmaf(lo, inv_d, a.eps)) : 1.f;
+                    const Pair inv2 = make_pair(inv, inv);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = x[i] * (inv2 * (is_q ? qw[i] : kw[i]));
+                }
+                if constexpr (kLayout == kPairsInterleaved) {
+                    const float4* word = turn[0][tok];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = sub * 4 + i;
+                        if (p < pairs) {
+                            const float* w = reinterpret_cast<const float*>(
+                                &word[turn_word(p, chunks)]);
+                            const float c = w[p & 1], sn = w[2 + (p & 1)];
+                            float y0, y1;
+                            split(x[i], y0, y1);
+                            x[i] = make_pair(fmaf(y0, c, -y1 * sn), fmaf(y1, c, y0 * sn));
+                        }
+                    }
+                } else if constexpr (kLayout == kPairsHalves) {
+                    const int per = pairs >> 3;  // lanes of half the rotary part
+                    const bool low = sub < per;
+                    const int mate = low ? lane + per : sub < 2 * per ? lane - per : lane;
+                    const float4* word = &turn[low ? 1 : 0][tok][low ? sub : sub - per];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float lo, hi;
+                        split(x[i], lo, hi);
+                        const Pair o = make_pair(__shfl_sync(0xffffffffu, lo, mate),
+                                                 __shfl_sync(0xffffffffu, hi, mate));
+                        if (sub < 2 * per) {
+                            const float4 w = word[i * chunks];
+                            x[i] = fma_pair(x[i], make_pair(w.x, w.y), o * make_pair(w.z, w.w));
+                        }
+                    }
+                } else {
+                    float* row = row_s + (threadIdx.x - sub) * 8;
+                    float z[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        split(x[i], z[2 * i], z[2 * i + 1]);
+                        row[sub * 8 + 2 * i] = z[2 * i];
+                        row[sub * 8 + 2 * i + 1] = z[2 * i + 1];
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int e = sub * 8 + i;
+                        if (e < 2 * pairs) {
+                            const int p = e < pairs ? e : e - pairs;
+                            const float* w = reinterpret_cast<const float*>(
+                                &turn[e < pairs ? 1 : 0][tok][turn_word(p, chunks)]);
+                            z[i] = fmaf(z[i], w[p & 1],
+                                        row[e < pairs ? e + pairs : p] * w[2 + (p & 1)]);
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = make_pair(z[2 * i], z[2 * i + 1]);
+                }
+                if (head < qk_heads) y = pack_row<E>(x);
+            }
             if (here) {
-                unpack8<E>(raw[u], x);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.f;
-            }
-            float sq = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-#pragma unroll
-            for (int m = LPR / 2; m >= 1; m >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-            if ((is_q ? a.q_weight : a.k_weight) != nullptr) {
-                const float inv = rsqrtf(fmaf(sq, inv_d, a.eps));
-                float w[8];
-                unpack8<E>(is_q ? qw : kw, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
-            }
-            const float2* cs = turn[here ? tok[u] : 0];
-            if constexpr (kLayout == kPairsInterleaved) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = sub * 4 + i;
-                    if (p < pairs) {
-                        const float2 c = cs[pair_slot(p, chunks)];
-                        const float y0 = x[2 * i], y1 = x[2 * i + 1];
-                        x[2 * i] = fmaf(y0, c.x, -y1 * c.y);
-                        x[2 * i + 1] = fmaf(y1, c.x, y0 * c.y);
-                    }
+                const int64_t slot = cached ? dst_s[tok] : 0;
+                unsigned short* dst;
+                int64_t at;
+                if (is_q) {
+                    dst = static_cast<unsigned short*>(a.q_out);
+                    at = (t0 + tok) * a.q_out_token + head * a.q_out_head;
+                } else if (cached) {
+                    const bool is_k = head < qk_heads;
+                    dst = static_cast<unsigned short*>(is_k ? a.k_cache : a.v_cache);
+                    at = slot + (head - (is_k ? a.q_heads : qk_heads)) * a.head_stride;
+                } else {
+                    dst = static_cast<unsigned short*>(a.k_out);
+                    at = (t0 + tok) * a.k_out_token + (head - a.q_heads) * a.k_out_head;
                 }
-            } else if constexpr (kLayout == kPairsHalves) {
-                const int per = pairs >> 3;  // lanes of half the rotary part
-                const int mate = sub < per ? lane + per : sub < 2 * per ? lane - per : lane;
-                const int chunk = sub < per ? sub : sub - per;
-                const float sign = sub < per ? -1.f : 1.f;
-                const float4* plane = reinterpret_cast<const float4*>(cs);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float o0 = __shfl_sync(0xffffffffu, x[2 * i], mate);
-                    const float o1 = __shfl_sync(0xffffffffu, x[2 * i + 1], mate);
-                    if (sub < 2 * per) {
-                        const float4 c = plane[i * chunks + chunk];
-                        x[2 * i] = fmaf(x[2 * i], c.x, sign * o0 * c.y);
-                        x[2 * i + 1] = fmaf(x[2 * i + 1], c.z, sign * o1 * c.w);
-                    }
-                }
-            } else {
-                float* mine = row_s + (threadIdx.x - sub) * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mine[sub * 8 + i] = x[i];
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int e = sub * 8 + i;
-                    if (e < R) {
-                        const int p = e < pairs ? e : e - pairs;
-                        const float2 c = cs[pair_slot(p, chunks)];
-                        const float o = mine[e < pairs ? e + pairs : p];
-                        x[i] = fmaf(x[i], c.x, (e < pairs ? -o : o) * c.y);
-                    }
-                }
-                __syncwarp();
+                if (is_q || slot >= 0) reinterpret_cast<uint4*>(dst + at)[sub] = y;
             }
-            if (!here) continue;
-            const uint4 y = is_v ? raw[u] : pack8<E>(x);
-            unsigned short* dst;
-            if (is_q) {
-                dst = static_cast<unsigned short*>(a.q_out) + (t0 + tok[u]) * a.q_out_token +
-                      head[u] * a.q_out_head;
-            } else if (cached) {
-                const int64_t at = dst_s[tok[u]];
-                if (at < 0) continue;
-                dst = is_v ? static_cast<unsigned short*>(a.v_cache) + at +
-                                 (head[u] - a.q_heads - a.kv_heads) * a.head_stride
-                           : static_cast<unsigned short*>(a.k_cache) + at +
-                                 (head[u] - a.q_heads) * a.head_stride;
-            } else {
-                dst = static_cast<unsigned short*>(a.k_out) + (t0 + tok[u]) * a.k_out_token +
-                      (head[u] - a.q_heads) * a.k_out_head;
-            }
-            reinterpret_cast<uint4*>(dst)[sub] = y;
+            next(tok, group);
         }
     }
 }
@@ -288,16 +355,33 @@ __global__ void prepare_rope_kernel(int R, double base, int scaling, double fact
 template <typename E, int LPR>
 cudaError_t launch_rows(const ple_qk_norm_rope_args& a, const DeviceFacts& dev,
                         cudaStream_t stream) {
+    constexpr int RPW = 32 / LPR;
+    constexpr int kWarps = kNormThreads / 32;
+    RowPlan plan;
     // one token a block until that makes as many blocks as the device holds
     // at once, then up to four
-    int tokens = (int)(a.num_tokens / (8 * (int64_t)dev.sm_count));
-    tokens = tokens < 1 ? 1 : tokens > kNormTokens ? kNormTokens : tokens;
-    const dim3 grid((unsigned)((a.num_tokens + tokens - 1) / tokens));
+    const int64_t tokens = a.num_tokens / (4 * (int64_t)dev.sm_count);
+    plan.tokens = (int)(tokens < 1 ? 1 : tokens > kNormTokens ? kNormTokens : tokens);
+    const int heads = a.q_heads + a.kv_heads * (a.k_cache != nullptr ? 2 : 1);
+    plan.groups = (heads + RPW - 1) / RPW;
+    // as few warps a token as leave none idle in its last step, but all of them
+    // on a block's only token
+    plan.abreast = 1;
+    int best = 0;
+    for (int abreast = 1; abreast <= plan.tokens && abreast <= kWarps; abreast *= 2) {
+        const int per = kWarps / abreast;
+        const int used = plan.groups * 1000 / ((plan.groups + per - 1) / per * per);
+        if (used > best) {
+            best = used;
+            plan.abreast = abreast;
+        }
+    }
+    const dim3 grid((unsigned)((a.num_tokens + plan.tokens - 1) / plan.tokens));
     auto* fn = a.interleaved           ? qk_norm_rope_kernel<E, LPR, kPairsInterleaved>
                : a.rotary_dim % 16 == 0 ? qk_norm_rope_kernel<E, LPR, kPairsHalves>
                                         : qk_norm_rope_kernel<E, LPR, kPairsAnyHalves>;
     return launch_kernel(fn, grid, dim3(kNormThreads), 0, stream, programmatic_launch(), a,
-                         tokens);
+                         plan);
 }
 
 template <typename E>

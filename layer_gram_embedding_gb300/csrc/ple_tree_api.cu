@@ -78,7 +78,7 @@ extern "C" ple_status ple_tree_row_ids(const void* input_ids, int32_t id_dtype,
     if (ctx_len != ngram_size - 1) return PLE_ERR_GEOMETRY_CTX;
     if ((int64_t)num_heads != (int64_t)(ngram_size - 1) * heads_per_ngram)
         return PLE_ERR_GEOMETRY_HEADS;
-    if (num_heads > PLE_MAX_HEADS) return PLE_ERR_SIZE;
+    if (num_heads > PLE_MAX_HEADS || num_layers > 65535) return PLE_ERR_SIZE;
     if ((int64_t)num_layers * num_tokens > (INT64_MAX / 8) / num_heads) return PLE_ERR_SIZE;
     if (out_dtype != PLE_I32 && out_dtype != PLE_I64) return PLE_ERR_DTYPE;
     if (num_tokens == 0) return PLE_OK;

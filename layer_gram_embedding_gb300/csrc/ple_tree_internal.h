@@ -19,7 +19,7 @@ cudaError_t launch_tree_index(const int32_t* parent, const int32_t* cu, const in
 
 // The tree's row ids: the row-id parameters (cu set, req and local unused)
 // and each node's parent.
-cudaError_t launch_tree_row_ids(const RowIdsParams& p, const int32_t* parent, int id_bytes,
+cudaError_t launch_tree_row_ids(RowIdsParams p, const int32_t* parent, int id_bytes,
                                 const DeviceFacts& dev, cudaStream_t stream);
 
 cudaError_t launch_prepare_rope(int32_t rotary_dim, double base, int32_t scaling, double factor,

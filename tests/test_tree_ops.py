@@ -291,6 +291,22 @@ def test_rotation_without_cache_or_norm_in_place(dtype):
     check_rows(k, *want[1], U[dtype], "k")
 
 
+@pytest.mark.parametrize("D,Hq,Hk", [(64, 3, 2), (128, 1, 4), (96, 2, 1)])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_norm_of_queries_or_keys_alone(which, D, Hq, Hk):
+    rng = np.random.default_rng(D)
+    q, k = rows(rng, (9, Hq, D), torch.bfloat16, 2.0), rows(rng, (9, Hk, D), torch.bfloat16, 2.0)
+    w = rows(rng, (D,), torch.bfloat16)
+    positions = rng.integers(0, 5000, 9).astype(np.int32)
+    freq = ref.inverse_frequencies(D, 10000.0)
+    a, b = ple.ple_qk_norm_rope(q, k, None, dev(positions), ple.ple_prepare_rope(D),
+                                w if which == "q" else None, w if which == "k" else None)
+    for got, x, name in ((a, q, "q"), (b, k, "k")):
+        want, size = ref.norm_rope(host(x), host(w) if name == which else None, positions, freq,
+                                   1e-6, False, 1.0)
+        check_rows(got, want, size, U[torch.bfloat16], name)
+
+
 def test_norm_of_extreme_rows():
     # zeros stay zeros (eps), an infinity makes its row NaN and no other's
     q = torch.ones((4, 2, 64), dtype=torch.bfloat16, device=DEV)
