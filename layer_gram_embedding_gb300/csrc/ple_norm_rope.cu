@@ -14,14 +14,15 @@
 // where m * w_i in 32 bits loses 2^-24 of the whole angle (0.008 radians at
 // position 131072).
 //
-// Layout.  Eight elements (16 bytes) a lane and D / 8 lanes a row, rounded up to
-// a power of two, so a warp holds one to four rows and a row's sum of squares
-// is a few shuffles.  A pair's other half is in the same lane (interleaved), or
-// R / 16 lanes away (halves).  A block takes up to four tokens: their
-// sines and cosines are computed once, one pair a thread, and shared by all
-// their heads.
+// Layout.  Eight elements a lane and D / 8 lanes a row, rounded up to a power of
+// two, so a warp holds one to four rows and a row's sum of squares is a few
+// shuffles.  A lane holds both elements of its pairs: eight in a row where pairs lie
+// side by side, else four and the four half the rotary part behind them.  A block takes up to eight tokens: their
+// sines and cosines are computed once and shared by all their heads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "ple_tree_common.cuh"
 
@@ -29,7 +30,13 @@ namespace ple {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormTokens = 4;    // tokens a block, for batches that fill the device
+// Tokens a block, for batches that fill the device; resident blocks an SM.  What
+// hides the memory's latency is warps, not rows in flight in one of them: on the
+// 32004-token prompts 149 us with six blocks (40 registers a thread) and one row
+// ahead, 162 with four blocks and two or four rows ahead, 193 with seven blocks
+// (spills); four tokens a block 148, sixteen 173.
+constexpr int kNormTokens = 8;
+constexpr int kNormBlocks = 6;
 constexpr int kMaxPairs = PLE_MAX_HEAD_DIM / 2;
 
 template <typename E>
@@ -56,15 +63,11 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 }
 
 // How a pair's two elements lie: side by side, half the rotary part apart with
-// both in whole lanes (R / 2 a multiple of 8), or half of it apart anyhow.
+// R a multiple of 8, or half of it apart anyhow.
 enum PairLayout { kPairsInterleaved = 0, kPairsHalves = 1, kPairsAnyHalves = 2 };
 
-// The table of a token's angles.  Pairs 2m and 2m + 1 make one 16-byte word
-// (cos, cos, sin, sin), ready for paired arithmetic; word m of a chunk of eight
-// pairs lies in plane m % 4, so that the lanes of a row read consecutive words.
-__device__ __forceinline__ int turn_word(int pair, int chunks) {
-    return ((pair & 7) >> 1) * chunks + (pair >> 3);
-}
+// The table of a token's angles: pairs 2m and 2m + 1 make 16-byte word m, (cos, cos,
+// sin, sin), ready for paired arithmetic.
 
 // Two 32-bit floats to a register pair: one instruction for both on sm_103a.
 struct Pair {
@@ -89,9 +92,24 @@ __device__ __forceinline__ Pair fma_pair(Pair a, Pair b, Pair c) {
     return r;
 }
 
+// A lane's eight elements, as two pieces of four.
+struct Row {
+    uint2 a, b;
+};
+__device__ __forceinline__ Row load_row(const unsigned short* p, int second) {
+    Row r;
+    r.a = __ldcs(reinterpret_cast<const uint2*>(p));
+    r.b = __ldcs(reinterpret_cast<const uint2*>(p + second));
+    return r;
+}
+__device__ __forceinline__ void store_row(unsigned short* p, int second, Row r) {
+    *reinterpret_cast<uint2*>(p) = r.a;
+    *reinterpret_cast<uint2*>(p + second) = r.b;
+}
+
 template <typename E>
-__device__ __forceinline__ void unpack_row(uint4 v, Pair (&x)[4]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack_row(Row v, Pair (&x)[4]) {
+    const uint32_t w[4] = {v.a.x, v.a.y, v.b.x, v.b.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = unpack2<E>(w[i]);
@@ -100,7 +118,7 @@ __device__ __forceinline__ void unpack_row(uint4 v, Pair (&x)[4]) {
 }
 
 template <typename E>
-__device__ __forceinline__ uint4 pack_row(const Pair (&x)[4]) {
+__device__ __forceinline__ Row pack_row(const Pair (&x)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -108,25 +126,24 @@ __device__ __forceinline__ uint4 pack_row(const Pair (&x)[4]) {
         split(x[i], lo, hi);
         w[i] = pack2<E>(lo, hi);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return Row{make_uint2(w[0], w[1]), make_uint2(w[2], w[3])};
 }
 
-// How the block's warps meet the rows: `abreast` tokens at a time with
-// 8 / abreast warps each, a warp taking every (8 / abreast)-th group of rows.
+// A token's rows come in groups of as many as a warp holds, all of one kind:
+// queries, then keys, then values.  A warp takes one group after another, each for
+// all tokens of the block, so that a group's addresses are set up once and only
+// step from token to token.
 struct RowPlan {
     int32_t tokens;   // of a block, at most kNormTokens
-    int32_t abreast;
-    int32_t groups;   // of 32 / lanes-a-row rows, of a token
+    int32_t q_groups, kv_groups;
 };
 
 template <typename E, int LPR, int kLayout>
-__global__ void __launch_bounds__(kNormThreads, 4)
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks)
 qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPlan plan) {
     constexpr int RPW = 32 / LPR;     // rows a warp
     constexpr int kWarps = kNormThreads / 32;
-    constexpr int U = 3;              // rows whose loads are in flight, a lane
-    // cosines with sines, and with negated sines for the first half's elements
-    __shared__ __align__(16) float4 turn[2][kNormTokens][kMaxPairs / 2];
+    __shared__ __align__(16) float4 turn[kNormTokens][kMaxPairs / 2];
     __shared__ int64_t dst_s[kNormTokens];
     __shared__ float row_s[kLayout == kPairsAnyHalves ? kNormThreads * 8 : 1];
 
@@ -134,60 +151,39 @@ qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPl
     const int64_t t0 = (int64_t)blockIdx.x * plan.tokens;
     const int nt = (int)min((int64_t)plan.tokens, a.num_tokens - t0);
     const bool cached = a.k_cache != nullptr;
-    const int qk_heads = a.q_heads + a.kv_heads;
-    const int heads = qk_heads + (cached ? a.kv_heads : 0);
+    const int k_end = plan.q_groups + plan.kv_groups;
+    const int groups = k_end + (cached ? plan.kv_groups : 0);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
     const int in_group = lane / LPR;
     const bool live = sub * 8 < a.head_dim;
     const int pairs = a.rotary_dim >> 1;
-    const int chunks = (pairs + 7) >> 3;
-    const int per_token = kWarps / plan.abreast;   // warps of a token
-    const int group0 = warp % per_token;
+    // A lane's eight elements: four and the four that they turn with (halves),
+    // or eight in a row (side by side, and what is not turned).
+    const bool turns = kLayout == kPairsHalves ? sub * 8 < a.rotary_dim : true;
+    const int first = kLayout == kPairsHalves && turns ? sub * 4 : sub * 8;
+    const int second = kLayout == kPairsHalves && turns ? pairs : 4;
 
-    // a row's elements of this lane; q, k and v rows follow one another
-    auto load = [&](int tok, int group) -> uint4 {
-        const int head = group * RPW + in_group;
-        if (head >= heads || !live) return make_uint4(0, 0, 0, 0);
-        const bool is_q = head < a.q_heads, is_k = head < qk_heads;
-        const unsigned short* base =
-            static_cast<const unsigned short*>(is_q ? a.q : is_k ? a.k : a.v);
-        const int64_t at = (t0 + tok) * (is_q ? a.q_token : is_k ? a.k_token : a.v_token) +
-                           (head - (is_q ? 0 : is_k ? a.q_heads : qk_heads)) *
-                               (is_q ? a.q_head : is_k ? a.k_head : a.v_head);
-        return __ldcs(reinterpret_cast<const uint4*>(base + at) + sub);
+    // a lane's row of a group, at the block's first token: its address, the step
+    // to the next token's, and whether there is such a row
+    const unsigned short* src;
+    int64_t src_step;
+    bool here;
+    auto open_group = [&](int group) {
+        const bool is_q = group < plan.q_groups, is_k = group < k_end;
+        const int head = (group - (is_q ? 0 : is_k ? plan.q_groups : k_end)) * RPW + in_group;
+        src_step = is_q ? a.q_token : is_k ? a.k_token : a.v_token;
+        src = static_cast<const unsigned short*>(is_q ? a.q : is_k ? a.k : a.v) + t0 * src_step +
+              head * (is_q ? a.q_head : is_k ? a.k_head : a.v_head) + first;
+        here = live && group < groups && head < (is_q ? a.q_heads : a.kv_heads);
     };
-    // the rows' loads first: they are in flight while the angles are computed
-    int ltok = warp / per_token, lgroup = group0;
-    auto next = [&](int& tok, int& group) {
-        group += per_token;
-        if (group >= plan.groups) {
-            group = group0;
-            tok += plan.abreast;
-        }
-    };
-    int tok = ltok, group = lgroup;
-    uint4 raw[U];
-    const bool any = group0 < plan.groups;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (any && ltok < nt) raw[u] = load(ltok, lgroup);
-        next(ltok, lgroup);
-    }
-    Pair qw[4], kw[4];
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        const uint4* from = static_cast<const uint4*>(side == 0 ? a.q_weight : a.k_weight);
-        Pair(&w)[4] = side == 0 ? qw : kw;
-        if (from != nullptr && live) {
-            unpack_row<E>(__ldg(from + sub), w);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = make_pair(1.f, 1.f);
-        }
-    }
-    const bool norms = a.q_weight != nullptr || a.k_weight != nullptr;
+    // the first rows' loads are in flight while the angles are computed, and every
+    // later row's while the one before it is
+    int group = blockIdx.y * kWarps + warp;
+    open_group(group);
+    Row ahead = {};
+    if (here) ahead = load_row(src, second);
 
     for (int i = threadIdx.x; i < nt * pairs; i += kNormThreads) {
         const int k = i / pairs;
@@ -198,12 +194,9 @@ qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPl
         const float half_turns = (float)(int32_t)(uint32_t)(phase >> 32) * 0x1p-31f;
         float sn, cs;
         sincospif(half_turns, &sn, &cs);
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            float* word = reinterpret_cast<float*>(&turn[side][k][turn_word(p, chunks)]);
-            word[p & 1] = cs * a.rope_scale;
-            word[2 + (p & 1)] = side == 0 ? sn * a.rope_scale : -sn * a.rope_scale;
-        }
+        float* word = reinterpret_cast<float*>(&turn[k][p >> 1]);
+        word[p & 1] = cs * a.rope_scale;
+        word[2 + (p & 1)] = sn * a.rope_scale;
     }
     if (cached) {
         for (int k = warp; k < nt; k += kWarps) {
@@ -218,24 +211,40 @@ qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPl
         }
     }
     __syncthreads();
-    if (!any) return;
 
     const float inv_d = 1.0f / (float)a.head_dim;
-    while (tok < nt) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (tok >= nt) break;  // a warp's rows go on together
-            const int head = group * RPW + in_group;
-            const uint4 mine = raw[u];
-            if (ltok < nt) raw[u] = load(ltok, lgroup);
-            next(ltok, lgroup);
-            const bool here = head < heads && live;
-            const bool is_q = head < a.q_heads;
-            uint4 y = mine;
-            if (group * RPW < qk_heads) {  // else value rows alone
+    // rows of one group through all tokens: turned (queries, keys) or copied, to
+    // `dst` stepping from token to token or to the tokens' slots behind it
+    auto run = [&](auto turned, auto slots, unsigned short* dst, int64_t dst_step,
+                   const void* weight) {
+        const bool here_now = here;
+        // behind this group's last row comes the next group's first
+        group += kWarps * gridDim.y;
+        const unsigned short* at = src;
+        const int64_t at_step = src_step;
+        open_group(group);
+        Pair w[4];
+        if constexpr (turned) {
+            Row r = {};
+            if (weight != nullptr && live) {
+                const unsigned short* from = static_cast<const unsigned short*>(weight) + first;
+                r.a = __ldg(reinterpret_cast<const uint2*>(from));
+                r.b = __ldg(reinterpret_cast<const uint2*>(from + second));
+            }
+            unpack_row<E>(r, w);
+        }
+        for (int tok = 0; tok < nt; ++tok) {
+            Row y = ahead;
+            at += at_step;
+            if (tok + 1 == nt) {
+                if (here) ahead = load_row(src, second);
+            } else if (here_now) {
+                ahead = load_row(at, second);
+            }
+            if constexpr (turned) {
                 Pair x[4];
-                unpack_row<E>(mine, x);
-                if (norms) {
+                unpack_row<E>(y, x);
+                if (weight != nullptr) {
                     Pair sq = x[0] * x[0];
 #pragma unroll
                     for (int i = 1; i < 4; ++i) sq = fma_pair(x[i], x[i], sq);
@@ -245,41 +254,36 @@ qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPl
 #pragma unroll
                     for (int m = LPR / 2; m >= 1; m >>= 1)
                         lo += __shfl_xor_sync(0xffffffffu, lo, m);
-                    // rows with a norm and rows without may share a warp
-                    const bool norm = (is_q ? a.q_weight : a.k_weight) != nullptr;
-                    const float inv = norm ? rsqrtf(fmaf(lo, inv_d, a.eps)) : 1.f;
+                    const float inv = rsqrtf(fmaf(lo, inv_d, a.eps));
                     const Pair inv2 = make_pair(inv, inv);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = x[i] * (inv2 * (is_q ? qw[i] : kw[i]));
+                    for (int i = 0; i < 4; ++i) x[i] = x[i] * (inv2 * w[i]);
                 }
-                if constexpr (kLayout == kPairsInterleaved) {
-                    const float4* word = turn[0][tok];
+                if constexpr (kLayout == kPairsHalves) {
+                    if (turns) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int p = sub * 4 + i;
-                        if (p < pairs) {
-                            const float* w = reinterpret_cast<const float*>(
-                                &word[turn_word(p, chunks)]);
-                            const float c = w[p & 1], sn = w[2 + (p & 1)];
-                            float y0, y1;
-                            split(x[i], y0, y1);
-                            x[i] = make_pair(fmaf(y0, c, -y1 * sn), fmaf(y1, c, y0 * sn));
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 v = turn[tok][sub * 2 + i];
+                            const Pair c = make_pair(v.x, v.y), n = make_pair(v.z, v.w);
+                            const Pair lo = x[i], hi = x[i + 2];
+                            x[i] = fma_pair(lo, c, hi * make_pair(-v.z, -v.w));
+                            x[i + 2] = fma_pair(hi, c, lo * n);
                         }
                     }
-                } else if constexpr (kLayout == kPairsHalves) {
-                    const int per = pairs >> 3;  // lanes of half the rotary part
-                    const bool low = sub < per;
-                    const int mate = low ? lane + per : sub < 2 * per ? lane - per : lane;
-                    const float4* word = &turn[low ? 1 : 0][tok][low ? sub : sub - per];
+                } else if constexpr (kLayout == kPairsInterleaved) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float lo, hi;
-                        split(x[i], lo, hi);
-                        const Pair o = make_pair(__shfl_sync(0xffffffffu, lo, mate),
-                                                 __shfl_sync(0xffffffffu, hi, mate));
-                        if (sub < 2 * per) {
-                            const float4 w = word[i * chunks];
-                            x[i] = fma_pair(x[i], make_pair(w.x, w.y), o * make_pair(w.z, w.w));
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 v = turn[tok][sub * 2 + i];
+                        const int p = sub * 4 + 2 * i;
+                        float y0, y1;
+                        if (p < pairs) {
+                            split(x[2 * i], y0, y1);
+                            x[2 * i] = make_pair(fmaf(y0, v.x, -y1 * v.z), fmaf(y1, v.x, y0 * v.z));
+                        }
+                        if (p + 1 < pairs) {
+                            split(x[2 * i + 1], y0, y1);
+                            x[2 * i + 1] =
+                                make_pair(fmaf(y0, v.y, -y1 * v.w), fmaf(y1, v.y, y0 * v.w));
                         }
                     }
                 } else {
@@ -297,36 +301,51 @@ qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPl
                         const int e = sub * 8 + i;
                         if (e < 2 * pairs) {
                             const int p = e < pairs ? e : e - pairs;
-                            const float* w = reinterpret_cast<const float*>(
-                                &turn[e < pairs ? 1 : 0][tok][turn_word(p, chunks)]);
-                            z[i] = fmaf(z[i], w[p & 1],
-                                        row[e < pairs ? e + pairs : p] * w[2 + (p & 1)]);
+                            const float* v = reinterpret_cast<const float*>(&turn[tok][p >> 1]);
+                            const float o = row[e < pairs ? e + pairs : p];
+                            z[i] = fmaf(z[i], v[p & 1], (e < pairs ? -o : o) * v[2 + (p & 1)]);
                         }
                     }
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[i] = make_pair(z[2 * i], z[2 * i + 1]);
                 }
-                if (head < qk_heads) y = pack_row<E>(x);
+                y = pack_row<E>(x);
             }
-            if (here) {
-                const int64_t slot = cached ? dst_s[tok] : 0;
-                unsigned short* dst;
-                int64_t at;
-                if (is_q) {
-                    dst = static_cast<unsigned short*>(a.q_out);
-                    at = (t0 + tok) * a.q_out_token + head * a.q_out_head;
-                } else if (cached) {
-                    const bool is_k = head < qk_heads;
-                    dst = static_cast<unsigned short*>(is_k ? a.k_cache : a.v_cache);
-                    at = slot + (head - (is_k ? a.q_heads : qk_heads)) * a.head_stride;
-                } else {
-                    dst = static_cast<unsigned short*>(a.k_out);
-                    at = (t0 + tok) * a.k_out_token + (head - a.q_heads) * a.k_out_head;
-                }
-                if (is_q || slot >= 0) reinterpret_cast<uint4*>(dst + at)[sub] = y;
+            if constexpr (slots) {
+                const int64_t slot = dst_s[tok];
+                if (here_now && slot >= 0) store_row(dst + slot, second, y);
+            } else {
+                if (here_now) store_row(dst, second, y);
+                dst += dst_step;
             }
-            next(tok, group);
+        }
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    while (group < groups) {
+        if (group < plan.q_groups) {
+            const int head = group * RPW + in_group;
+            run(Yes{}, No{},
+                static_cast<unsigned short*>(a.q_out) + t0 * a.q_out_token + head * a.q_out_head +
+                    first,
+                a.q_out_token, a.q_weight);
+        } else if (group < k_end) {
+            const int head = (group - plan.q_groups) * RPW + in_group;
+            if (cached)
+                run(Yes{}, Yes{},
+                    static_cast<unsigned short*>(a.k_cache) + head * a.head_stride + first, 0,
+                    a.k_weight);
+            else
+                run(Yes{}, No{},
+                    static_cast<unsigned short*>(a.k_out) + t0 * a.k_out_token +
+                        head * a.k_out_head + first,
+                    a.k_out_token, a.k_weight);
+        } else {
+            const int head = (group - k_end) * RPW + in_group;
+            run(No{}, Yes{},
+                static_cast<unsigned short*>(a.v_cache) + head * a.head_stride + first, 0,
+                nullptr);
         }
     }
 }
@@ -358,27 +377,22 @@ cudaError_t launch_rows(const ple_qk_norm_rope_args& a, const DeviceFacts& dev,
     constexpr int RPW = 32 / LPR;
     constexpr int kWarps = kNormThreads / 32;
     RowPlan plan;
+    plan.q_groups = (a.q_heads + RPW - 1) / RPW;
+    plan.kv_groups = (a.kv_heads + RPW - 1) / RPW;
     // one token a block until that makes as many blocks as the device holds
-    // at once, then up to four
-    const int64_t tokens = a.num_tokens / (4 * (int64_t)dev.sm_count);
+    // at once, then up to kNormTokens; while there are fewer blocks than that,
+    // a token's groups spread over several blocks too
+    const int64_t resident = kNormBlocks * (int64_t)dev.sm_count;
+    const int64_t tokens = a.num_tokens / resident;
     plan.tokens = (int)(tokens < 1 ? 1 : tokens > kNormTokens ? kNormTokens : tokens);
-    const int heads = a.q_heads + a.kv_heads * (a.k_cache != nullptr ? 2 : 1);
-    plan.groups = (heads + RPW - 1) / RPW;
-    // as few warps a token as leave none idle in its last step, but all of them
-    // on a block's only token
-    plan.abreast = 1;
-    int best = 0;
-    for (int abreast = 1; abreast <= plan.tokens && abreast <= kWarps; abreast *= 2) {
-        const int per = kWarps / abreast;
-        const int used = plan.groups * 1000 / ((plan.groups + per - 1) / per * per);
-        if (used > best) {
-            best = used;
-            plan.abreast = abreast;
-        }
-    }
-    const dim3 grid((unsigned)((a.num_tokens + plan.tokens - 1) / plan.tokens));
+    const int64_t blocks = (a.num_tokens + plan.tokens - 1) / plan.tokens;
+    const int groups = plan.q_groups + plan.kv_groups * (a.k_cache != nullptr ? 2 : 1);
+    int64_t split = resident / blocks;
+    const int64_t most = (groups + kWarps - 1) / kWarps;
+    split = split < 1 ? 1 : split > most ? most : split;
+    const dim3 grid((unsigned)blocks, (unsigned)split);
     auto* fn = a.interleaved           ? qk_norm_rope_kernel<E, LPR, kPairsInterleaved>
-               : a.rotary_dim % 16 == 0 ? qk_norm_rope_kernel<E, LPR, kPairsHalves>
+               : a.rotary_dim % 8 == 0 ? qk_norm_rope_kernel<E, LPR, kPairsHalves>
                                         : qk_norm_rope_kernel<E, LPR, kPairsAnyHalves>;
     return launch_kernel(fn, grid, dim3(kNormThreads), 0, stream, programmatic_launch(), a,
                          plan);
