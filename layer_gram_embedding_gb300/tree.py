@@ -11,8 +11,9 @@ the paged cache (ple_tree_attention) and the commit of the accepted branches
 As in binding.py every function checks and converts its arguments and calls
 the C ABI entry point of its name; tensors that are not all on one CUDA device
 are refused with ValueError, and there is no CPU path.  A verification step
-makes these calls once per layer, so the checks here are kept to a few
-microseconds.
+makes most of these calls once per layer, and a small one lasts a few
+microseconds on the device, so each function first tests its arguments in one
+expression; only when that fails do the checks that name the culprit run.
 
 Caches are [pages, kv_heads, page_size, head_dim] views (for the commit of
 several layers [layers, pages, kv_heads, page_size, head_dim]): any strides
@@ -52,14 +53,17 @@ def _device(where: str, *tensors) -> int:
     return dev
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_empty = torch.empty
+_i32, _i64 = torch.int32, torch.int64
+
+
 def _call(where: str, fn, dev: int, stream, *args):
     """Call a library function on the tensors' device and the given (or the
     device's current) stream."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        handle = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    handle = _current_stream(dev) if stream is None else stream.cuda_stream
+    if _current_device() == dev:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -125,21 +129,28 @@ def ple_build_tree_index(parent: torch.Tensor, cu_seqlens: torch.Tensor, ctx_len
     bit j of a mask (64 to a word) is set for the node itself and its
     ancestors.  mask_words words hold trees of up to 64 * mask_words nodes."""
     where = "ple_build_tree_index"
-    dev = _device(where, parent, cu_seqlens, ctx_lens, positions, tree_mask)
+    dev = parent.get_device()
     T, B, W = parent.shape[0], ctx_lens.shape[0], int(mask_words)
-    _vector(parent, torch.int32, T, "parent", where)
-    _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", where)
-    _vector(ctx_lens, torch.int32, B, "ctx_lens", where)
+    if not (positions is None and tree_mask is None and dev >= 0
+            and parent.dtype is _i32 and cu_seqlens.dtype is _i32 and ctx_lens.dtype is _i32
+            and cu_seqlens.get_device() == dev and ctx_lens.get_device() == dev
+            and parent.dim() == 1 and ctx_lens.dim() == 1 and cu_seqlens.shape == (B + 1,)
+            and parent.is_contiguous() and cu_seqlens.is_contiguous()
+            and ctx_lens.is_contiguous()):
+        dev = _device(where, parent, cu_seqlens, ctx_lens, positions, tree_mask)
+        _vector(parent, _i32, T, "parent", where)
+        _vector(cu_seqlens, _i32, B + 1, "cu_seqlens", where)
+        _vector(ctx_lens, _i32, B, "ctx_lens", where)
+        if positions is not None:
+            _vector(positions, _i32, T, "positions", where)
+        if tree_mask is not None:
+            _table(tree_mask, _i64, T, "tree_mask", where)
+            if tree_mask.shape[1] != W:
+                raise ValueError(f"{where}: tree_mask must be [T, mask_words]")
     if positions is None:
-        positions = torch.empty(T, dtype=torch.int32, device=parent.device)
-    else:
-        _vector(positions, torch.int32, T, "positions", where)
+        positions = _empty(T, dtype=_i32, device=parent.device)
     if tree_mask is None:
-        tree_mask = torch.empty((T, max(W, 0)), dtype=torch.int64, device=parent.device)
-    else:
-        _table(tree_mask, torch.int64, T, "tree_mask", where)
-        if tree_mask.shape[1] != W:
-            raise ValueError(f"{where}: tree_mask must be [T, mask_words]")
+        tree_mask = _empty((T, max(W, 0)), dtype=_i64, device=parent.device)
     _call(where, lib().ple_build_tree_index, dev, stream, parent.data_ptr(),
           cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, T, W, positions.data_ptr(),
           tree_mask.data_ptr())
@@ -158,39 +169,52 @@ def ple_tree_row_ids(input_ids: torch.Tensor, parent: torch.Tensor, cu_seqlens: 
     ancestors, then the carried context.  parent [T] and cu_seqlens [B + 1]:
     int32, as for ple_build_tree_index; the other arguments as ple_row_ids."""
     where = "ple_tree_row_ids"
-    dev = _device(where, input_ids, parent, cu_seqlens, ngram_context, layer_multipliers,
-                  vocab_sizes, offsets, out, heads)
-    ids = _IDS.get(input_ids.dtype)
-    if ids is None or ngram_context.dtype != input_ids.dtype:
-        raise TypeError(f"{where}: input_ids and ngram_context must share int32 or int64")
-    N = int(ngram_size)
-    T = input_ids.shape[0]
-    B, C = ngram_context.shape if ngram_context.dim() == 2 else (-1, -1)
+    dev = input_ids.get_device()
+    kind = input_ids.dtype
+    ids, out_code = _IDS.get(kind), _IDS.get(out_dtype)
+    N, T = int(ngram_size), input_ids.shape[0]
     M = layer_multipliers.reshape(1, -1) if layer_multipliers.dim() == 1 else layer_multipliers
     vocab = vocab_sizes.reshape(1, -1) if vocab_sizes.dim() == 1 else vocab_sizes
     off = offsets.reshape(1, -1) if offsets.dim() == 1 else offsets
-    L = vocab.shape[0]
-    _vector(input_ids, input_ids.dtype, T, "input_ids", where)
-    _vector(parent, torch.int32, T, "parent", where)
-    _table(ngram_context, input_ids.dtype, B, "ngram_context", where)
-    _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", where)
-    _table(vocab, torch.int64, L, "vocab_sizes", where)
-    _table(M, torch.int64, L, "layer_multipliers", where)
-    _table(off, torch.int64, L, "offsets", where)
-    H = vocab.shape[1]
-    if M.shape[1] != N or off.shape[1] != H:
-        raise ValueError(f"{where}: layer_multipliers must be [L, ngram_size], offsets must have "
-                         "the shape of vocab_sizes")
-    out_code = _IDS.get(out_dtype)
-    if out_code is None:
-        raise TypeError(f"{where}: out_dtype must be torch.int64 or torch.int32")
+    shape = vocab.shape
+    B, C = ngram_context.shape if ngram_context.dim() == 2 else (-1, -1)
+    if not (out is None and heads is None and dev >= 0 and ids is not None
+            and out_code is not None and ngram_context.dtype is kind and parent.dtype is _i32
+            and cu_seqlens.dtype is _i32 and M.dtype is _i64 and vocab.dtype is _i64
+            and off.dtype is _i64 and parent.get_device() == dev
+            and cu_seqlens.get_device() == dev and ngram_context.get_device() == dev
+            and M.get_device() == dev and vocab.get_device() == dev and off.get_device() == dev
+            and B >= 0 and cu_seqlens.shape == (B + 1,) and input_ids.dim() == 1
+            and parent.shape == (T,) and len(shape) == 2 and off.shape == shape
+            and M.shape == (shape[0], N) and input_ids.is_contiguous() and parent.is_contiguous()
+            and cu_seqlens.is_contiguous() and ngram_context.is_contiguous()
+            and M.is_contiguous() and vocab.is_contiguous() and off.is_contiguous()):
+        dev = _device(where, input_ids, parent, cu_seqlens, ngram_context, layer_multipliers,
+                      vocab_sizes, offsets, out, heads)
+        if ids is None or ngram_context.dtype != kind:
+            raise TypeError(f"{where}: input_ids and ngram_context must share int32 or int64")
+        _vector(input_ids, kind, T, "input_ids", where)
+        _vector(parent, _i32, T, "parent", where)
+        _table(ngram_context, kind, B, "ngram_context", where)
+        _vector(cu_seqlens, _i32, B + 1, "cu_seqlens", where)
+        _table(vocab, _i64, shape[0], "vocab_sizes", where)
+        _table(M, _i64, shape[0], "layer_multipliers", where)
+        _table(off, _i64, shape[0], "offsets", where)
+        if M.shape[1] != N or off.shape[1] != shape[1]:
+            raise ValueError(f"{where}: layer_multipliers must be [L, ngram_size], offsets must "
+                             "have the shape of vocab_sizes")
+        if out_code is None:
+            raise TypeError(f"{where}: out_dtype must be torch.int64 or torch.int32")
+        if out is not None and (out.dtype != out_dtype or not out.is_contiguous()
+                                or out.shape != (shape[0], T, shape[1])):
+            raise ValueError(f"{where}: out must be a contiguous {out_dtype} [L, T, H]")
+        if heads is not None and (heads.dtype != torch.uint8 or not heads.is_contiguous()
+                                  or heads.shape != (shape[0], shape[1], PLE_HEAD_BYTES)):
+            raise ValueError(f"{where}: heads must be ple_prepare_heads' [L, H, "
+                             f"{PLE_HEAD_BYTES}]")
+    L, H = shape
     if out is None:
-        out = torch.empty((L, T, H), dtype=out_dtype, device=input_ids.device)
-    elif out.dtype != out_dtype or tuple(out.shape) != (L, T, H) or not out.is_contiguous():
-        raise ValueError(f"{where}: out must be a contiguous {out_dtype} [L, T, H]")
-    if heads is not None and (heads.dtype != torch.uint8 or not heads.is_contiguous() or
-                              tuple(heads.shape) != (L, H, PLE_HEAD_BYTES)):
-        raise ValueError(f"{where}: heads must be ple_prepare_heads' [L, H, {PLE_HEAD_BYTES}]")
+        out = _empty((L, T, H), dtype=out_dtype, device=input_ids.device)
     _call(where, lib().ple_tree_row_ids, dev, stream, input_ids.data_ptr(), ids, T,
           parent.data_ptr(), cu_seqlens.data_ptr(), ngram_context.data_ptr(), B, C, M.data_ptr(),
           vocab.data_ptr(), off.data_ptr(), H, N, int(heads_per_ngram), L, int(boundary_id),
@@ -253,35 +277,84 @@ def ple_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
     Without one v is not read and (q_out, k_out) is returned.  q_out and k_out
     may be q and k themselves."""
     where = "ple_qk_norm_rope"
+    dev = q.get_device()
+    dtype = q.dtype
+    element = _ELEMENTS.get(dtype)
+    if element is None or q.dim() != 3 or k.dim() != 3:
+        _device(where, q, k)
+        _element(q, "q", where)
+        raise ValueError(f"{where}: q must be [T, q_heads, head_dim] and k [T, kv_heads, head_dim]")
+    T, Hq, D = q_shape = q.shape
+    k_shape = k.shape
+    Hk = k_shape[1]
+    R = 0 if rope is None else 2 * rope.shape[0]
+    qs, ks = q.stride(), k.stride()
+    cached = k_cache is not None
+    # the step of a serving loop: norms, a rotation and a cache, new queries
+    quick = (cached and q_out is None and k_out is None and rope is not None
+             and positions is not None and q_weight is not None and k_weight is not None
+             and v is not None and v_cache is not None and page_table is not None
+             and ctx_lens is not None and cu_seqlens is not None and dev >= 0
+             and k.dtype is dtype and v.dtype is dtype and q_weight.dtype is dtype
+             and k_weight.dtype is dtype and k_cache.dtype is dtype and v_cache.dtype is dtype
+             and positions.dtype is _i32 and rope.dtype is _i64 and page_table.dtype is _i32
+             and ctx_lens.dtype is _i32 and cu_seqlens.dtype is _i32
+             and k.get_device() == dev and v.get_device() == dev
+             and q_weight.get_device() == dev and k_weight.get_device() == dev
+             and k_cache.get_device() == dev and v_cache.get_device() == dev
+             and positions.get_device() == dev and rope.get_device() == dev
+             and page_table.get_device() == dev and ctx_lens.get_device() == dev
+             and cu_seqlens.get_device() == dev)
+    if quick:
+        B = ctx_lens.shape[0]
+        v_strides, cache_strides, cache_shape = v.stride(), k_cache.stride(), k_cache.shape
+        table_shape = page_table.shape
+        quick = (k_shape[0] == T and k_shape[2] == D and v.shape == k_shape
+                 and qs[2] == 1 and ks[2] == 1 and v_strides[2] == 1
+                 and q_weight.shape == (D,) and k_weight.shape == (D,)
+                 and positions.shape == (T,) and rope.dim() == 1
+                 and len(cache_shape) == 4 and v_cache.shape == cache_shape
+                 and v_cache.stride() == cache_strides and cache_strides[3] == 1
+                 and cache_shape[1] == Hk and cache_shape[3] == D and ctx_lens.dim() == 1
+                 and cu_seqlens.shape == (B + 1,) and len(table_shape) == 2
+                 and table_shape[0] == B and q_weight.is_contiguous()
+                 and k_weight.is_contiguous() and positions.is_contiguous()
+                 and rope.is_contiguous() and page_table.is_contiguous()
+                 and ctx_lens.is_contiguous() and cu_seqlens.is_contiguous())
+    if quick:
+        q_out = _empty(q_shape, dtype=dtype, device=q.device)
+        args = _NORM_ROPE.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], v_strides[0],
+            v_strides[1], positions.data_ptr(), rope.data_ptr(), q_weight.data_ptr(),
+            k_weight.data_ptr(), q_out.data_ptr(), Hq * D, D, 0, 0, 0, k_cache.data_ptr(),
+            v_cache.data_ptr(), cache_strides[0], cache_strides[1], cache_strides[2],
+            cache_shape[0], page_table.data_ptr(), ctx_lens.data_ptr(), cu_seqlens.data_ptr(), T,
+            B, table_shape[1], cache_shape[2], element, Hq, Hk, D, R, 1 if interleaved else 0,
+            rope_scale, eps)
+        _call(where, lib().ple_qk_norm_rope, dev, stream, args)
+        return q_out
+
     dev = _device(where, q, k, v, positions, rope, q_weight, k_weight, k_cache, v_cache,
                   page_table, ctx_lens, cu_seqlens, q_out, k_out)
-    element = _element(q, "q", where)
-    dtype = q.dtype
-    if q.dim() != 3:
-        raise ValueError(f"{where}: q must be [T, q_heads, head_dim]")
-    T, Hq, D = q.shape
     _heads(q, dtype, T, None, D, "q", where)
     _heads(k, dtype, T, None, D, "k", where)
-    Hk = k.shape[1]
-    R = 0
     if rope is not None:
-        _vector(rope, torch.int64, rope.shape[0], "rope", where)
-        R = 2 * rope.shape[0]
+        _vector(rope, _i64, rope.shape[0], "rope", where)
         if positions is None:
             raise ValueError(f"{where}: a rotation needs positions")
-        _vector(positions, torch.int32, T, "positions", where)
+        _vector(positions, _i32, T, "positions", where)
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             _vector(w, dtype, D, name, where)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+        q_out = _empty((T, Hq, D), dtype=dtype, device=q.device)
     else:
         _heads(q_out, dtype, T, Hq, D, "q_out", where)
     pages = B = 0
     cache_strides = (0, 0, 0, 0)
     page_size = max_pages = 1
     v_strides = k_out_strides = (0, 0, 0)
-    if k_cache is not None:
+    if cached:
         if v is None or v_cache is None or page_table is None or ctx_lens is None or \
                 cu_seqlens is None:
             raise ValueError(f"{where}: a cache needs v, v_cache, page_table, ctx_lens and "
@@ -294,20 +367,19 @@ def ple_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
         pages, page_size, B = k_cache.shape[0], k_cache.shape[2], ctx_lens.shape[0]
         if k_cache.shape[1] != Hk or k_cache.shape[3] != D:
             raise ValueError(f"{where}: the caches must be [pages, {Hk}, page_size, {D}]")
-        _vector(ctx_lens, torch.int32, B, "ctx_lens", where)
-        _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", where)
-        _table(page_table, torch.int32, B, "page_table", where)
+        _vector(ctx_lens, _i32, B, "ctx_lens", where)
+        _vector(cu_seqlens, _i32, B + 1, "cu_seqlens", where)
+        _table(page_table, _i32, B, "page_table", where)
         max_pages = page_table.shape[1]
     else:
         if v_cache is not None:
             raise ValueError(f"{where}: pass both caches or neither")
         if k_out is None:
-            k_out = torch.empty((T, Hk, D), dtype=dtype, device=q.device)
+            k_out = _empty((T, Hk, D), dtype=dtype, device=q.device)
         else:
             _heads(k_out, dtype, T, Hk, D, "k_out", where)
         k_out_strides = k_out.stride()
-    qs, ks, os = q.stride(), k.stride(), q_out.stride()
-    cached = k_cache is not None
+    os = q_out.stride()
     args = _NORM_ROPE.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr() if cached else 0, qs[0], qs[1], ks[0], ks[1],
         v_strides[0], v_strides[1], 0 if positions is None else positions.data_ptr(),
@@ -321,6 +393,10 @@ def ple_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
         1 if interleaved else 0, rope_scale, eps)
     _call(where, lib().ple_qk_norm_rope, dev, stream, args)
     return q_out if cached else (q_out, k_out)
+
+
+# bytes by (num_tokens, q_heads, kv_heads, head_dim, device index)
+_workspace_sizes: dict = {}
 
 
 def ple_tree_attention_workspace(num_tokens: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -352,44 +428,72 @@ def ple_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     return_lse.  workspace: ple_tree_attention_workspace's, taken from torch's
     allocator in each call when None."""
     where = "ple_tree_attention"
-    dev = _device(where, q, k_cache, v_cache, page_table, ctx_lens, cu_seqlens, tree_mask, out,
-                  lse, workspace)
-    element = _element(q, "q", where)
+    dev = q.get_device()
     dtype = q.dtype
-    if q.dim() != 3:
-        raise ValueError(f"{where}: q must be [T, q_heads, head_dim]")
+    element = _ELEMENTS.get(dtype)
+    if element is None or q.dim() != 3 or k_cache.dim() != 4:
+        _device(where, q, k_cache, v_cache)
+        _element(q, "q", where)
+        raise ValueError(f"{where}: q must be [T, q_heads, head_dim] and the caches [pages, "
+                         "kv_heads, page_size, head_dim]")
     T, Hq, D = q.shape
-    _heads(q, dtype, T, Hq, D, "q", where)
-    strides = _caches(k_cache, v_cache, dtype, 4, where)
-    pages, Hk, page_size, cache_dim = k_cache.shape
-    if cache_dim != D or Hk < 1 or Hq % Hk:
-        raise ValueError(f"{where}: the caches' heads must divide q's and have their width")
+    cache_shape = k_cache.shape
+    pages, Hk, page_size, cache_dim = cache_shape
+    qs, strides = q.stride(), k_cache.stride()
     B = ctx_lens.shape[0]
-    _vector(ctx_lens, torch.int32, B, "ctx_lens", where)
-    _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", where)
-    _table(page_table, torch.int32, B, "page_table", where)
-    _table(tree_mask, torch.int64, T, "tree_mask", where)
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
-    elif out.dtype != dtype or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError(f"{where}: out must be contiguous, of q's shape and dtype")
-    if lse is not None:
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
+    table_shape, mask_shape = page_table.shape, tree_mask.shape
+    if not (out is None and lse is None and workspace is None and dev >= 0
+            and k_cache.dtype is dtype and v_cache.dtype is dtype and page_table.dtype is _i32
+            and ctx_lens.dtype is _i32 and cu_seqlens.dtype is _i32 and tree_mask.dtype is _i64
+            and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and page_table.get_device() == dev and ctx_lens.get_device() == dev
+            and cu_seqlens.get_device() == dev and tree_mask.get_device() == dev
+            and qs[2] == 1 and v_cache.shape == cache_shape and v_cache.stride() == strides
+            and strides[3] == 1 and cache_dim == D and Hk >= 1 and Hq % Hk == 0
+            and ctx_lens.dim() == 1 and cu_seqlens.shape == (B + 1,)
+            and len(table_shape) == 2 and table_shape[0] == B and len(mask_shape) == 2
+            and mask_shape[0] == T and page_table.is_contiguous() and ctx_lens.is_contiguous()
+            and cu_seqlens.is_contiguous() and tree_mask.is_contiguous()):
+        dev = _device(where, q, k_cache, v_cache, page_table, ctx_lens, cu_seqlens, tree_mask, out,
+                      lse, workspace)
+        _heads(q, dtype, T, Hq, D, "q", where)
+        _caches(k_cache, v_cache, dtype, 4, where)
+        if cache_dim != D or Hk < 1 or Hq % Hk:
+            raise ValueError(f"{where}: the caches' heads must divide q's and have their width")
+        _vector(ctx_lens, _i32, B, "ctx_lens", where)
+        _vector(cu_seqlens, _i32, B + 1, "cu_seqlens", where)
+        _table(page_table, _i32, B, "page_table", where)
+        _table(tree_mask, _i64, T, "tree_mask", where)
+        if out is not None and (out.dtype != dtype or out.shape != q.shape
+                                or not out.is_contiguous()):
+            raise ValueError(f"{where}: out must be contiguous, of q's shape and dtype")
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq)
+                                or not lse.is_contiguous()):
             raise ValueError(f"{where}: lse must be a contiguous float32 [T, q_heads]")
-    elif return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        if workspace is not None and (workspace.dtype != torch.uint8 or workspace.dim() != 1
+                                      or not workspace.is_contiguous()):
+            raise ValueError(f"{where}: workspace must be a contiguous uint8 tensor")
+    device = q.device
+    if out is None:
+        out = _empty((T, Hq, D), dtype=dtype, device=device)
+    if lse is None and return_lse:
+        lse = _empty((T, Hq), dtype=torch.float32, device=device)
     if workspace is None:
-        n = lib().ple_tree_attention_workspace(T, Hq, Hk, D)
-        workspace = torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"{where}: workspace must be a contiguous uint8 tensor")
-    qs = q.stride()
+        sizes = (T, Hq, Hk, D, dev)
+        size = _workspace_sizes.get(sizes)
+        if size is None:
+            if len(_workspace_sizes) >= 4096:
+                _workspace_sizes.clear()
+            with torch.cuda.device(dev):
+                size = max(lib().ple_tree_attention_workspace(T, Hq, Hk, D), 0)
+            _workspace_sizes[sizes] = size
+        workspace = _empty(size, dtype=torch.uint8, device=device)
     args = _ATTENTION.pack(
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), strides[0],
         strides[1], strides[2], pages, page_table.data_ptr(), ctx_lens.data_ptr(),
         cu_seqlens.data_ptr(), tree_mask.data_ptr(), out.data_ptr(),
         0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.shape[0], T, B,
-        page_table.shape[1], page_size, element, Hq, Hk, D, tree_mask.shape[1],
+        table_shape[1], page_size, element, Hq, Hk, D, mask_shape[1],
         D ** -0.5 if scale is None else scale)
     _call(where, lib().ple_tree_attention, dev, stream, args)
     return (out, lse) if return_lse else out
@@ -410,44 +514,65 @@ def ple_tree_commit(input_ids: torch.Tensor, path: torch.Tensor, accepted: torch
     [B, ngram_size - 1] what the next step passes as its ngram_context (None
     when ngram_context is None)."""
     where = "ple_tree_commit"
-    dev = _device(where, input_ids, path, accepted, cu_seqlens, ngram_context, ctx_lens,
-                  page_table, k_cache, v_cache, next_context, next_ctx_lens)
-    element = _element(k_cache, "the caches", where)
+    dev = input_ids.get_device()
     if k_cache.dim() == 4 and v_cache.dim() == 4:
         k_cache, v_cache = k_cache.unsqueeze(0), v_cache.unsqueeze(0)
-    strides = _caches(k_cache, v_cache, k_cache.dtype, 5, where)
-    L, pages, Hk, page_size, D = k_cache.shape
-    ids = _IDS.get(input_ids.dtype)
-    if ids is None:
-        raise TypeError(f"{where}: input_ids must be int32 or int64")
+    dtype, kind = k_cache.dtype, input_ids.dtype
+    element, ids = _ELEMENTS.get(dtype), _IDS.get(kind)
+    strides, cache_shape = k_cache.stride(), k_cache.shape
     T, B = input_ids.shape[0], ctx_lens.shape[0]
-    _vector(input_ids, input_ids.dtype, T, "input_ids", where)
-    _vector(ctx_lens, torch.int32, B, "ctx_lens", where)
-    _vector(accepted, torch.int32, B, "accepted", where)
-    _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", where)
-    _table(path, torch.int32, B, "path", where)
-    _table(page_table, torch.int32, B, "page_table", where)
-    C = 0
-    if ngram_context is not None:
-        _table(ngram_context, input_ids.dtype, B, "ngram_context", where)
-        C = ngram_context.shape[1]
-        if next_context is None:
-            next_context = torch.empty((B, C), dtype=input_ids.dtype, device=input_ids.device)
-        else:
-            _table(next_context, input_ids.dtype, B, "next_context", where)
-            if next_context.shape[1] != C:
-                raise ValueError(f"{where}: next_context must have ngram_context's shape")
-    elif next_context is not None:
-        raise ValueError(f"{where}: next_context needs ngram_context")
+    path_shape, table_shape = path.shape, page_table.shape
+    if not (element is not None and ids is not None and next_context is None
+            and next_ctx_lens is None and ngram_context is not None and dev >= 0
+            and v_cache.dtype is dtype and path.dtype is _i32 and accepted.dtype is _i32
+            and cu_seqlens.dtype is _i32 and ctx_lens.dtype is _i32
+            and page_table.dtype is _i32 and ngram_context.dtype is kind
+            and path.get_device() == dev and accepted.get_device() == dev
+            and cu_seqlens.get_device() == dev and ngram_context.get_device() == dev
+            and ctx_lens.get_device() == dev and page_table.get_device() == dev
+            and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and input_ids.dim() == 1 and ctx_lens.dim() == 1 and accepted.shape == (B,)
+            and cu_seqlens.shape == (B + 1,) and len(path_shape) == 2 and path_shape[0] == B
+            and len(table_shape) == 2 and table_shape[0] == B and ngram_context.dim() == 2
+            and ngram_context.shape[0] == B and len(cache_shape) == 5
+            and v_cache.shape == cache_shape and v_cache.stride() == strides
+            and strides[4] == 1 and input_ids.is_contiguous() and path.is_contiguous()
+            and accepted.is_contiguous() and cu_seqlens.is_contiguous()
+            and ngram_context.is_contiguous() and ctx_lens.is_contiguous()
+            and page_table.is_contiguous()):
+        dev = _device(where, input_ids, path, accepted, cu_seqlens, ngram_context, ctx_lens,
+                      page_table, k_cache, v_cache, next_context, next_ctx_lens)
+        _element(k_cache, "the caches", where)
+        _caches(k_cache, v_cache, dtype, 5, where)
+        if ids is None:
+            raise TypeError(f"{where}: input_ids must be int32 or int64")
+        _vector(input_ids, kind, T, "input_ids", where)
+        _vector(ctx_lens, _i32, B, "ctx_lens", where)
+        _vector(accepted, _i32, B, "accepted", where)
+        _vector(cu_seqlens, _i32, B + 1, "cu_seqlens", where)
+        _table(path, _i32, B, "path", where)
+        _table(page_table, _i32, B, "page_table", where)
+        if ngram_context is not None:
+            _table(ngram_context, kind, B, "ngram_context", where)
+            if next_context is not None:
+                _table(next_context, kind, B, "next_context", where)
+                if next_context.shape != ngram_context.shape:
+                    raise ValueError(f"{where}: next_context must have ngram_context's shape")
+        elif next_context is not None:
+            raise ValueError(f"{where}: next_context needs ngram_context")
+        if next_ctx_lens is not None:
+            _vector(next_ctx_lens, _i32, B, "next_ctx_lens", where)
+    C = 0 if ngram_context is None else ngram_context.shape[1]
+    if next_context is None and ngram_context is not None:
+        next_context = _empty((B, C), dtype=kind, device=input_ids.device)
     if next_ctx_lens is None:
-        next_ctx_lens = torch.empty(B, dtype=torch.int32, device=input_ids.device)
-    else:
-        _vector(next_ctx_lens, torch.int32, B, "next_ctx_lens", where)
+        next_ctx_lens = _empty(B, dtype=_i32, device=input_ids.device)
+    L, pages, Hk, page_size, D = cache_shape
     args = _COMMIT.pack(
         input_ids.data_ptr(), path.data_ptr(), accepted.data_ptr(), cu_seqlens.data_ptr(),
         0 if C == 0 else ngram_context.data_ptr(), 0 if C == 0 else next_context.data_ptr(),
         ctx_lens.data_ptr(), next_ctx_lens.data_ptr(), page_table.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), strides[0], strides[1], strides[2], strides[3], pages, T, B,
-        path.shape[1], ids, C, L, page_table.shape[1], page_size, Hk, D, element)
+        path_shape[1], ids, C, L, table_shape[1], page_size, Hk, D, element)
     _call(where, lib().ple_tree_commit, dev, stream, args)
     return next_context, next_ctx_lens
