@@ -44,16 +44,17 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
 constexpr long long kWaitClocks = 2000000000ll;
 
 // A whole warp waits for the phase of the given parity.  Where it does not come
-// within kWaitClocks the block's `failed` is set, and every later wait of the
-// block returns at once.
-__device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
-    if (!mbar_try(bar, parity)) {
-        const long long start = clock64();
-        while (!mbar_try(bar, parity) && !*failed) {
-            if (clock64() - start > kWaitClocks) *failed = 1;
-        }
+// within kWaitClocks the block's `failed` is set and every later wait of the
+// block that is not met at once returns false, to all lanes.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    const long long start = clock64();
+    bool over = false;
+    while (!mbar_try(bar, parity) && !over) {
+        if (clock64() - start > kWaitClocks) *failed = 1;
+        over = *failed != 0;
     }
-    __syncwarp();
+    return !__any_sync(0xffffffffu, over);
 }
 
 // A whole warp waits until *count has come to `least`, as mbar_wait does.

@@ -416,8 +416,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     const uint32_t item = items + (keys ? key_item(j) : value_item(j, n));
                     const uint32_t slot = item % S::kSlots, round = item / S::kSlots;
                     count_wait(&armed[slot], round, failed);
-                    mbar_wait(&empty[slot], (round & 1) ^ 1, failed);
-                    if (__any_sync(0xffffffffu, *failed)) break;
+                    if (!mbar_wait(&empty[slot], (round & 1) ^ 1, failed) ||
+                        __any_sync(0xffffffffu, *failed))
+                        break;
                     if (lane == 0) {
                         mbar_arrive_expect(&full[slot], S::kTileBytes);
                         armed[slot] = round + 1;
@@ -490,9 +491,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 __syncwarp();
             };
-            auto wait_weights = [&](int w) {
-                mbar_wait(&p_full[w], p_count[w]++ & 1, failed);
+            auto wait_weights = [&](int w) -> bool {
+                const bool ok = mbar_wait(&p_full[w], p_count[w]++ & 1, failed);
                 tmem_fence_after();
+                return ok;
             };
             while (walk.next(s)) {
                 const int n = s.k1 - s.k0;
@@ -545,16 +547,15 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     scores(1, k, 1, true);
                     for (int j = 0; j < n; ++j) {
                         const bool more = j + 1 < n;
-                        wait_weights(0);
+                        // the next keys were copied before these values: both are
+                        // at hand before the weights are
                         const uint32_t v = wait_item(items + value_item(j, n));
-                        if (__any_sync(0xffffffffu, *failed)) break;
+                        if (more) k = wait_item(items + key_item(j + 1));
                         clean(j, v);
+                        if (!wait_weights(0)) break;
                         values(0, v, j > 0, false);
-                        if (more) {
-                            k = wait_item(items + key_item(j + 1));
-                            scores(0, k, 0, false);
-                        }
-                        wait_weights(1);
+                        if (more) scores(0, k, 0, false);
+                        if (!wait_weights(1)) break;
                         values(1, v, j > 0, true);
                         if (more) scores(1, k, 1, true);
                     }
@@ -563,10 +564,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         scores(w, wait_item(items + key_item(w)), 0, true);
                     for (int j = 0; j < n; ++j) {
                         const int w = j & 1;
-                        wait_weights(w);
                         const uint32_t v = wait_item(items + value_item(j, n));
-                        if (__any_sync(0xffffffffu, *failed)) break;
                         clean(j, v);
+                        if (!wait_weights(w)) break;
                         values(w, v, j > 1, true);
                         if (j + 2 < n) scores(w, wait_item(items + key_item(j + 2)), 0, true);
                     }
@@ -639,8 +639,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             const int step = s.pair ? 1 : 2;
             bool begun = false;
             for (int j = s.pair ? 0 : w; j < n; j += step) {
-                mbar_wait(&s_full[w], count & 1, failed);
-                if (__any_sync(0xffffffffu, *failed)) break;
+                if (!mbar_wait(&s_full[w], count & 1, failed)) break;
                 tmem_fence_after();
                 if (active) {
                     const int first = (s.k0 + j) * kTile;
