@@ -69,9 +69,15 @@ struct TcArgs {
     ple_tree_attention_args a;
     int32_t blocks;      // shares
     int32_t rows_cap;    // rows of a state in the workspace, a multiple of 4
+    int32_t group;       // query heads a key head
     float c;             // |scale| * log2(e)
     uint32_t flip;       // sign bits to turn in Q: scale < 0
 };
+
+// a / b for a >= 0, b > 0; most are small, and a 64-bit division is a routine.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 
 // One request's tiles.
 struct Request {
@@ -81,7 +87,8 @@ struct Request {
     int32_t tiles, units;    // key tiles of a unit; units a key head
 };
 
-__device__ __forceinline__ Request request_of(const ple_tree_attention_args& a, int r) {
+__device__ __forceinline__ Request request_of(const TcArgs& args, int r) {
+    const ple_tree_attention_args& a = args.a;
     Request q;
     int32_t end;
     request_nodes(a.cu_seqlens, r, a.num_tokens, q.begin, end);
@@ -91,7 +98,7 @@ __device__ __forceinline__ Request request_of(const ple_tree_attention_args& a, 
     q.ctx = (int32_t)min(ctx, cap);
     q.length = (int32_t)min(ctx + q.nodes, cap);
     q.tiles = (q.length + kTile - 1) / kTile;
-    const int64_t rows = (int64_t)q.nodes * (a.q_heads / a.kv_heads);
+    const int64_t rows = (int64_t)q.nodes * args.group;
     q.units = (int32_t)((rows + kUnitRows - 1) / kUnitRows);
     q.work = (int64_t)q.units * q.tiles * a.kv_heads;
     return q;
@@ -99,10 +106,10 @@ __device__ __forceinline__ Request request_of(const ple_tree_attention_args& a, 
 
 // First tile of share c of `shares`, and the share of a tile.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int c, int shares) {
-    return total * c / shares;
+    return quotient(total * c, shares);
 }
 __device__ __forceinline__ int share_of(int64_t total, int64_t tile, int shares) {
-    return (int)(((tile + 1) * shares - 1) / total);
+    return (int)quotient((tile + 1) * shares - 1, total);
 }
 
 // A block's tiles [lo, hi) of `total`, the request that owns the first one, and
@@ -116,14 +123,15 @@ struct Share {
 // scanned a block's width at a time: once where they fit, else once for the
 // total and once for the owner.
 template <int kBlock>
-__device__ __forceinline__ void find_share(const ple_tree_attention_args& a, int blocks,
-                                           int64_t* scratch, Share* share) {
+__device__ __forceinline__ void find_share(const TcArgs& args, int64_t* scratch, Share* share) {
+    const ple_tree_attention_args& a = args.a;
+    const int blocks = args.blocks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = a.num_requests;
     int64_t total = 0;
     if (B > kBlock) {
         int64_t mine = 0;
-        for (int r = threadIdx.x; r < B; r += kBlock) mine += request_of(a, r).work;
+        for (int r = threadIdx.x; r < B; r += kBlock) mine += request_of(args, r).work;
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
         if (lane == 0) scratch[warp] = mine;
@@ -133,7 +141,7 @@ __device__ __forceinline__ void find_share(const ple_tree_attention_args& a, int
     int64_t base = 0;
     for (int from = 0; from < B; from += kBlock) {
         const int r = from + threadIdx.x;
-        const int64_t w = r < B ? request_of(a, r).work : 0;
+        const int64_t w = r < B ? request_of(args, r).work : 0;
         int64_t upto = w;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -178,31 +186,30 @@ struct Segment {
 
 // The block's segments in order; every role walks them alike.
 struct Walk {
-    const ple_tree_attention_args& a;
+    const TcArgs& args;
     int64_t at, end;     // tiles still to do
     int64_t base;        // tiles before request r
     int r;
     Request q;
-    __device__ __forceinline__ Walk(const ple_tree_attention_args& args, const Share& share)
-        : a(args), at(share.lo), end(share.hi), base(share.before), r(share.first) {
-        if (at < end) q = request_of(a, r);
+    __device__ __forceinline__ Walk(const TcArgs& the, const Share& share)
+        : args(the), at(share.lo), end(share.hi), base(share.before), r(share.first) {
+        if (at < end) q = request_of(args, r);
     }
     __device__ __forceinline__ bool next(Segment& s) {
         if (at >= end) return false;
         while (at >= base + q.work) {
             base += q.work;
-            q = request_of(a, ++r);
+            q = request_of(args, ++r);
         }
         const int64_t rel = at - base;
-        const int32_t u = (int32_t)(rel / q.tiles);
+        const int32_t u = (int32_t)quotient(rel, q.tiles);
         s.q = q;
         s.k0 = (int32_t)(rel - (int64_t)u * q.tiles);
         s.k1 = (int32_t)min((int64_t)q.tiles, s.k0 + (end - at));
         s.head = u / q.units;
         s.unit = u - s.head * q.units;
-        s.rows = (int32_t)min((int64_t)kUnitRows,
-                              (int64_t)q.nodes * (a.q_heads / a.kv_heads) -
-                                  (int64_t)s.unit * kUnitRows);
+        s.rows = (int32_t)min((int64_t)kUnitRows, (int64_t)q.nodes * args.group -
+                                                     (int64_t)s.unit * kUnitRows);
         s.pair = s.rows > kTile;
         at += s.k1 - s.k0;
         return true;
@@ -210,9 +217,9 @@ struct Walk {
 };
 
 // The offset of the query of a key head's row.
-__device__ __forceinline__ int64_t query_row(const ple_tree_attention_args& a, const Segment& s,
-                                             int row) {
-    const uint32_t group = a.q_heads / a.kv_heads;
+__device__ __forceinline__ int64_t query_row(const TcArgs& args, const Segment& s, int row) {
+    const ple_tree_attention_args& a = args.a;
+    const uint32_t group = args.group;
     const uint32_t node = (uint32_t)row / group;
     return (s.q.begin + (int64_t)node) * a.q_token +
            (int64_t)(s.head * group + (row - node * group)) * a.q_head;
@@ -290,16 +297,17 @@ __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
 }
 
 // Which of 32 slots from `slot` on a node sees, as bits: all below ctx, above it
-// those of its mask.
+// those of its mask (whose first word is at hand).
 __device__ __forceinline__ uint32_t seen_bits(const unsigned long long* __restrict__ mask,
-                                              int words, int ctx, int length, int slot) {
+                                              uint64_t first_word, int words, int ctx, int length,
+                                              int slot) {
     const int b = slot - ctx;
     if (b + 32 <= 0) return 0xffffffffu;
     const int lo = max(b, 0);
     const int limit = min(length - ctx, 64 * words);
     if (lo >= limit) return b < 0 ? (1u << -b) - 1 : 0u;
     const int w = lo >> 6, s = lo & 63;
-    uint64_t v = __ldg(mask + w) >> s;
+    uint64_t v = (w == 0 ? first_word : __ldg(mask + w)) >> s;
     if (s > 32 && w + 1 < words) v |= __ldg(mask + w + 1) << (64 - s);
     uint32_t bits = (uint32_t)v;
     if (limit - lo < 32) bits &= (1u << (limit - lo)) - 1;
@@ -369,13 +377,13 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     }
     wait_grid_before();
 
-    find_share<kThreads>(a, args.blocks, scratch, &share_s);
+    find_share<kThreads>(args, scratch, &share_s);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_s;
-    const int group = a.q_heads / a.kv_heads;
-    Walk walk(a, share_s);
+    const int group = args.group;
+    Walk walk(args, share_s);
     Segment s;
 
     if (warp >= 8) {
@@ -383,8 +391,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             // ------------------------------------------------------- copies
             const bool keys = warp == kKeyWarp;
             const CUtensorMap* map = keys ? &k_map : &v_map;
-            const int box = min(a.page_size, kTile);          // slots a box
+            // a tile is `boxes` whole pages, or one of `per_page` tiles of a page
+            const int box = min(a.page_size, kTile);
             const int boxes = kTile / box;
+            const int per_page = a.page_size / box;
             const int which = lane / S::kHalves, half = lane % S::kHalves;
             const bool mine = which < boxes;
             uint32_t items = 0;
@@ -394,9 +404,11 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 // a box past the tokens, or of a page outside the cache, is filled
                 // with zeros: its page number is outside the map
                 auto page_of = [&](int j) -> int {
-                    const int slot = (s.k0 + j) * kTile + which * box;
-                    if (!mine || j >= n || slot >= s.q.length) return (int)a.num_pages;
-                    const int p = __ldg(table + slot / a.page_size);
+                    const int tile = s.k0 + j;
+                    if (!mine || j >= n || tile * kTile + which * box >= s.q.length)
+                        return (int)a.num_pages;
+                    const int p =
+                        __ldg(table + (per_page == 1 ? tile * boxes + which : tile / per_page));
                     return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
                 };
                 // this warp is some tiles ahead: the queries come to the L2 cache
@@ -405,7 +417,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     const int first_row = s.unit * kUnitRows;
                     for (int r = lane; r < s.rows; r += 32) {
                         const unsigned short* at = static_cast<const unsigned short*>(a.q) +
-                                                   query_row(a, s, first_row + r);
+                                                   query_row(args, s, first_row + r);
 #pragma unroll
                         for (int h = 0; h < S::kHalves; ++h) prefetch_l2(at + 64 * h);
                     }
@@ -429,7 +441,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                                  smem_addr(ring) + slot * S::kTileBytes + half * S::kHalfBytes +
                                      which * box * 128,
                                  &full[slot], half * 64,
-                                 ((s.k0 + j) * kTile + which * box) % a.page_size, s.head, page);
+                                 per_page == 1 ? 0 : (s.k0 + j) % per_page * kTile, s.head, page);
                     page = after;
                 }
                 items += 2 * n;
@@ -607,6 +619,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             const unsigned long long* mask =
                 reinterpret_cast<const unsigned long long*>(a.tree_mask) +
                 (here ? token : 0) * a.mask_words;
+            // asked for long before the tiles that need it
+            const uint64_t mask_word = here ? __ldg(mask) : 0;
 
             // this group's queries, rows of the unit, into swizzled shared memory
             if (s.pair || w == 0) {
@@ -620,7 +634,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 const unsigned short* from = static_cast<const unsigned short*>(a.q) + ch * 8;
 #pragma unroll 4
                 for (int r = row / kPer; r < rows; r += 128 / kPer)
-                    copy16(to + r * 128 + (((ch & 7) ^ (r & 7)) << 4), from + query_row(a, s, first_row + r));
+                    copy16(to + r * 128 + (((ch & 7) ^ (r & 7)) << 4), from + query_row(args, s, first_row + r));
                 copy16_wait();
                 if (args.flip != 0) {
                     for (int r = row / kPer; r < rows; r += 128 / kPer) {
@@ -652,7 +666,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     if (masked) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            bits[q] = here ? seen_bits(mask, a.mask_words, s.q.ctx, s.q.length,
+                            bits[q] = here ? seen_bits(mask, mask_word, a.mask_words, s.q.ctx, s.q.length,
                                                        first + 32 * q)
                                            : 0u;
                         __syncwarp();
@@ -824,7 +838,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                             // that see them: infinities and NaN
                             for (int slot = max(s.q.ctx, s.k0 * kTile);
                                  slot < min(s.q.length, s.k1 * kTile); ++slot) {
-                                if (!(seen_bits(mask, a.mask_words, s.q.ctx, s.q.length, slot) & 1))
+                                if (!(seen_bits(mask, mask_word, a.mask_words, s.q.ctx, s.q.length, slot) & 1))
                                     continue;
                                 const int64_t at = slot_offset(
                                     a.page_table, a.max_pages, a.page_size, a.num_pages,
@@ -964,7 +978,7 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
     }
     if (!live) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const uint32_t group = a.q_heads / a.kv_heads;
+    const uint32_t group = args.group;
     const uint32_t row = cut.w + local;
     const uint32_t node = row / group;
     const int64_t o = (cut.z + (int64_t)node) * a.q_heads + cut_head * group + row - node * group;
@@ -1071,6 +1085,7 @@ cudaError_t launch_tree_attention_tc(const ple_tree_attention_args& a, const Dev
     TcArgs args;
     args.a = a;
     args.blocks = tc_blocks(dev);
+    args.group = a.q_heads / a.kv_heads;
     args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads);
     // a scale of 0 as the least normal number: every exponent still rounds to 0,
     // and a hidden score stays -infinity
