@@ -13,11 +13,11 @@ namespace ple {
 namespace {
 
 constexpr int kTreeThreads = 256;
-// Blocks an SM that the tiled kernel's layer groups aim for.
-#ifndef PLE_TREE_BLOCKS_PER_SM
-#define PLE_TREE_BLOCKS_PER_SM 16
-#endif
-constexpr int kTreeBlocksPerSm = PLE_TREE_BLOCKS_PER_SM;
+// Blocks an SM that the tiled kernel's layer groups aim for.  Longer groups walk a
+// branch and divide for a head's reciprocal less often, more blocks hide those
+// better: 8065 nodes x 48 layers x 32 heads take 28.3 us at 2, 24.3 at 4, 20.4
+// at 8, 21.8 at 12 and 16 (99 MB written: 4.9 TB/s).
+constexpr int kTreeBlocksPerSm = 8;
 
 template <typename IdT>
 __global__ void __launch_bounds__(kTreeThreads)
@@ -84,10 +84,11 @@ __device__ __forceinline__ void store_row(OutT* p, int64_t v) {
 // layer each lane folds its node's mixes, one an order, into shared memory; then
 // the warp writes the tile's [nodes, H] row ids 32 at a time in global order,
 // one contiguous store a step, each lane hashing the row it stores.
+// The layer group's head constants are staged in shared memory by the block: a
+// reciprocal is a 64-bit division, worth sharing among the block's four tiles.
 // kLaneHeads: H divides 32 or is a multiple of it, so a lane meets one head for
 // all nodes (of 32 heads) and holds its constants in registers; otherwise the
-// head changes from step to step and the layer group's constants are staged in
-// shared memory by the block.
+// head changes from step to step.
 template <typename IdT, typename OutT, int NT, bool kLaneHeads>
 __global__ void __launch_bounds__(kTileWarps * 32, 8)
 tree_row_ids_tiled_kernel(const RowIdsParams p, const int32_t* __restrict__ parent) {
@@ -99,12 +100,9 @@ tree_row_ids_tiled_kernel(const RowIdsParams p, const int32_t* __restrict__ pare
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     extern __shared__ __align__(16) unsigned char smem[];
     wait_prior_grid();
-    SmemLayout sm{};
     uint2* mix_s = reinterpret_cast<uint2*>(smem + (size_t)warp * mix_bytes(N));
-    if constexpr (!kLaneHeads) {
-        sm = carve_smem(smem + kTileWarps * mix_bytes(N), p.group_layers, H, N, 0);
-        load_group_constants(p, sm, l0, gl, H, N);
-    }
+    const SmemLayout sm = carve_smem(smem + kTileWarps * mix_bytes(N), p.group_layers, H, N, 0);
+    load_group_constants(p, sm, l0, gl, H, N);
     const int64_t t0 = ((int64_t)blockIdx.x * kTileWarps + warp) * kTileRows;
     const int ntile = (int)max((int64_t)0, min((int64_t)kTileRows, p.T - t0));
     int64_t V[NMAX];
@@ -136,13 +134,16 @@ tree_row_ids_tiled_kernel(const RowIdsParams p, const int32_t* __restrict__ pare
             V[s] = valid ? w : p.boundary;
         }
     }
-    if constexpr (!kLaneHeads) __syncthreads();
+    __syncthreads();
     if (ntile == 0) return;
 
 #pragma unroll 1
     for (int l = 0; l < gl; ++l) {
         const int64_t layer = (int64_t)l0 + l;
-        const int64_t* ml = p.mult + layer * N;
+        const int64_t* ml = sm.mul + l * N;
+        const uint4* fasts = sm.fast + l * H;
+        const int64_t* offs = sm.off + l * H;
+        const uint4* exts = sm.ext + l * H;
         uint64_t mix = (uint64_t)V[0] * (uint64_t)ml[0];
 #pragma unroll
         for (int s = 1; s < NMAX; ++s) {
@@ -158,9 +159,7 @@ tree_row_ids_tiled_kernel(const RowIdsParams p, const int32_t* __restrict__ pare
             const int sub = H >= 32 ? 0 : lane / H;
 #pragma unroll 1
             for (int h = H >= 32 ? lane : lane % H; h < H; h += 32) {
-                const int64_t k = layer * H + h;
-                const HeadConst c = p.heads != nullptr ? load_head_const(p.heads, k)
-                                                       : make_head_const(p.vocab[k], p.offsets[k]);
+                const HeadConst c = {fasts[h], offs[h], exts[h]};
                 const uint2* m = mix_s + sub * pitch + h / p.hpn;
                 OutT* dst = out + sub * H + h;
                 const bool fast = c.ext.z == kHeadFast;
@@ -186,16 +185,13 @@ tree_row_ids_tiled_kernel(const RowIdsParams p, const int32_t* __restrict__ pare
         } else {
             const int dq = 32 / H, dr = 32 % H;
             int node = lane / H, h = lane % H;
-            const uint4* fast = sm.fast + l * H;
-            const int64_t* off = sm.off + l * H;
-            const uint4* ext = sm.ext + l * H;
 #pragma unroll 4
             for (int e = lane; e < ntile * H; e += 32) {
                 const uint2 w = mix_s[node * pitch + h / p.hpn];
                 const OffsetBinary u{w.x, w.y};
-                const uint4 x = ext[h];
-                store_row(out + e, x.z == kHeadFast ? row_fast(u, fast[h], off[h])
-                                                    : row_general(u, fast[h], off[h], x));
+                const uint4 x = exts[h];
+                store_row(out + e, x.z == kHeadFast ? row_fast(u, fasts[h], offs[h])
+                                                    : row_general(u, fasts[h], offs[h], x));
                 h += dr;
                 node += dq;
                 if (h >= H) {
@@ -246,12 +242,12 @@ cudaError_t launch_tree_row_ids(RowIdsParams p, const int32_t* parent, int id_by
     groups = groups < 1 ? 1 : groups > p.L ? p.L : groups;
     int64_t G = (p.L + groups - 1) / groups;
     const size_t per_layer = head_const_bytes(p.H) + 8 * (size_t)(p.N + 1);
-    if (!lane_heads && G > (int64_t)(kConstBudgetBytes / per_layer))
+    if (G > (int64_t)(kConstBudgetBytes / per_layer))
         G = kConstBudgetBytes / per_layer > 0 ? kConstBudgetBytes / per_layer : 1;
     if ((p.L + G - 1) / G > 65535) return cudaErrorInvalidConfiguration;
     p.group_layers = (int)G;
-    const size_t smem = kTileWarps * mix_bytes(p.N) +
-                        (lane_heads ? 0 : head_const_bytes((int)G * p.H) + ((size_t)G * p.N + 1) * 8);
+    const size_t smem = kTileWarps * mix_bytes(p.N) + head_const_bytes((int)G * p.H) +
+                        ((size_t)G * p.N + 1) * 8;
     TreeFn fn;
     if (p.out_bytes == 4)
         fn = id_bytes == 4 ? pick_tiled<int32_t, int32_t>(p.N, lane_heads)
