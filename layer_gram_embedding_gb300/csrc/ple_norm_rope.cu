@@ -30,13 +30,15 @@ namespace ple {
 namespace {
 
 constexpr int kNormThreads = 256;
-// Tokens a block, for batches that fill the device; resident blocks an SM.  What
-// hides the memory's latency is warps, not rows in flight in one of them: on the
-// 32004-token prompts 149 us with six blocks (40 registers a thread) and one row
-// ahead, 162 with four blocks and two or four rows ahead, 193 with seven blocks
-// (spills); four tokens a block 148, sixteen 173.
+// Tokens a block, for batches that fill the device; resident blocks an SM.  On the
+// 32004-token prompts (805 MB) 145 us with five blocks and eight tokens (5.55 TB/s);
+// four blocks 157, six 149, four tokens 148, sixteen 173.  Two to four rows in flight
+// a warp instead of one ahead measured no faster (153 to 157), and the kernel
+// with its arithmetic taken out, the copies alone, takes 138: what is left is how
+// fast rows of 256 bytes between the product's, the queries' and the pages' layouts
+// move at all.
 constexpr int kNormTokens = 8;
-constexpr int kNormBlocks = 6;
+constexpr int kNormBlocks = 5;
 constexpr int kMaxPairs = PLE_MAX_HEAD_DIM / 2;
 
 template <typename E>
@@ -98,8 +100,8 @@ struct Row {
 };
 __device__ __forceinline__ Row load_row(const unsigned short* p, int second) {
     Row r;
-    r.a = __ldcs(reinterpret_cast<const uint2*>(p));
-    r.b = __ldcs(reinterpret_cast<const uint2*>(p + second));
+    r.a = __ldcg(reinterpret_cast<const uint2*>(p));
+    r.b = __ldcg(reinterpret_cast<const uint2*>(p + second));
     return r;
 }
 __device__ __forceinline__ void store_row(unsigned short* p, int second, Row r) {
