@@ -331,7 +331,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     const ple_tree_attention_args& a = args.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
-    __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_full[2], pv_done[2];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_low[2], p_high[2], pv_done[2];
     __shared__ __align__(8) uint64_t last;
     // How often a slot was armed for a tile.  A barrier tells only the parity of
     // its phase, and neither copying warp sees every tile of a slot: before it
@@ -361,7 +361,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
         for (int w = 0; w < 2; ++w) {
             mbar_init(&q_full[w], 128);
             mbar_init(&s_full[w], 1);
-            mbar_init(&p_full[w], 4);
+            mbar_init(&p_low[w], 4);
+            mbar_init(&p_high[w], 4);
             mbar_init(&pv_done[w], 1);
             bad_s[w] = 0;
         }
@@ -490,23 +491,32 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 __syncwarp();
             };
-            auto values = [&](int w, uint32_t slot, bool accumulate, bool free) {
-                const uint64_t vd = operand_desc(ring_at + slot * S::kTileBytes, S::kHalfBytes);
+            // the product of half a tile's weights
+            auto values = [&](int w, uint32_t slot, int half, bool accumulate, bool free) {
+                const uint64_t vd = operand_desc(
+                    ring_at + slot * S::kTileBytes + half * (kTile / 2) * 128, S::kHalfBytes);
                 if (elected) {
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
+                    for (int k = 0; k < kTile / 32; ++k)
                         mma_tmem(tmem + w * S::kGroupColumns + S::kOut,
-                                 tmem + w * S::kGroupColumns + k * 8, vd + (k * 16 * 128 >> 4),
-                                 kOutWord, accumulate || k != 0);
+                                 tmem + w * S::kGroupColumns + half * (kTile / 4) + k * 8,
+                                 vd + (k * 16 * 128 >> 4), kOutWord, accumulate || k != 0);
                     mma_commit(&pv_done[w]);
                     if (free) mma_commit(&empty[slot]);
                 }
                 __syncwarp();
             };
-            auto wait_weights = [&](int w) -> bool {
-                const bool ok = mbar_wait(&p_full[w], p_count[w]++ & 1, failed);
+            // both halves, each behind its weights: the first runs while the second's
+            // weights are computed
+            auto product = [&](int w, uint32_t slot, bool accumulate, bool free) -> bool {
+                const uint32_t parity = p_count[w]++ & 1;
+                if (!mbar_wait(&p_low[w], parity, failed)) return false;
                 tmem_fence_after();
-                return ok;
+                values(w, slot, 0, accumulate, false);
+                if (!mbar_wait(&p_high[w], parity, failed)) return false;
+                tmem_fence_after();
+                values(w, slot, 1, true, free);
+                return true;
             };
             while (walk.next(s)) {
                 const int n = s.k1 - s.k0;
@@ -564,11 +574,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         const uint32_t v = wait_item(items + value_item(j, n));
                         if (more) k = wait_item(items + key_item(j + 1));
                         clean(j, v);
-                        if (!wait_weights(0)) break;
-                        values(0, v, j > 0, false);
+                        if (!product(0, v, j > 0, false)) break;
                         if (more) scores(0, k, 0, false);
-                        if (!wait_weights(1)) break;
-                        values(1, v, j > 0, true);
+                        if (!product(1, v, j > 0, true)) break;
                         if (more) scores(1, k, 1, true);
                     }
                 } else {
@@ -578,8 +586,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         const int w = j & 1;
                         const uint32_t v = wait_item(items + value_item(j, n));
                         clean(j, v);
-                        if (!wait_weights(w)) break;
-                        values(w, v, j > 1, true);
+                        if (!product(w, v, j > 1, true)) break;
                         if (j + 2 < n) scores(w, wait_item(items + key_item(j + 2)), 0, true);
                     }
                 }
@@ -604,7 +611,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
         const uint32_t s_at = tmem + w * S::kGroupColumns + lanes;
         const uint32_t o_at = s_at + S::kOut;
         const float c = args.c;
-        uint32_t seg = 0, count = 0;
+        uint32_t seg = 0, count = 0, parts = 0;
         Cut cut = {};
         cut.last = -1;
         while (walk.next(s)) {
@@ -706,7 +713,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         if (move) top = m;
                         sum *= f;
                         if (begun) {
-                            mbar_wait(&pv_done[w], (count - 1) & 1, failed);
+                            mbar_wait(&pv_done[w], (parts - 1) & 1, failed);
                             tmem_fence_after();
 #pragma unroll 1
                             for (int q = 0; q < D / 32; ++q) {
@@ -745,6 +752,12 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                         // over columns whose scores have been read
                         tmem_store(s_at + 16 * q, p);
+                        if (q == 1) {
+                            tmem_wait_store();
+                            tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_low[w]);
+                        }
                     }
                     float p0, p1;
                     unpack_f32(add_f32x2(part[0], part[1]), p0, p1);
@@ -753,11 +766,20 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[w]);
+                if (lane == 0) {
+                    if (!active) mbar_arrive(&p_low[w]);
+                    mbar_arrive(&p_high[w]);
+                }
                 begun = true;
+                parts += 2;
                 ++count;
             }
-            if (begun) mbar_wait(&pv_done[w], (count - 1) & 1, failed);
+            if (begun) {
+                // the last two half tiles' products may both be under way, and a
+                // barrier tells only the parity of its phase: one after the other
+                mbar_wait(&pv_done[w], (parts - 2) & 1, failed);
+                mbar_wait(&pv_done[w], (parts - 1) & 1, failed);
+            }
             tmem_fence_after();
 
             // ------------------------------------ the segment's rows go out
