@@ -501,7 +501,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         mma_tmem(tmem + w * S::kGroupColumns + S::kOut,
                                  tmem + w * S::kGroupColumns + half * (kTile / 4) + k * 8,
                                  vd + (k * 16 * 128 >> 4), kOutWord, accumulate || k != 0);
-                    mma_commit(&pv_done[w]);
+                    if (half == 1) mma_commit(&pv_done[w]);
                     if (free) mma_commit(&empty[slot]);
                 }
                 __syncwarp();
@@ -611,7 +611,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
         const uint32_t s_at = tmem + w * S::kGroupColumns + lanes;
         const uint32_t o_at = s_at + S::kOut;
         const float c = args.c;
-        uint32_t seg = 0, count = 0, parts = 0;
+        uint32_t seg = 0, count = 0;
         Cut cut = {};
         cut.last = -1;
         while (walk.next(s)) {
@@ -665,10 +665,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 if (active) {
                     const int first = (s.k0 + j) * kTile;
                     const bool masked = first + kTile > s.q.ctx;
-                    // The row's scores are read twice, 32 columns at a time and
-                    // the next ones on their way: for the maximum, then for
-                    // the weights.  Keeping all 128 between would not leave
-                    // registers for the rest.
+                    // The row's scores are walked twice, 64 columns at a time: the
+                    // upper half and then the lower for the maximum, the lower, still in
+                    // registers, and the upper again for the weights.  All 128 would
+                    // not leave registers for the rest.
                     uint32_t bits[4];
                     if (masked) {
 #pragma unroll
@@ -687,23 +687,26 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     };
                     uint32_t v[2][32];
                     float m = -INFINITY;
-                    tmem_load(s_at, v[0]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t(&x)[32] = v[q & 1];
-                        tmem_wait_load(x);
-                        tmem_load(s_at + 32 * ((q + 1) & 3), v[(q + 1) & 1]);
-                        hide(x, q);
-                        float m0 = max3(m, as_float(x[0]), as_float(x[1]));
-                        float m1 = fmaxf(as_float(x[2]), as_float(x[3]));
+                    for (int h = 1; h >= 0; --h) {
+                        float m0, m1;
+                        tmem_load_max(s_at + 64 * h, v[0], m0);
+                        tmem_load_max(s_at + 64 * h + 32, v[1], m1);
+                        tmem_wait_load(v[0]);
+                        tmem_settle(v[0], m0);
+                        tmem_settle(v[1], m1);
+                        if (masked) {
+                            hide(v[0], 2 * h);
+                            hide(v[1], 2 * h + 1);
+                            m0 = m1 = -INFINITY;
 #pragma unroll
-                        for (int i = 4; i < 32; i += 4) {
-                            m0 = max3(m0, as_float(x[i]), as_float(x[i + 1]));
-                            m1 = max3(m1, as_float(x[i + 2]), as_float(x[i + 3]));
+                            for (int i = 0; i < 32; i += 2) {
+                                m0 = max3(m0, as_float(v[0][i]), as_float(v[0][i + 1]));
+                                m1 = max3(m1, as_float(v[1][i]), as_float(v[1][i + 1]));
+                            }
                         }
-                        m = fmaxf(m0, m1);
+                        m = max3(m, m0, m1);
                     }
-                    tmem_wait_load(v[0]);  // the first quarter again
                     // a new maximum only where it grew by more than kLag
                     const bool grow = here && (m - top) * c > kLag;
                     const bool set = here && top == -INFINITY && m > -INFINITY;
@@ -713,7 +716,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         if (move) top = m;
                         sum *= f;
                         if (begun) {
-                            mbar_wait(&pv_done[w], (parts - 1) & 1, failed);
+                            mbar_wait(&pv_done[w], (count - 1) & 1, failed);
                             tmem_fence_after();
 #pragma unroll 1
                             for (int q = 0; q < D / 32; ++q) {
@@ -735,9 +738,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t(&x)[32] = v[q & 1];
-                        if (q > 0) tmem_wait_load(x);
-                        if (q < 3) tmem_load(s_at + 32 * (q + 1), v[(q + 1) & 1]);
-                        hide(x, q);
+                        if (q > 1) {
+                            tmem_wait_load(x);
+                            hide(x, q);
+                        }
                         uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -750,6 +754,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                             part[i & 1] = add_f32x2(part[i & 1], pack_f32(x0, x1));
                             p[i] = round_pair<kBf16>(x0, x1);
                         }
+                        if (q < 2) tmem_load(s_at + 32 * (q + 2), x);
                         // over columns whose scores have been read
                         tmem_store(s_at + 16 * q, p);
                         if (q == 1) {
@@ -771,15 +776,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     mbar_arrive(&p_high[w]);
                 }
                 begun = true;
-                parts += 2;
                 ++count;
             }
-            if (begun) {
-                // the last two half tiles' products may both be under way, and a
-                // barrier tells only the parity of its phase: one after the other
-                mbar_wait(&pv_done[w], (parts - 2) & 1, failed);
-                mbar_wait(&pv_done[w], (parts - 1) & 1, failed);
-            }
+            if (begun) mbar_wait(&pv_done[w], (count - 1) & 1, failed);
             tmem_fence_after();
 
             // ------------------------------------ the segment's rows go out

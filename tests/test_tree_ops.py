@@ -335,7 +335,12 @@ def test_append_outside_the_page_table_is_dropped():
 # ------------------------------------------------------------------ attention
 
 
-def check_attention(q, cache, ctx, cu, masks, scale=None, what="", workspace=None, sanitize=False):
+def host_attention(q, cache, ctx, cu, masks, scale):
+    return ref.attention(host(q), host(cache.k), host(cache.v), cache.table, ctx, cu, masks, scale)
+
+
+def check_attention(q, cache, ctx, cu, masks, scale=None, what="", workspace=None, sanitize=False,
+                    reference=host_attention):
     """The call against the reference.  Errors: the output's rounding u |o|; the weights' rounding and the 32-bit scores'
     error (D + 8 roundings of the products' sum, and a few of the exponent) on sum p |v|."""
     scale = q.shape[-1] ** -0.5 if scale is None else scale
@@ -343,8 +348,7 @@ def check_attention(q, cache, ctx, cu, masks, scale=None, what="", workspace=Non
     out, lse = ple.ple_tree_attention(q, cache.k, cache.v, dev(cache.table), dev(ctx), dev(cu),
                                       dev(masks), scale=scale, return_lse=True,
                                       workspace=workspace)
-    want, want_lse, weight, reach = ref.attention(host(q), host(cache.k), host(cache.v),
-                                                  cache.table, ctx, cu, masks, scale)
+    want, want_lse, weight, reach = reference(q, cache, ctx, cu, masks, scale)
     D = q.shape[-1]
     score = 2.0 ** -24 * (D + 8) * reach + 2.0 ** -20
     bound = u * (1 + 2.0 ** -8) * np.abs(want) + (u + 2 * score[..., None]) * weight + 2.0 ** -25
@@ -422,6 +426,75 @@ def test_attention_is_the_same_every_time(D):
     for _ in range(3):
         again = check_attention(q, cache, ctx, cu, masks)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def dense_attention(q, cache, ctx, cu, masks, scale):
+    """The reference in 64 bits on the device, a request at a time: for sizes the host is too slow for."""
+    T, Hq, D = q.shape
+    Hk = cache.k.shape[1]
+    out = torch.zeros((T, Hq, D), dtype=torch.float64, device=DEV)
+    weight, lse = out.clone(), torch.full((T, Hq), -np.inf, dtype=torch.float64, device=DEV)
+    reach = torch.zeros((T, Hq), dtype=torch.float64, device=DEV)
+    for r in range(len(cu) - 1):
+        n, first = int(cu[r + 1] - cu[r]), int(cu[r])
+        if n == 0:
+            continue
+        length = int(ctx[r]) + n
+        at = np.arange(length)
+        p, s = dev(cache.table[r][at // cache.page].astype(np.int64)), dev(at % cache.page)
+        k, v = (c[p, :, s].double().transpose(0, 1) for c in (cache.k, cache.v))  # [Hk, length, D]
+        bits = (dev(masks[first:first + n])[:, :, None] >> torch.arange(64, device=DEV)) & 1
+        sees = torch.ones((n, length), dtype=torch.bool, device=DEV)
+        sees[:, int(ctx[r]):] = bits.reshape(n, -1)[:, :n].bool()
+        x = q[first:first + n].double().reshape(n, Hk, Hq // Hk, D).permute(1, 2, 0, 3)
+        score = (x @ k[:, None].transpose(2, 3)) * scale
+        score = score.masked_fill(~sees, -np.inf)
+        p = torch.softmax(score, -1)
+
+        def back(t):
+            return t.permute(2, 0, 1, 3).reshape(n, Hq, -1)
+
+        out[first:first + n] = back(p @ v[:, None])
+        weight[first:first + n] = back(p @ v[:, None].abs())
+        lse[first:first + n] = back(torch.logsumexp(score, -1, keepdim=True))[..., 0]
+        reach[first:first + n] = back((x.abs() @ k[:, None].abs().transpose(2, 3))
+                                      .amax(-1, keepdim=True))[..., 0] * abs(scale)
+    return tuple(t.cpu().numpy() for t in (out, lse, weight, reach))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_random_batches(seed):
+    rng = np.random.default_rng(1000 + seed)
+    D = int(rng.choice([64, 128]))
+    page = int(rng.choice([8, 16, 32, 64, 128, 256, 384]))
+    dtype = [torch.bfloat16, torch.float16][seed % 2]
+    Hk = int(rng.choice([1, 2, 4, 8]))
+    Hq = Hk * int(rng.choice([1, 2, 3, 4, 7, 8, 16]))
+    B = int(rng.integers(1, 40))
+    most = int(rng.choice([1, 3, 17, 64, 90, 200]))
+    counts = [int(rng.integers(0 if B > 1 else 1, most + 1)) for _ in range(B)]
+    counts[0] = max(counts[0], 1)
+    room = max(1, int(3e6 / max(sum(counts) * Hq, 1) * B))  # scores of the reference
+    ctx = [int(rng.integers(0, min(room, 9000) + 1)) for _ in range(B)]
+    q, cache, ctx, cu, masks = attention_inputs(rng, counts, ctx, Hq, Hk, D, page, dtype,
+                                                str(rng.choice(["phsd", "pshd"])))
+    first = check_attention(q, cache, ctx, cu, masks, what=str((counts, ctx, Hq, Hk, D, page)),
+                            reference=dense_attention)
+    for _ in range(20):  # nothing depends on timing
+        again = ple.ple_tree_attention(q, cache.k, cache.v, dev(cache.table), dev(ctx), dev(cu),
+                                       dev(masks), return_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_attention_many_short_units_again_and_again():
+    # blocks with several units of a few tiles each, 300 times
+    rng = np.random.default_rng(16)
+    q, cache, ctx, cu, masks = attention_inputs(rng, [2] * 40, [100 + 19 * i for i in range(40)],
+                                                16, 8, 128, 16, torch.bfloat16)
+    args = (q, cache.k, cache.v, dev(cache.table), dev(ctx), dev(cu), dev(masks))
+    first = ple.ple_tree_attention(*args)
+    for _ in range(300):
+        assert torch.equal(ple.ple_tree_attention(*args), first)
 
 
 @pytest.mark.parametrize("D", [64, 128, 96])
