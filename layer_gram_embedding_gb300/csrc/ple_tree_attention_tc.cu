@@ -924,15 +924,16 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
 
 constexpr int kJoinThreads = 128;
 constexpr int kJoinRows = kJoinThreads / 16;  // rows a block
+constexpr int kJoinAhead = 8;
 
 // The cut units' rows: for a row, the states of the blocks that share its unit,
 // in block order.  The first grid dimension is the block that started a unit, the
 // second its rows.  Sixteen lanes take a row: they read up to 16 states' pairs at
-// once, then every lane D / 16 accumulators of each state, four states' loads
-// in flight (a unit is mostly cut into two or three).  The work is a few bytes
+// once, then every lane D / 16 accumulators of each state, kJoinAhead
+// states' loads in flight.  The work is a few bytes
 // a row behind three dependent reads, so it is spread thin and wide.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads, 8)
+__global__ void __launch_bounds__(kJoinThreads)
 tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
     constexpr int E = D / 16;
     const ple_tree_attention_args& a = args.a;
@@ -969,10 +970,10 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
         for (int e = 0; e < E; ++e) acc[e] *= keep;
         const int n = min(16, c1 - from + 1);
         const int at = 2 * args.rows_cap + ((lane * E / 8) * args.rows_cap + local) * 8 + lane * E % 8;
-        for (int i0 = 0; i0 < n; i0 += 4) {
-            float4 x[4][E / 4];
+        for (int i0 = 0; i0 < n; i0 += kJoinAhead) {
+            float4 x[kJoinAhead][E / 4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kJoinAhead; ++i) {
                 if (i0 + i < n && live) {
                     const float* theirs =
                         space + at +
@@ -983,7 +984,7 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kJoinAhead; ++i) {
                 const float g = __shfl_sync(0xffffffffu, f, (i0 + i) & 15, 16);
                 if (i0 + i < n && live) {
 #pragma unroll
