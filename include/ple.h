@@ -604,7 +604,7 @@ typedef struct {
 } ple_tree_attention_args;
 
 /* Errors: PLE_ERR_SIZE, PLE_ERR_ELEMENT, PLE_ERR_NULL, PLE_ERR_ALIGN,
- * PLE_ERR_CUDA.  Two kernel launches. */
+ * PLE_ERR_CUDA.  At most two kernel launches. */
 ple_status ple_tree_attention(const ple_tree_attention_args* args, void* stream);
 
 /* The workspace that a call on the current device needs, in bytes, or -1 when

@@ -20,9 +20,10 @@
 // they take the tiles in turn over the same rows and are joined in shared memory.
 // Either way one group's softmax runs while the tensor cores work for the other.
 //
-// Split.  All tiles of all (request, key head, 256 rows) are laid end to end
-// and cut into equal shares, one a block, so ragged requests and few long ones
-// fill the device alike.  A block writes a unit that it has whole; of a cut
+// Split.  All tiles of all (request, key head, 256 rows) are laid end to end, each
+// unit behind a few places for what it costs besides its tiles, and cut into equal
+// shares, one a block, so ragged requests and few long ones fill the device
+// alike.  A block writes a unit that it has whole; of a cut
 // unit it writes the state (row maximum, sum, O in 32 bits) to the workspace,
 // and a second kernel joins the states in block order: results do not depend
 // on timing.
@@ -79,9 +80,15 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// One request's tiles.
+// What a unit costs besides its tiles (queries in, rows out), in tiles.  Without it
+// the share with the most short units ends last: 32 ragged requests of 17 to 32749
+// slots take 380 us at 0, 352 at 2, 346 at 4, 344 at 6, 345 at 8.
+constexpr int kUnitCost = 6;
+
+// One request's work, in tiles: that of all its units, kUnitCost each ahead of
+// their tiles.
 struct Request {
-    int64_t work;            // tiles of all its units
+    int64_t work;
     int32_t begin, nodes;
     int32_t ctx, length;     // cached slots all rows see; slots with the nodes'
     int32_t tiles, units;    // key tiles of a unit; units a key head
@@ -100,11 +107,11 @@ __device__ __forceinline__ Request request_of(const TcArgs& args, int r) {
     q.tiles = (q.length + kTile - 1) / kTile;
     const int64_t rows = (int64_t)q.nodes * args.group;
     q.units = (int32_t)((rows + kUnitRows - 1) / kUnitRows);
-    q.work = (int64_t)q.units * q.tiles * a.kv_heads;
+    q.work = (int64_t)q.units * (q.tiles + kUnitCost) * a.kv_heads;
     return q;
 }
 
-// First tile of share c of `shares`, and the share of a tile.
+// Where share c of `shares` begins, and the share of a place.
 __device__ __forceinline__ int64_t share_begin(int64_t total, int c, int shares) {
     return quotient(total * c, shares);
 }
@@ -112,8 +119,8 @@ __device__ __forceinline__ int share_of(int64_t total, int64_t tile, int shares)
     return (int)quotient((tile + 1) * shares - 1, total);
 }
 
-// A block's tiles [lo, hi) of `total`, the request that owns the first one, and
-// the tiles before that request.  Not more shares than tiles.
+// A block's part [lo, hi) of the work `total`, the request that owns its first
+// place, and the work before that request.  No share is empty.
 struct Share {
     int64_t lo, hi, total, before;
     int32_t first, shares;
@@ -187,8 +194,8 @@ struct Segment {
 // The block's segments in order; every role walks them alike.
 struct Walk {
     const TcArgs& args;
-    int64_t at, end;     // tiles still to do
-    int64_t base;        // tiles before request r
+    int64_t at, end;     // what is still to do
+    int64_t base;        // the work before request r
     int r;
     Request q;
     __device__ __forceinline__ Walk(const TcArgs& the, const Share& share)
@@ -196,23 +203,29 @@ struct Walk {
         if (at < end) q = request_of(args, r);
     }
     __device__ __forceinline__ bool next(Segment& s) {
-        if (at >= end) return false;
-        while (at >= base + q.work) {
-            base += q.work;
-            q = request_of(args, ++r);
+        while (at < end) {
+            while (at >= base + q.work) {
+                base += q.work;
+                q = request_of(args, ++r);
+            }
+            const int32_t span = q.tiles + kUnitCost;
+            const int64_t rel = at - base;
+            const int32_t u = (int32_t)quotient(rel, span);
+            const int32_t from = (int32_t)(rel - (int64_t)u * span);
+            const int32_t upto = (int32_t)min((int64_t)span, from + (end - at));
+            at += upto - from;
+            if (upto <= kUnitCost) continue;  // its first tile is the next share's
+            s.q = q;
+            s.k0 = max(from - kUnitCost, 0);
+            s.k1 = upto - kUnitCost;
+            s.head = u / q.units;
+            s.unit = u - s.head * q.units;
+            s.rows = (int32_t)min((int64_t)kUnitRows, (int64_t)q.nodes * args.group -
+                                                         (int64_t)s.unit * kUnitRows);
+            s.pair = s.rows > kTile;
+            return true;
         }
-        const int64_t rel = at - base;
-        const int32_t u = (int32_t)quotient(rel, q.tiles);
-        s.q = q;
-        s.k0 = (int32_t)(rel - (int64_t)u * q.tiles);
-        s.k1 = (int32_t)min((int64_t)q.tiles, s.k0 + (end - at));
-        s.head = u / q.units;
-        s.unit = u - s.head * q.units;
-        s.rows = (int32_t)min((int64_t)kUnitRows, (int64_t)q.nodes * args.group -
-                                                     (int64_t)s.unit * kUnitRows);
-        s.pair = s.rows > kTile;
-        at += s.k1 - s.k0;
-        return true;
+        return false;
     }
 };
 

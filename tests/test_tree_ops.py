@@ -405,6 +405,10 @@ ATTENTION_CASES = [
     ([40, 64, 33], [2500, 900, 3000], 32, 4, 64, 32, "phsd"),
     ([18], [9001], 32, 4, 128, 64, "phsd"),
     ([1, 1], [20000, 11], 4, 2, 128, 128, "phsd"),
+    # widths and page sizes of the other kernel: split slots, more heads than a block takes
+    ([1, 3], [5000, 0], 20, 2, 256, 16, "phsd"),
+    ([1], [3001], 3, 1, 128, 24, "pshd"),
+    ([60, 70], [90, 300], 8, 8, 80, 16, "phsd"),
 ]
 
 
