@@ -108,6 +108,9 @@ __device__ __forceinline__ void copy_box(const CUtensorMap* map, uint32_t dst, u
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void zero16(uint32_t dst) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+}
 __device__ __forceinline__ void copy16_wait() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }

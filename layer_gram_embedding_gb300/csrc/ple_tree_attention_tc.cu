@@ -1,5 +1,6 @@
 // Attention of drafted nodes over the paged cache and their own branch, on the
-// tensor cores of sm_103a, for head widths 64 and 128.
+// tensor cores of sm_103a, for heads of up to 128 elements (narrower ones are filled up with
+// zeros to 64 or 128 in shared memory).
 //
 // Rows.  The query heads of one key head share its keys, so for a request of n
 // nodes and G = q_heads / kv_heads a key head has n * G rows (node-major).  A
@@ -229,6 +230,12 @@ struct Walk {
     }
 };
 
+// Slots a box: the largest power of two that cuts pages and tiles evenly.
+__host__ __device__ __forceinline__ int page_box(int page_size) {
+    const int two = page_size & -page_size;
+    return two < kTile ? two : kTile;
+}
+
 // The offset of the query of a key head's row.
 __device__ __forceinline__ int64_t query_row(const TcArgs& args, const Segment& s, int row) {
     const ple_tree_attention_args& a = args.a;
@@ -405,10 +412,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             // ------------------------------------------------------- copies
             const bool keys = warp == kKeyWarp;
             const CUtensorMap* map = keys ? &k_map : &v_map;
-            // a tile is `boxes` whole pages, or one of `per_page` tiles of a page
-            const int box = min(a.page_size, kTile);
+            // a tile is `boxes` boxes of slots, each in one page
+            const int box = page_box(a.page_size);
             const int boxes = kTile / box;
-            const int per_page = a.page_size / box;
             const int which = lane / S::kHalves, half = lane % S::kHalves;
             const bool mine = which < boxes;
             uint32_t items = 0;
@@ -418,11 +424,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 // a box past the tokens, or of a page outside the cache, is filled
                 // with zeros: its page number is outside the map
                 auto page_of = [&](int j) -> int {
-                    const int tile = s.k0 + j;
-                    if (!mine || j >= n || tile * kTile + which * box >= s.q.length)
-                        return (int)a.num_pages;
-                    const int p =
-                        __ldg(table + (per_page == 1 ? tile * boxes + which : tile / per_page));
+                    const int slot = (s.k0 + j) * kTile + which * box;
+                    if (!mine || j >= n || slot >= s.q.length) return (int)a.num_pages;
+                    const int p = __ldg(table + (box == a.page_size ? (s.k0 + j) * boxes + which
+                                                                    : slot / a.page_size));
                     return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
                 };
                 // this warp is some tiles ahead: the queries come to the L2 cache
@@ -433,7 +438,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         const unsigned short* at = static_cast<const unsigned short*>(a.q) +
                                                    query_row(args, s, first_row + r);
 #pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h) prefetch_l2(at + 64 * h);
+                        for (int h = 0; h < S::kHalves; ++h)
+                            if (64 * h < a.head_dim) prefetch_l2(at + 64 * h);
                     }
                 }
                 int page = page_of(0);
@@ -455,7 +461,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                                  smem_addr(ring) + slot * S::kTileBytes + half * S::kHalfBytes +
                                      which * box * 128,
                                  &full[slot], half * 64,
-                                 per_page == 1 ? 0 : (s.k0 + j) % per_page * kTile, s.head, page);
+                                 box == a.page_size
+                                     ? 0
+                                     : ((s.k0 + j) * kTile + which * box) % a.page_size,
+                                 s.head, page);
                     page = after;
                 }
                 items += 2 * n;
@@ -653,8 +662,13 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 const uint32_t to = smem_addr(tile) + (ch / 8) * S::kHalfBytes;
                 const unsigned short* from = static_cast<const unsigned short*>(a.q) + ch * 8;
 #pragma unroll 4
-                for (int r = row / kPer; r < rows; r += 128 / kPer)
-                    copy16(to + r * 128 + (((ch & 7) ^ (r & 7)) << 4), from + query_row(args, s, first_row + r));
+                for (int r = row / kPer; r < rows; r += 128 / kPer) {
+                    const uint32_t dst = to + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                    if (ch * 8 < a.head_dim)
+                        copy16(dst, from + query_row(args, s, first_row + r));
+                    else  // columns past a narrower head's
+                        zero16(dst);
+                }
                 copy16_wait();
                 if (args.flip != 0) {
                     for (int r = row / kPer; r < rows; r += 128 / kPer) {
@@ -883,6 +897,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                                     s.head * a.head_stride + 32 * q;
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) {
+                                    if (32 * q + i >= a.head_dim) break;
                                     const float e = widen16<kBf16>(vrow[i]);
                                     if (!isfinite(e)) x[i] += e;
                                 }
@@ -890,9 +905,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                         if (here && whole) {
                             uint4* dst = reinterpret_cast<uint4*>(
-                                static_cast<unsigned short*>(a.out) + o_row * D + 32 * q);
+                                static_cast<unsigned short*>(a.out) + o_row * a.head_dim + 32 * q);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
+                                if (32 * q + 8 * i >= a.head_dim) break;
                                 uint32_t y[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
@@ -1021,12 +1037,15 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll
     for (int e = 0; e < E / 2; ++e)
         y[e] = round_pair<kBf16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned short*>(a.out) + o * D) +
-                    lane * (E / 2);
-    if constexpr (E == 8)
-        *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-    else
-        *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    uint32_t* dst =
+        reinterpret_cast<uint32_t*>(static_cast<unsigned short*>(a.out) + o * a.head_dim) +
+        lane * (E / 2);
+    if (lane * E < a.head_dim) {
+        if constexpr (E == 8)
+            *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+        else
+            *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    }
     if (lane == 0 && a.lse != nullptr)
         a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
 }
@@ -1049,8 +1068,9 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// A cache as a map of (element, slot, head, page); boxes of 64 elements by one
-// page's (or 128) slots.  Pages outside read as zeros.
+// A cache as a map of (element, slot, head, page); boxes of 64 elements by the
+// slots of page_box.  Pages outside read as zeros, and so do elements past a head
+// narrower than the tile.
 bool encode_cache(CUtensorMap* map, const ple_tree_attention_args& a, const void* cache) {
     const EncodeTiled fn = encode_tiled();
     if (fn == nullptr) return false;
@@ -1062,7 +1082,7 @@ bool encode_cache(CUtensorMap* map, const ple_tree_attention_args& a, const void
     const cuuint64_t strides[3] = {stride(a.slot_stride, a.page_size),
                                    stride(a.head_stride, a.kv_heads),
                                    stride(a.page_stride, a.num_pages)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(a.page_size < kTile ? a.page_size : kTile), 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)page_box(a.page_size), 1, 1};
     const cuuint32_t ones[4] = {1, 1, 1, 1};
     return fn(map,
               a.dtype == PLE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -1102,13 +1122,13 @@ cudaError_t launch_tc(const TcArgs& args, const CUtensorMap& k, const CUtensorMa
 
 int64_t tree_attention_tc_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D,
                                     const DeviceFacts& dev) {
-    return 4 * state_at(tc_blocks(dev), 0, tc_rows_cap(T, q_heads, kv_heads), D);
+    return 4 * state_at(tc_blocks(dev), 0, tc_rows_cap(T, q_heads, kv_heads), D <= 64 ? 64 : 128);
 }
 
-// The shapes whose tiles are whole boxes of whole swizzle atoms.
+// Heads up to the widest tile, and pages that boxes of whole swizzle atoms (8
+// slots) cut evenly.
 bool tree_attention_tc_fits(const ple_tree_attention_args& a) {
-    return (a.head_dim == 64 || a.head_dim == 128) && a.page_size % 8 == 0 &&
-           (kTile % a.page_size == 0 || a.page_size % kTile == 0);
+    return a.head_dim <= 128 && a.page_size % 8 == 0;
 }
 
 // *taken: whether the tensor maps take the caches' strides (else nothing ran).
@@ -1126,7 +1146,7 @@ cudaError_t launch_tree_attention_tc(const ple_tree_attention_args& a, const Dev
     // and a hidden score stays -infinity
     args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     args.flip = a.scale < 0 ? 0x80008000u : 0u;
-    if (a.head_dim == 64)
+    if (a.head_dim <= 64)
         return a.dtype == PLE_BF16 ? launch_tc<64, true>(args, k, v, stream)
                                    : launch_tc<64, false>(args, k, v, stream);
     return a.dtype == PLE_BF16 ? launch_tc<128, true>(args, k, v, stream)

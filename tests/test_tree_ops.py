@@ -407,7 +407,10 @@ ATTENTION_CASES = [
     ([1, 1], [20000, 11], 4, 2, 128, 128, "phsd"),
     # widths and page sizes of the other kernel: split slots, more heads than a block takes
     ([1, 3], [5000, 0], 20, 2, 256, 16, "phsd"),
-    ([1], [3001], 3, 1, 128, 24, "pshd"),
+    ([1], [3001], 3, 1, 128, 20, "pshd"),
+    ([1, 40], [3001, 129], 6, 2, 128, 24, "pshd"),
+    ([33, 2], [500, 1000], 8, 2, 120, 40, "phsd"),
+    ([9, 9], [1000, 20], 4, 1, 40, 384, "phsd"),
     ([60, 70], [90, 300], 8, 8, 80, 16, "phsd"),
 ]
 
@@ -421,7 +424,7 @@ def test_tree_attention(case, dtype):
     check_attention(q, cache, ctx, cu, masks, what=str(case))
 
 
-@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("D", [64, 128, 96, 160])
 def test_attention_is_the_same_every_time(D):
     rng = np.random.default_rng(8)
     q, cache, ctx, cu, masks = attention_inputs(rng, [20, 3, 64], [900, 2000, 31], 8, 2, D, 16,
@@ -469,8 +472,8 @@ def dense_attention(q, cache, ctx, cu, masks, scale):
 @pytest.mark.parametrize("seed", range(24))
 def test_attention_random_batches(seed):
     rng = np.random.default_rng(1000 + seed)
-    D = int(rng.choice([64, 128]))
-    page = int(rng.choice([8, 16, 32, 64, 128, 256, 384]))
+    D = int(rng.choice([64, 128, 128, 96, 72, 32]))
+    page = int(rng.choice([8, 16, 32, 64, 128, 256, 384, 24, 80]))
     dtype = [torch.bfloat16, torch.float16][seed % 2]
     Hk = int(rng.choice([1, 2, 4, 8]))
     Hq = Hk * int(rng.choice([1, 2, 3, 4, 7, 8, 16]))
@@ -501,7 +504,7 @@ def test_attention_many_short_units_again_and_again():
         assert torch.equal(ple.ple_tree_attention(*args), first)
 
 
-@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("D", [64, 128, 96, 160])
 def test_attention_large_scores(D):
     # a softmax of few weights, whose running maximum moves often and far
     rng = np.random.default_rng(9)
@@ -514,7 +517,7 @@ def test_attention_large_scores(D):
     check_attention(q, cache, ctx, cu, masks)
 
 
-@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("D", [64, 128, 96, 160])
 def test_nodes_that_see_nothing(D):
     rng = np.random.default_rng(4)
     q, cache, ctx, cu, masks = attention_inputs(rng, [6, 5, 70], [0, 40, 0], 4, 2, D, 16,
@@ -526,7 +529,7 @@ def test_nodes_that_see_nothing(D):
         assert torch.all(out[t] == 0) and torch.all(lse[t] == float("-inf"))
 
 
-@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("D", [64, 128, 96, 160])
 def test_nothing_unseen_has_an_effect(D):
     # nodes no row sees hold NaN; a node that some rows see holds infinities, which reach those rows alone
     rng = np.random.default_rng(6)
@@ -552,7 +555,7 @@ def test_nothing_unseen_has_an_effect(D):
 
 
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0])
-@pytest.mark.parametrize("D", [64, 96])
+@pytest.mark.parametrize("D", [64, 96, 160])
 def test_attention_scales(D, scale):
     rng = np.random.default_rng(19)
     q, cache, ctx, cu, masks = attention_inputs(rng, [5, 70], [200, 31], 4, 2, D, 16,
@@ -573,7 +576,7 @@ def test_attention_masks_bits_past_the_nodes_are_ignored():
     assert all(torch.equal(a, b) for a, b in zip(out, plain))
 
 
-@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("D", [64, 128, 96, 160])
 def test_attention_pages_outside_the_cache_read_as_zeros(D):
     rng = np.random.default_rng(13)
     q, cache, ctx, cu, masks = attention_inputs(rng, [4], [60], 4, 2, D, 16, torch.bfloat16)
