@@ -1,6 +1,6 @@
 // Attention of drafted nodes over the paged cache and their own branch, on the
-// tensor cores of sm_103a, for heads of up to 128 elements (narrower ones are filled up with
-// zeros to 64 or 128 in shared memory).
+// tensor cores of sm_103a, for heads of up to 128 elements (narrower ones are filled
+// up with zeros to 64 or 128 in shared memory).
 //
 // Rows.  The query heads of one key head share its keys, so for a request of n
 // nodes and G = q_heads / kv_heads a key head has n * G rows (node-major).  A
@@ -24,10 +24,17 @@
 // Split.  All tiles of all (request, key head, 256 rows) are laid end to end, each
 // unit behind a few places for what it costs besides its tiles, and cut into equal
 // shares, one a block, so ragged requests and few long ones fill the device
-// alike.  A block writes a unit that it has whole; of a cut
-// unit it writes the state (row maximum, sum, O in 32 bits) to the workspace,
-// and a second kernel joins the states in block order: results do not depend
-// on timing.
+// alike.  A block writes a unit that it has whole; of a cut unit it writes the
+// state (row maximum, sum, O in 32 bits) to the workspace, and a second kernel
+// joins the states in block order: results do not depend on timing.
+//
+// Measured (bf16, heads of 128, 8 key heads, 64-slot pages, the join with it).  Up
+// to 128 rows a unit the keys' and values' bytes bound it: 4 rows over 32 x 16384
+// slots 316 us (6.8 TB/s), 128 rows 335 us.  Above, the chain of one group's softmax, its second
+// product and its next first one does (some 3500 clocks a tile, 2048 of them the
+// tensor cores' for both groups): 256 rows 391 us (1.4 PFLOP/s), 512 rows over
+// 1 x 131000 slots 208 us (1.3 PFLOP/s).  Few keys are a latency: 4 rows over 701
+// slots 11 us.
 //
 // What is not seen.  Scores outside the mask are replaced by -infinity before
 // the maximum, so what their keys hold does not matter.  Zero weights would
@@ -486,7 +493,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             // in order: a group's next scores follow the product that reads its
             // weights).  A second issuing warp, one a group, measured slower: the
             // two groups' instructions then interleave one by one (256 rows over
-            // 32 x 16384 slots: 515 us against 597)
+            // 32 x 16384 slots, measured before the weights came in halves: 515 us
+            // with one, 597 with two)
             constexpr uint32_t kScoreWord = mma_word(kBf16, false, kTile, kTile);
             constexpr uint32_t kOutWord = mma_word(kBf16, true, kTile, D);
             const bool elected = elect_lane();
@@ -672,8 +680,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 copy16_wait();
                 if (args.flip != 0) {
                     for (int r = row / kPer; r < rows; r += 128 / kPer) {
-                        uint4* at = reinterpret_cast<uint4*>(tile + (ch / 8) * S::kHalfBytes + r * 128 +
-                                                             (((ch & 7) ^ (r & 7)) << 4));
+                        uint4* at = reinterpret_cast<uint4*>(tile + (ch / 8) * S::kHalfBytes +
+                                                             r * 128 + (((ch & 7) ^ (r & 7)) << 4));
                         const uint4 x = *at;
                         *at = make_uint4(x.x ^ args.flip, x.y ^ args.flip, x.z ^ args.flip,
                                          x.w ^ args.flip);
@@ -700,8 +708,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     if (masked) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            bits[q] = here ? seen_bits(mask, mask_word, a.mask_words, s.q.ctx, s.q.length,
-                                                       first + 32 * q)
+                            bits[q] = here ? seen_bits(mask, mask_word, a.mask_words, s.q.ctx,
+                                                       s.q.length, first + 32 * q)
                                            : 0u;
                         __syncwarp();
                     }
@@ -773,9 +781,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float x0, x1;
-                            unpack_f32(fma_f32x2(pack_f32(as_float(x[2 * i]), as_float(x[2 * i + 1])),
-                                                 c2, shift2),
-                                       x0, x1);
+                            const uint64_t two =
+                                pack_f32(as_float(x[2 * i]), as_float(x[2 * i + 1]));
+                            unpack_f32(fma_f32x2(two, c2, shift2), x0, x1);
                             x0 = exp2_fast(x0);
                             x1 = exp2_fast(x1);
                             part[i & 1] = add_f32x2(part[i & 1], pack_f32(x0, x1));
@@ -845,7 +853,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 const bool whole = s.k0 == 0 && s.k1 == s.q.tiles;
                 if (threadIdx.x == 0 && s.k0 == 0 && !whole) {
-                    cut.last = share_of(share_s.total, walk.at - 1 + (s.q.tiles - s.k1), share_s.shares);
+                    cut.last = share_of(share_s.total, walk.at - 1 + (s.q.tiles - s.k1),
+                                        share_s.shares);
                     cut.rows = s.rows;
                     cut.begin = s.q.begin;
                     cut.first_row = s.unit * kUnitRows;
@@ -886,7 +895,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                             // that see them: infinities and NaN
                             for (int slot = max(s.q.ctx, s.k0 * kTile);
                                  slot < min(s.q.length, s.k1 * kTile); ++slot) {
-                                if (!(seen_bits(mask, mask_word, a.mask_words, s.q.ctx, s.q.length, slot) & 1))
+                                if (!(seen_bits(mask, mask_word, a.mask_words, s.q.ctx, s.q.length,
+                                                slot) & 1))
                                     continue;
                                 const int64_t at = slot_offset(
                                     a.page_table, a.max_pages, a.page_size, a.num_pages,
@@ -958,9 +968,10 @@ constexpr int kJoinAhead = 8;
 // The cut units' rows: for a row, the states of the blocks that share its unit,
 // in block order.  The first grid dimension is the block that started a unit, the
 // second its rows.  Sixteen lanes take a row: they read up to 16 states' pairs at
-// once, then every lane D / 16 accumulators of each state, kJoinAhead
-// states' loads in flight.  The work is a few bytes
-// a row behind three dependent reads, so it is spread thin and wide.
+// once, then every lane D / 16 accumulators of each state, kJoinAhead states' loads
+// in flight.  The work is a few bytes a row behind three dependent reads, a
+// latency, so it is spread thin and wide: 6 us behind the main kernel's 95 for 8
+// requests of 4 rows over 16384 slots, 16 with 256 rows (states of 39 MB).
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
 tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
@@ -998,7 +1009,8 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] *= keep;
         const int n = min(16, c1 - from + 1);
-        const int at = 2 * args.rows_cap + ((lane * E / 8) * args.rows_cap + local) * 8 + lane * E % 8;
+        const int at =
+            2 * args.rows_cap + ((lane * E / 8) * args.rows_cap + local) * 8 + lane * E % 8;
         for (int i0 = 0; i0 < n; i0 += kJoinAhead) {
             float4 x[kJoinAhead][E / 4];
 #pragma unroll
