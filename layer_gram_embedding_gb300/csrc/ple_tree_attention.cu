@@ -1,5 +1,5 @@
 // Attention of drafted nodes over the paged cache and their own branch, on
-// sm_103a: the kernel for every head width and page size.
+// sm_103a: the kernel for every page size and stride.
 //
 //   out = sum_j p_j v_j,  p = softmax_j(scale q . k_j)
 // over the slots that a node sees, in one pass over the keys with the running
@@ -9,10 +9,12 @@
 // with few blocks split the slots over several; those leave their states in
 // the workspace and a second kernel joins them in the slots' order.
 //
-// It serves the head widths and page sizes that the tensor-core kernel does not
-// take.  Bound by its 32-bit multiply-adds: one row a key head costs 4 D operations
-// a slot, and every node reads the keys for itself.  Heads of 256, 8 key heads of 4
-// query heads: 1 node over 32768 slots 380 us, 4 requests of 16 nodes over 8192 slots 4.9 ms.
+// It serves what the tensor-core kernel does not take: page sizes that are no
+// multiple of 8 and caches with strides that a tensor map refuses.  Bound by its
+// 32-bit multiply-adds, 4 D operations a row and slot, and by every node reading
+// the keys for itself.  20-slot pages, 8 key heads of 4 query heads: 8 requests of
+// 1 node over 8192 slots, heads of 128, 368 us (0.7 TB/s); 4 requests of 16 nodes
+// over 8192 slots, heads of 256, 4.8 ms.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -1,6 +1,6 @@
 // Attention of drafted nodes over the paged cache and their own branch, on the
-// tensor cores of sm_103a, for heads of up to 128 elements (narrower ones are filled
-// up with zeros to 64 or 128 in shared memory).
+// tensor cores of sm_103a, for heads of up to 256 elements (narrower ones are filled
+// up with zeros to 64, 128 or 256 in shared memory).
 //
 // Rows.  The query heads of one key head share its keys, so for a request of n
 // nodes and G = q_heads / kv_heads a key head has n * G rows (node-major).  A
@@ -20,6 +20,11 @@
 // each over the same tiles, so that a key is read once for 256 rows; with fewer
 // they take the tiles in turn over the same rows and are joined in shared memory.
 // Either way one group's softmax runs while the tensor cores work for the other.
+// Heads above 128 are two parts of 128 elements, a part a place of the ring, and a
+// unit is 128 rows: tensor memory holds no two accumulators of 256.  Both groups
+// take the same rows and tiles, each forms the scores and weights for itself
+// and group w the product with the values' part w, so a key is still read
+// once and the groups never meet.
 //
 // Split.  All tiles of all (request, key head, 256 rows) are laid end to end, each
 // unit behind a few places for what it costs besides its tiles, and cut into equal
@@ -34,7 +39,9 @@
 // product and its next first one does (some 3500 clocks a tile, 2048 of them the
 // tensor cores' for both groups): 256 rows 391 us (1.4 PFLOP/s), 512 rows over
 // 1 x 131000 slots 208 us (1.3 PFLOP/s).  Few keys are a latency: 4 rows over 701
-// slots 11 us.
+// slots 11 us.  Heads of 256: 4 rows over 32 x 8192 slots 353 us (6.1 TB/s), 128
+// rows 384, 64 rows over 4 x 8192 slots 73 (4.8 ms on the kernel without tensor
+// cores).
 //
 // What is not seen.  Scores outside the mask are replaced by -infinity before
 // the maximum, so what their keys hold does not matter.  Zero weights would
@@ -53,21 +60,30 @@ namespace ple {
 namespace {
 
 constexpr int kTile = 128;           // keys a tile, rows a matrix instruction
-constexpr int kUnitRows = 2 * kTile; // rows a unit
 constexpr int kThreads = 352;        // two groups of 128, two copying warps, an issuing one
 constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10;
 constexpr int kMaxBlocks = 1024;     // blocks of a launch: an SM's number of them is far below
 constexpr float kLag = 8.0f;         // how far, in the exponent, a maximum may lag
 
+// D is a head's width in shared memory: 64, 128 or 256.
+__host__ __device__ constexpr int padded_width(int head_dim) {
+    return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+}
+__host__ __device__ constexpr int unit_rows(int width) {
+    return width > 128 ? kTile : 2 * kTile;
+}
+
 template <int D>
 struct Shape {
-    static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kHalves = D / 64;
+    static constexpr int kParts = D > 128 ? 2 : 1;   // of a head
+    static constexpr int kWidth = D / kParts;        // elements a part
+    static constexpr int kTileBytes = kTile * kWidth * 2;
+    static constexpr int kHalves = kWidth / 64;
     static constexpr int kHalfBytes = kTile * 128;
-    // as many tiles as fit beside the two query tiles: at D = 128 five of 32 KB,
+    // as many tiles as fit beside the two query tiles: five of 32 KB,
     // more in flight than the 54 KB that an SM's share of the measured
     // bandwidth times a memory latency of 1.2 us asks for
-    static constexpr int kSlots = D == 128 ? 5 : 10;
+    static constexpr int kSlots = kWidth == 128 ? 5 : 10;
     static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
     // half of the 512 columns for each group: S (and P over it), O behind it
     static constexpr uint32_t kGroupColumns = 256;
@@ -78,6 +94,7 @@ struct TcArgs {
     ple_tree_attention_args a;
     int32_t blocks;      // shares
     int32_t rows_cap;    // rows of a state in the workspace, a multiple of 4
+    int32_t unit_rows;   // rows of a key head that go together
     int32_t group;       // query heads a key head
     float c;             // |scale| * log2(e)
     uint32_t flip;       // sign bits to turn in Q: scale < 0
@@ -114,7 +131,7 @@ __device__ __forceinline__ Request request_of(const TcArgs& args, int r) {
     q.length = (int32_t)min(ctx + q.nodes, cap);
     q.tiles = (q.length + kTile - 1) / kTile;
     const int64_t rows = (int64_t)q.nodes * args.group;
-    q.units = (int32_t)((rows + kUnitRows - 1) / kUnitRows);
+    q.units = (int32_t)((rows + args.unit_rows - 1) / args.unit_rows);
     q.work = (int64_t)q.units * (q.tiles + kUnitCost) * a.kv_heads;
     return q;
 }
@@ -195,11 +212,12 @@ struct Segment {
     Request q;
     int32_t head, unit;
     int32_t k0, k1;
-    int32_t rows;     // of the unit, at most kUnitRows
-    bool pair;        // more than 128 rows: a group each
+    int32_t rows;     // of the unit, at most unit_rows
+    bool pair;        // more than 128 rows, a group each, or the same for both
 };
 
 // The block's segments in order; every role walks them alike.
+template <int kParts>
 struct Walk {
     const TcArgs& args;
     int64_t at, end;     // what is still to do
@@ -228,9 +246,10 @@ struct Walk {
             s.k1 = upto - kUnitCost;
             s.head = u / q.units;
             s.unit = u - s.head * q.units;
-            s.rows = (int32_t)min((int64_t)kUnitRows, (int64_t)q.nodes * args.group -
-                                                         (int64_t)s.unit * kUnitRows);
-            s.pair = s.rows > kTile;
+            s.rows = (int32_t)min((int64_t)args.unit_rows,
+                                  (int64_t)q.nodes * args.group -
+                                      (int64_t)s.unit * args.unit_rows);
+            s.pair = kParts == 2 || s.rows > kTile;
             return true;
         }
         return false;
@@ -274,10 +293,16 @@ __host__ __device__ __forceinline__ int64_t state_at(int64_t block, int slot, in
 }
 
 // K_j's and V_j's places in the order of copies K_0, K_1, V_0, K_2, V_1, ... of
-// a segment of n tiles: the order in which the issuing warp wants them.
-__device__ __forceinline__ int key_item(int j) { return j == 0 ? 0 : 2 * j - 1; }
+// a segment of n tiles: the order in which the issuing warp wants them.  Of heads
+// in parts five places hold no three tiles: K_0, V_0, K_1, V_1, ..., a part after
+// the other.
+template <int kParts>
+__device__ __forceinline__ int key_item(int j) {
+    return kParts == 2 ? 4 * j : j == 0 ? 0 : 2 * j - 1;
+}
+template <int kParts>
 __device__ __forceinline__ int value_item(int j, int n) {
-    return j < n - 1 ? 2 * j + 2 : 2 * j + 1;
+    return kParts == 2 ? 4 * j + 2 : j < n - 1 ? 2 * j + 2 : 2 * j + 1;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -411,7 +436,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     tmem_fence_after();
     const uint32_t tmem = tmem_s;
     const int group = args.group;
-    Walk walk(args, share_s);
+    Walk<S::kParts> walk(args, share_s);
     Segment s;
 
     if (warp >= 8) {
@@ -440,41 +465,49 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 // this warp is some tiles ahead: the queries come to the L2 cache
                 // before the groups read them
                 if (!keys) {
-                    const int first_row = s.unit * kUnitRows;
+                    const int first_row = s.unit * args.unit_rows;
                     for (int r = lane; r < s.rows; r += 32) {
                         const unsigned short* at = static_cast<const unsigned short*>(a.q) +
                                                    query_row(args, s, first_row + r);
 #pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h)
+                        for (int h = 0; h < D / 64; ++h)
                             if (64 * h < a.head_dim) prefetch_l2(at + 64 * h);
                     }
                 }
                 int page = page_of(0);
-                for (int j = 0; j < n; ++j) {
+                bool ended = false;
+                for (int j = 0; j < n && !ended; ++j) {
                     const int after = page_of(j + 1);
-                    const uint32_t item = items + (keys ? key_item(j) : value_item(j, n));
-                    const uint32_t slot = item % S::kSlots, round = item / S::kSlots;
-                    count_wait(&armed[slot], round, failed);
-                    if (!mbar_wait(&empty[slot], (round & 1) ^ 1, failed) ||
-                        __any_sync(0xffffffffu, *failed))
-                        break;
-                    if (lane == 0) {
-                        mbar_arrive_expect(&full[slot], S::kTileBytes);
-                        armed[slot] = round + 1;
+#pragma unroll
+                    for (int part = 0; part < S::kParts; ++part) {
+                        const uint32_t item = items + part +
+                                              (keys ? key_item<S::kParts>(j)
+                                                    : value_item<S::kParts>(j, n));
+                        const uint32_t slot = item % S::kSlots, round = item / S::kSlots;
+                        count_wait(&armed[slot], round, failed);
+                        if (!mbar_wait(&empty[slot], (round & 1) ^ 1, failed) ||
+                            __any_sync(0xffffffffu, *failed)) {
+                            ended = true;
+                            break;
+                        }
+                        if (lane == 0) {
+                            mbar_arrive_expect(&full[slot], S::kTileBytes);
+                            armed[slot] = round + 1;
+                        }
+                        __syncwarp();
+                        if (mine)
+                            copy_box(map,
+                                     smem_addr(ring) + slot * S::kTileBytes +
+                                         half * S::kHalfBytes + which * box * 128,
+                                     &full[slot], part * S::kWidth + half * 64,
+                                     box == a.page_size
+                                         ? 0
+                                         : ((s.k0 + j) * kTile + which * box) % a.page_size,
+                                     s.head, page);
                     }
-                    __syncwarp();
-                    if (mine)
-                        copy_box(map,
-                                 smem_addr(ring) + slot * S::kTileBytes + half * S::kHalfBytes +
-                                     which * box * 128,
-                                 &full[slot], half * 64,
-                                 box == a.page_size
-                                     ? 0
-                                     : ((s.k0 + j) * kTile + which * box) % a.page_size,
-                                 s.head, page);
                     page = after;
                 }
-                items += 2 * n;
+                items += 2 * S::kParts * n;
             }
             if (*failed) {
                 // copies may be in flight: they end before the block does
@@ -496,7 +529,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             // 32 x 16384 slots, measured before the weights came in halves: 515 us
             // with one, 597 with two)
             constexpr uint32_t kScoreWord = mma_word(kBf16, false, kTile, kTile);
-            constexpr uint32_t kOutWord = mma_word(kBf16, true, kTile, D);
+            constexpr uint32_t kOutWord = mma_word(kBf16, true, kTile, S::kWidth);
             const bool elected = elect_lane();
             const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(q_tiles);
             uint32_t items = 0, p_count[2] = {0, 0}, pairs = 0, seg = 0;
@@ -507,17 +540,27 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             };
             // a descriptor's address counts 16 bytes and stays below 2^14, so
             // steps within a tile add to it
-            auto scores = [&](int w, uint32_t slot, uint32_t q_tile, bool free) {
-                const uint64_t qd = operand_desc(q_at + q_tile * S::kTileBytes, 16);
-                const uint64_t kd = operand_desc(ring_at + slot * S::kTileBytes, 16);
+            // (the first keys' part in `slot`, a second one in `slot2`)
+            auto scores = [&](int w, uint32_t slot, uint32_t slot2, uint32_t q_tile, bool free) {
                 if (elected) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = ((k / 4) * S::kHalfBytes + (k % 4) * 32) >> 4;
-                        mma_smem(tmem + w * S::kGroupColumns, qd + at, kd + at, kScoreWord, k != 0);
+                    for (int part = 0; part < S::kParts; ++part) {
+                        const uint64_t qd =
+                            operand_desc(q_at + (q_tile + part) * S::kTileBytes, 16);
+                        const uint64_t kd =
+                            operand_desc(ring_at + (part ? slot2 : slot) * S::kTileBytes, 16);
+#pragma unroll
+                        for (int k = 0; k < S::kWidth / 16; ++k) {
+                            const uint32_t at = ((k / 4) * S::kHalfBytes + (k % 4) * 32) >> 4;
+                            mma_smem(tmem + w * S::kGroupColumns, qd + at, kd + at, kScoreWord,
+                                     part != 0 || k != 0);
+                        }
                     }
                     mma_commit(&s_full[w]);
-                    if (free) mma_commit(&empty[slot]);
+                    if (free) {
+                        mma_commit(&empty[slot]);
+                        if (S::kParts == 2) mma_commit(&empty[slot2]);
+                    }
                 }
                 __syncwarp();
             };
@@ -593,36 +636,57 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 mbar_wait(&q_full[0], seg & 1, failed);
                 if (s.pair) mbar_wait(&q_full[1], pairs++ & 1, failed);
                 tmem_fence_after();
-                if (s.pair) {
+                if (S::kParts == 2) {
+                    uint32_t k = wait_item(items), k2 = wait_item(items + 1);
+                    scores(0, k, k2, 0, false);
+                    scores(1, k, k2, 0, true);
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        const uint32_t at = items + value_item<S::kParts>(j, n);
+                        const uint32_t v = wait_item(at), v2 = wait_item(at + 1);
+                        clean(j, v);
+                        clean(j, v2);
+                        if (!product(0, v, j > 0, true)) break;
+                        if (more) {
+                            const uint32_t next = items + key_item<S::kParts>(j + 1);
+                            k = wait_item(next);
+                            k2 = wait_item(next + 1);
+                            scores(0, k, k2, 0, false);
+                        }
+                        if (!product(1, v2, j > 0, true)) break;
+                        if (more) scores(1, k, k2, 0, true);
+                    }
+                } else if (s.pair) {
                     uint32_t k = wait_item(items);
-                    scores(0, k, 0, false);
-                    scores(1, k, 1, true);
+                    scores(0, k, 0, 0, false);
+                    scores(1, k, 0, 1, true);
                     for (int j = 0; j < n; ++j) {
                         const bool more = j + 1 < n;
                         // the next keys were copied before these values: both are
                         // at hand before the weights are
-                        const uint32_t v = wait_item(items + value_item(j, n));
-                        if (more) k = wait_item(items + key_item(j + 1));
+                        const uint32_t v = wait_item(items + value_item<S::kParts>(j, n));
+                        if (more) k = wait_item(items + key_item<S::kParts>(j + 1));
                         clean(j, v);
                         if (!product(0, v, j > 0, false)) break;
-                        if (more) scores(0, k, 0, false);
+                        if (more) scores(0, k, 0, 0, false);
                         if (!product(1, v, j > 0, true)) break;
-                        if (more) scores(1, k, 1, true);
+                        if (more) scores(1, k, 0, 1, true);
                     }
                 } else {
                     for (int w = 0; w < min(2, n); ++w)
-                        scores(w, wait_item(items + key_item(w)), 0, true);
+                        scores(w, wait_item(items + key_item<S::kParts>(w)), 0, 0, true);
                     for (int j = 0; j < n; ++j) {
                         const int w = j & 1;
-                        const uint32_t v = wait_item(items + value_item(j, n));
+                        const uint32_t v = wait_item(items + value_item<S::kParts>(j, n));
                         clean(j, v);
                         if (!product(w, v, j > 1, true)) break;
-                        if (j + 2 < n) scores(w, wait_item(items + key_item(j + 2)), 0, true);
+                        if (j + 2 < n)
+                            scores(w, wait_item(items + key_item<S::kParts>(j + 2)), 0, 0, true);
                     }
                 }
                 if (elected) mma_commit(&q_empty);
                 __syncwarp();
-                items += 2 * n;
+                items += 2 * S::kParts * n;
                 ++seg;
             }
             // everything issued is done before the block ends, also after a failure
@@ -646,8 +710,11 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
         cut.last = -1;
         while (walk.next(s)) {
             const int n = s.k1 - s.k0;
-            const int first_row = s.unit * kUnitRows + (s.pair ? w * kTile : 0);
-            const int rows = s.pair ? (w == 0 ? kTile : s.rows - kTile) : s.rows;
+            constexpr bool kSplit = S::kParts == 2;   // both groups have the same rows
+            const int row0 = s.pair && !kSplit ? w * kTile : 0;   // the group's in the unit
+            const int first_row = s.unit * args.unit_rows + row0;
+            const int rows = s.pair && !kSplit ? (w == 0 ? kTile : s.rows - kTile) : s.rows;
+            const int column0 = kSplit ? w * S::kWidth : 0;       // of the group's accumulators
             const bool active = (warp & 3) * 32 < rows;   // a warp with no row only keeps step
             const bool here = row < rows;
             const int node = (first_row + row) / group;
@@ -659,20 +726,22 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             // asked for long before the tiles that need it
             const uint64_t mask_word = here ? __ldg(mask) : 0;
 
-            // this group's queries, rows of the unit, into swizzled shared memory
+            // this group's queries, rows of the unit, into swizzled shared memory, or
+            // its part of all of them
             if (s.pair || w == 0) {
                 if (seg > 0) mbar_wait(&q_empty, (seg - 1) & 1, failed);
                 if (w == 0 && row == 0) bad_s[seg & 1] = 0;
                 uint8_t* tile = q_tiles + (s.pair ? w : 0) * S::kTileBytes;
                 // 16-byte pieces copied without a register, all in flight at once
-                constexpr int kPer = D / 8;
+                constexpr int kPer = S::kWidth / 8;
                 const int ch = row % kPer;
                 const uint32_t to = smem_addr(tile) + (ch / 8) * S::kHalfBytes;
-                const unsigned short* from = static_cast<const unsigned short*>(a.q) + ch * 8;
+                const unsigned short* from =
+                    static_cast<const unsigned short*>(a.q) + column0 + ch * 8;
 #pragma unroll 4
                 for (int r = row / kPer; r < rows; r += 128 / kPer) {
                     const uint32_t dst = to + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                    if (ch * 8 < a.head_dim)
+                    if (column0 + ch * 8 < a.head_dim)
                         copy16(dst, from + query_row(args, s, first_row + r));
                     else  // columns past a narrower head's
                         zero16(dst);
@@ -754,7 +823,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                             mbar_wait(&pv_done[w], (count - 1) & 1, failed);
                             tmem_fence_after();
 #pragma unroll 1
-                            for (int q = 0; q < D / 32; ++q) {
+                            for (int q = 0; q < S::kWidth / 32; ++q) {
                                 uint32_t o[32];
                                 tmem_load(o_at + 32 * q, o);
                                 tmem_wait_load(o);
@@ -823,7 +892,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 mbar_wait(&q_empty, seg & 1, failed);   // the queries have been read
                 if (active) {
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
+                    for (int q = 0; q < S::kWidth / 32; ++q) {
                         uint32_t o[32];
                         tmem_load(o_at + 32 * q, o);
                         tmem_wait_load(o);
@@ -857,21 +926,23 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                                         share_s.shares);
                     cut.rows = s.rows;
                     cut.begin = s.q.begin;
-                    cut.first_row = s.unit * kUnitRows;
+                    cut.first_row = s.unit * args.unit_rows;
                     cut.head = s.head;
                 }
-                if (*failed) sum = __int_as_float(0x7FC00000);  // NaN, not an unfinished sum
+                const bool spoiled = *failed;
+                if (spoiled) sum = __int_as_float(0x7FC00000);  // NaN, not an unfinished sum
                 const bool bad = bad_s[seg & 1] != 0;
                 const int64_t o_row = token * a.q_heads + head;
                 float* state = static_cast<float*>(a.workspace) +
                                state_at(blockIdx.x, s.k0 == 0 ? 1 : 0, args.rows_cap, D);
-                const int state_row = (s.pair ? w * kTile : 0) + row;
+                const int state_row = row0 + row;
                 float* pairs = state + 2 * state_row;
-                float* acc = state + 2 * args.rows_cap + 8 * state_row;
+                float* acc = state + (2 + column0) * args.rows_cap + 8 * state_row;
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 if (active) {
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
+                    for (int q = 0; q < S::kWidth / 32; ++q) {
+                        const int column = column0 + 32 * q;
                         uint32_t o[32];
                         if (begun) {
                             tmem_load(o_at + 32 * q, o);
@@ -880,6 +951,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         float x[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
+                        if (kSplit && spoiled) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = __int_as_float(0x7FC00000);
+                        }
                         if (join) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
@@ -904,10 +979,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                                 if (at < 0) continue;
                                 const unsigned short* vrow =
                                     static_cast<const unsigned short*>(a.v_cache) + at +
-                                    s.head * a.head_stride + 32 * q;
+                                    s.head * a.head_stride + column;
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) {
-                                    if (32 * q + i >= a.head_dim) break;
+                                    if (column + i >= a.head_dim) break;
                                     const float e = widen16<kBf16>(vrow[i]);
                                     if (!isfinite(e)) x[i] += e;
                                 }
@@ -915,10 +990,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                         if (here && whole) {
                             uint4* dst = reinterpret_cast<uint4*>(
-                                static_cast<unsigned short*>(a.out) + o_row * a.head_dim + 32 * q);
+                                static_cast<unsigned short*>(a.out) + o_row * a.head_dim + column);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                if (32 * q + 8 * i >= a.head_dim) break;
+                                if (column + 8 * i >= a.head_dim) break;
                                 uint32_t y[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
@@ -935,7 +1010,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                         __syncwarp();  // the next load is the whole warp's
                     }
-                    if (here) {
+                    if (here && column0 == 0) {
                         if (!whole) {
                             pairs[0] = top == -INFINITY ? -INFINITY : top * c;
                             pairs[1] = sum;
@@ -963,19 +1038,19 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
 
 constexpr int kJoinThreads = 128;
 constexpr int kJoinRows = kJoinThreads / 16;  // rows a block
-constexpr int kJoinAhead = 8;
 
 // The cut units' rows: for a row, the states of the blocks that share its unit,
 // in block order.  The first grid dimension is the block that started a unit, the
 // second its rows.  Sixteen lanes take a row: they read up to 16 states' pairs at
-// once, then every lane D / 16 accumulators of each state, kJoinAhead states' loads
-// in flight.  The work is a few bytes a row behind three dependent reads, a
+// once, then every lane D / 16 accumulators of each state, eight states' loads in
+// flight (four of 256).  The work is a few bytes a row behind three dependent reads, a
 // latency, so it is spread thin and wide: 6 us behind the main kernel's 95 for 8
 // requests of 4 rows over 16384 slots, 16 with 256 rows (states of 39 MB).
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
 tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
     constexpr int E = D / 16;
+    constexpr int kJoinAhead = D > 128 ? 4 : 8;
     const ple_tree_attention_args& a = args.a;
     wait_grid_before();
     const int c0 = blockIdx.x;
@@ -1021,7 +1096,8 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
                         state_at(from + i0 + i, from + i0 + i == c0 ? 1 : 0, args.rows_cap, D);
 #pragma unroll
                     for (int e = 0; e < E / 4; ++e)
-                        x[i][e] = __ldcg(reinterpret_cast<const float4*>(theirs) + e);
+                        x[i][e] = __ldcg(reinterpret_cast<const float4*>(
+                            theirs + e / 2 * 8 * args.rows_cap + e % 2 * 4));
                 }
             }
 #pragma unroll
@@ -1052,11 +1128,14 @@ tree_attention_join_kernel(const __grid_constant__ TcArgs args) {
     uint32_t* dst =
         reinterpret_cast<uint32_t*>(static_cast<unsigned short*>(a.out) + o * a.head_dim) +
         lane * (E / 2);
-    if (lane * E < a.head_dim) {
-        if constexpr (E == 8)
-            *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-        else
-            *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    if constexpr (E == 4) {
+        if (lane * E < a.head_dim) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 8)
+            if (lane * E + e < a.head_dim)
+                *reinterpret_cast<uint4*>(dst + e / 2) =
+                    make_uint4(y[e / 2], y[e / 2 + 1], y[e / 2 + 2], y[e / 2 + 3]);
     }
     if (lane == 0 && a.lse != nullptr)
         a.lse[o] = sum == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(sum);
@@ -1109,9 +1188,10 @@ int tc_blocks(const DeviceFacts& dev) {
     return dev.sm_count < kMaxBlocks ? dev.sm_count : kMaxBlocks;
 }
 
-int tc_rows_cap(int64_t T, int32_t q_heads, int32_t kv_heads) {
+int tc_rows_cap(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
     const int64_t rows = T * (q_heads / kv_heads);
-    return (int)(rows < kUnitRows ? (rows + 3) / 4 * 4 : kUnitRows);  // 16-byte rows
+    const int most = unit_rows(padded_width(head_dim));
+    return (int)(rows < most ? (rows + 3) / 4 * 4 : most);  // 16-byte rows
 }
 
 template <int D, bool kBf16>
@@ -1134,13 +1214,13 @@ cudaError_t launch_tc(const TcArgs& args, const CUtensorMap& k, const CUtensorMa
 
 int64_t tree_attention_tc_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D,
                                     const DeviceFacts& dev) {
-    return 4 * state_at(tc_blocks(dev), 0, tc_rows_cap(T, q_heads, kv_heads), D <= 64 ? 64 : 128);
+    return 4 * state_at(tc_blocks(dev), 0, tc_rows_cap(T, q_heads, kv_heads, D), padded_width(D));
 }
 
-// Heads up to the widest tile, and pages that boxes of whole swizzle atoms (8
-// slots) cut evenly.
+// Pages that boxes of whole swizzle atoms (8 slots) cut evenly, and tiles whose
+// ends stay within 31 bits.
 bool tree_attention_tc_fits(const ple_tree_attention_args& a) {
-    return a.head_dim <= 128 && a.page_size % 8 == 0;
+    return a.page_size % 8 == 0 && (int64_t)a.max_pages * a.page_size <= INT32_MAX - kTile;
 }
 
 // *taken: whether the tensor maps take the caches' strides (else nothing ran).
@@ -1153,16 +1233,24 @@ cudaError_t launch_tree_attention_tc(const ple_tree_attention_args& a, const Dev
     args.a = a;
     args.blocks = tc_blocks(dev);
     args.group = a.q_heads / a.kv_heads;
-    args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads);
+    args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads, a.head_dim);
+    args.unit_rows = unit_rows(padded_width(a.head_dim));
     // a scale of 0 as the least normal number: every exponent still rounds to 0,
     // and a hidden score stays -infinity
     args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     args.flip = a.scale < 0 ? 0x80008000u : 0u;
-    if (a.head_dim <= 64)
-        return a.dtype == PLE_BF16 ? launch_tc<64, true>(args, k, v, stream)
-                                   : launch_tc<64, false>(args, k, v, stream);
-    return a.dtype == PLE_BF16 ? launch_tc<128, true>(args, k, v, stream)
-                               : launch_tc<128, false>(args, k, v, stream);
+    const bool bf16 = a.dtype == PLE_BF16;
+    switch (padded_width(a.head_dim)) {
+        case 64:
+            return bf16 ? launch_tc<64, true>(args, k, v, stream)
+                        : launch_tc<64, false>(args, k, v, stream);
+        case 128:
+            return bf16 ? launch_tc<128, true>(args, k, v, stream)
+                        : launch_tc<128, false>(args, k, v, stream);
+        default:
+            return bf16 ? launch_tc<256, true>(args, k, v, stream)
+                        : launch_tc<256, false>(args, k, v, stream);
+    }
 }
 
 }  // namespace ple

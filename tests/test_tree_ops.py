@@ -405,7 +405,7 @@ ATTENTION_CASES = [
     ([40, 64, 33], [2500, 900, 3000], 32, 4, 64, 32, "phsd"),
     ([18], [9001], 32, 4, 128, 64, "phsd"),
     ([1, 1], [20000, 11], 4, 2, 128, 128, "phsd"),
-    # widths and page sizes of the other kernel: split slots, more heads than a block takes
+    # other widths, and page sizes of the other kernel: split slots, more heads than a block takes
     ([1, 3], [5000, 0], 20, 2, 256, 16, "phsd"),
     ([1], [3001], 3, 1, 128, 20, "pshd"),
     ([1, 40], [3001, 129], 6, 2, 128, 24, "pshd"),
@@ -479,6 +479,54 @@ def test_attention_random_batches(seed):
     Hq = Hk * int(rng.choice([1, 2, 3, 4, 7, 8, 16]))
     B = int(rng.integers(1, 40))
     most = int(rng.choice([1, 3, 17, 64, 90, 200]))
+    counts = [int(rng.integers(0 if B > 1 else 1, most + 1)) for _ in range(B)]
+    counts[0] = max(counts[0], 1)
+    room = max(1, int(3e6 / max(sum(counts) * Hq, 1) * B))  # scores of the reference
+    ctx = [int(rng.integers(0, min(room, 9000) + 1)) for _ in range(B)]
+    q, cache, ctx, cu, masks = attention_inputs(rng, counts, ctx, Hq, Hk, D, page, dtype,
+                                                str(rng.choice(["phsd", "pshd"])))
+    first = check_attention(q, cache, ctx, cu, masks, what=str((counts, ctx, Hq, Hk, D, page)),
+                            reference=dense_attention)
+    for _ in range(20):  # nothing depends on timing
+        again = ple.ple_tree_attention(q, cache.k, cache.v, dev(cache.table), dev(ctx), dev(cu),
+                                       dev(masks), return_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+# Heads in two parts: one tile, cut units, more than a unit's 128 rows, a part of one
+# piece, tiles of several pages; then pages of the other kernel.
+WIDE_CASES = [
+    ([1], [0], 1, 1, 256, 64, "phsd"),
+    ([1], [127], 8, 1, 256, 64, "pshd"),
+    ([1, 1, 1], [20000, 0, 300], 8, 2, 256, 64, "phsd"),
+    ([40, 64, 33], [900, 2500, 1], 8, 2, 256, 16, "phsd"),
+    ([33, 0, 200], [3001, 5, 130], 16, 4, 192, 32, "pshd"),
+    ([18], [9001], 16, 2, 136, 128, "phsd"),
+    ([65], [4000], 6, 2, 248, 8, "phsd"),
+    ([9, 3], [700, 64], 20, 2, 256, 12, "phsd"),
+    ([5], [2000], 4, 4, 192, 20, "pshd"),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("case", WIDE_CASES)
+def test_attention_of_wide_heads(case, dtype):
+    counts, ctx, Hq, Hk, D, page, order = case
+    rng = np.random.default_rng(sum(counts) + D + page)
+    q, cache, ctx, cu, masks = attention_inputs(rng, counts, ctx, Hq, Hk, D, page, dtype, order)
+    check_attention(q, cache, ctx, cu, masks, what=str(case))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_attention_random_batches_of_wide_heads(seed):
+    rng = np.random.default_rng(2000 + seed)
+    D = int(rng.choice([256, 256, 192, 136, 160, 200]))
+    page = int(rng.choice([8, 16, 32, 64, 128, 24]))
+    dtype = [torch.bfloat16, torch.float16][seed % 2]
+    Hk = int(rng.choice([1, 2, 4, 8]))
+    Hq = Hk * int(rng.choice([1, 2, 3, 4, 8]))
+    B = int(rng.integers(1, 40))
+    most = int(rng.choice([1, 3, 17, 64, 90]))
     counts = [int(rng.integers(0 if B > 1 else 1, most + 1)) for _ in range(B)]
     counts[0] = max(counts[0], 1)
     room = max(1, int(3e6 / max(sum(counts) * Hq, 1) * B))  # scores of the reference
