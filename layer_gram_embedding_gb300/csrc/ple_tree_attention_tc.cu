@@ -15,8 +15,9 @@
 //
 // Blocks.  One block an SM: two warps that copy key and value tiles into a ring
 // of shared memory (tiled bulk copies, page by page, 128-byte swizzle), a warp
-// that issues the matrix instructions, and two groups of four warps that do the
-// softmax, one row a thread.  With more than 128 rows the two groups take 128
+// that issues the matrix instructions, one that works out the next segment (a unit's
+// tiles in this block) ahead of the softmax, and two groups of four warps that do
+// the softmax, one row a thread.  With more than 128 rows the two groups take 128
 // each over the same tiles, so that a key is read once for 256 rows; with fewer
 // they take the tiles in turn over the same rows and are joined in shared memory.
 // Either way one group's softmax runs while the tensor cores work for the other.
@@ -60,8 +61,8 @@ namespace ple {
 namespace {
 
 constexpr int kTile = 128;           // keys a tile, rows a matrix instruction
-constexpr int kThreads = 352;        // two groups of 128, two copying warps, an issuing one
-constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10;
+constexpr int kThreads = 384;        // two groups of 128 and four warps of a task each
+constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10, kWalkWarp = 11;
 constexpr int kMaxBlocks = 1024;     // blocks of a launch: an SM's number of them is far below
 constexpr float kLag = 8.0f;         // how far, in the exponent, a maximum may lag
 
@@ -212,6 +213,7 @@ struct Segment {
     Request q;
     int32_t head, unit;
     int32_t k0, k1;
+    int32_t r;        // the request
     int32_t rows;     // of the unit, at most unit_rows
     bool pair;        // more than 128 rows, a group each, or the same for both
 };
@@ -219,16 +221,18 @@ struct Segment {
 // The block's segments in order; every role walks them alike.
 template <int kParts>
 struct Walk {
-    const TcArgs& args;
     int64_t at, end;     // what is still to do
     int64_t base;        // the work before request r
     int r;
     Request q;
-    __device__ __forceinline__ Walk(const TcArgs& the, const Share& share)
-        : args(the), at(share.lo), end(share.hi), base(share.before), r(share.first) {
+    __device__ __forceinline__ void begin(const TcArgs& args, const Share& share) {
+        at = share.lo;
+        end = share.hi;
+        base = share.before;
+        r = share.first;
         if (at < end) q = request_of(args, r);
     }
-    __device__ __forceinline__ bool next(Segment& s) {
+    __device__ __forceinline__ bool next(const TcArgs& args, Segment& s) {
         while (at < end) {
             while (at >= base + q.work) {
                 base += q.work;
@@ -242,6 +246,7 @@ struct Walk {
             at += upto - from;
             if (upto <= kUnitCost) continue;  // its first tile is the next share's
             s.q = q;
+            s.r = r;
             s.k0 = max(from - kUnitCost, 0);
             s.k1 = upto - kUnitCost;
             s.head = u / q.units;
@@ -263,7 +268,8 @@ __host__ __device__ __forceinline__ int page_box(int page_size) {
 }
 
 // The offset of the query of a key head's row.
-__device__ __forceinline__ int64_t query_row(const TcArgs& args, const Segment& s, int row) {
+template <typename S>
+__device__ __forceinline__ int64_t query_row(const TcArgs& args, const S& s, int row) {
     const ple_tree_attention_args& a = args.a;
     const uint32_t group = args.group;
     const uint32_t node = (uint32_t)row / group;
@@ -348,19 +354,38 @@ __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
     return v;
 }
 
+// A node's mask where a tile's slots from `slot` on meet it: three words, all
+// that 128 bits may reach, from word `base` on.
+struct MaskWindow {
+    uint64_t w[3];
+    int base;
+};
+
+__device__ __forceinline__ MaskWindow mask_window(const unsigned long long* __restrict__ mask,
+                                                  uint64_t first_word, int words, int ctx,
+                                                  int slot) {
+    MaskWindow m;
+    m.base = max(slot - ctx, 0) >> 6;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        m.w[k] = m.base + k == 0 ? first_word : 0;
+        if (m.base + k > 0 && m.base + k < words) m.w[k] = __ldg(mask + m.base + k);
+    }
+    return m;
+}
+
 // Which of 32 slots from `slot` on a node sees, as bits: all below ctx, above it
-// those of its mask (whose first word is at hand).
-__device__ __forceinline__ uint32_t seen_bits(const unsigned long long* __restrict__ mask,
-                                              uint64_t first_word, int words, int ctx, int length,
+// those of its mask.
+__device__ __forceinline__ uint32_t seen_bits(const MaskWindow& m, int words, int ctx, int length,
                                               int slot) {
     const int b = slot - ctx;
     if (b + 32 <= 0) return 0xffffffffu;
     const int lo = max(b, 0);
     const int limit = min(length - ctx, 64 * words);
     if (lo >= limit) return b < 0 ? (1u << -b) - 1 : 0u;
-    const int w = lo >> 6, s = lo & 63;
-    uint64_t v = (w == 0 ? first_word : __ldg(mask + w)) >> s;
-    if (s > 32 && w + 1 < words) v |= __ldg(mask + w + 1) << (64 - s);
+    const int k = (lo >> 6) - m.base, s = lo & 63;
+    uint64_t v = (k == 0 ? m.w[0] : k == 1 ? m.w[1] : m.w[2]) >> s;
+    if (s > 32) v |= (k == 0 ? m.w[1] : m.w[2]) << (64 - s);
     uint32_t bits = (uint32_t)v;
     if (limit - lo < 32) bits &= (1u << (limit - lo)) - 1;
     return b < 0 ? bits << -b | ((1u << -b) - 1) : bits;
@@ -396,6 +421,12 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     __shared__ int failed_s;
     __shared__ int bad_s[2];          // a segment's drafted values hold infinities or NaN
     __shared__ float join_s[kTile][2];
+    // The softmax groups' segments, the one that they work on and the next, and
+    // whether there is one.  They read them here where they need them: registers are
+    // short, and what they spill goes through the little cache that the ring leaves.
+    __shared__ Segment seg_s[2];
+    __shared__ int more_s[2];
+    __shared__ int64_t end_s[2];      // the place behind the segment
     volatile int* failed = &failed_s;
     volatile uint32_t* armed = armed_s;
 
@@ -436,11 +467,25 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
     tmem_fence_after();
     const uint32_t tmem = tmem_s;
     const int group = args.group;
-    Walk<S::kParts> walk(args, share_s);
-    Segment s;
-
     if (warp >= 8) {
-        if (warp == kKeyWarp || warp == kValueWarp) {
+        Walk<S::kParts> walk;
+        walk.begin(args, share_s);
+        Segment s;
+        if (warp == kWalkWarp) {
+            // --------------------------- the groups' segments, one ahead
+            bool more;
+            uint32_t seg = 0;
+            do {
+                more = walk.next(args, s);
+                if (lane == 0) {
+                    seg_s[seg & 1] = s;
+                    end_s[seg & 1] = walk.at;
+                    more_s[seg & 1] = more;
+                }
+                ++seg;
+                named_barrier<288>(3);
+            } while (more);
+        } else if (warp == kKeyWarp || warp == kValueWarp) {
             // ------------------------------------------------------- copies
             const bool keys = warp == kKeyWarp;
             const CUtensorMap* map = keys ? &k_map : &v_map;
@@ -450,9 +495,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             const int which = lane / S::kHalves, half = lane % S::kHalves;
             const bool mine = which < boxes;
             uint32_t items = 0;
-            while (walk.next(s)) {
+            while (walk.next(args, s)) {
                 const int n = s.k1 - s.k0;
-                const int32_t* table = a.page_table + (int64_t)walk.r * a.max_pages;
+                const int32_t* table = a.page_table + (int64_t)s.r * a.max_pages;
                 // a box past the tokens, or of a page outside the cache, is filled
                 // with zeros: its page number is outside the map
                 auto page_of = [&](int j) -> int {
@@ -591,41 +636,53 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 values(w, slot, 1, true, free);
                 return true;
             };
-            while (walk.next(s)) {
+            while (walk.next(args, s)) {
                 const int n = s.k1 - s.k0;
-                // values past the request's tokens, and drafted ones that are not
-                // finite, are cleared before the product reads them
+                // Values past the request's tokens, and drafted ones that are not
+                // finite, are cleared before the product reads them.  Eight pieces a
+                // lane are looked at together: one by one, behind each other's
+                // stores, a tile took some 5000 clocks and was what long drafts waited
+                // for (512 nodes for each of 8 requests over 512 slots: 187 us, 126 with
+                // this and the masks' words fetched ahead)
                 auto clean = [&](int j, uint32_t slot) {
                     const int first = (s.k0 + j) * kTile;
                     if (first + kTile <= s.q.ctx) return;
-                    uint8_t* tile = ring + slot * S::kTileBytes;
                     const int from = max(s.q.ctx - first, 0), upto = min(s.q.length - first, kTile);
-                    constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
+                    // an exponent of ones carries into its element's sign bit
+                    constexpr uint32_t kExp = kBf16 ? 0x7F807F80u : 0x7C007C00u;
+                    constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
+                    auto flags = [](uint32_t x) { return ((x & kExp) + kOne) & 0x80008000u; };
                     bool bad = false;
-                    for (int i = from * 8 + lane; i < kTile * 8; i += 32) {
-                        const bool live = i < upto * 8;
 #pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h) {
-                            uint4* at = reinterpret_cast<uint4*>(tile + h * S::kHalfBytes) + i;
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            bool change = !live;
-                            if (live) {
-                                v = *at;
-                                uint32_t* x = &v.x;
+                    for (int h = 0; h < S::kHalves; ++h) {
+                        uint4* tile = reinterpret_cast<uint4*>(ring + slot * S::kTileBytes +
+                                                               h * S::kHalfBytes);
+                        constexpr int kAhead = 8;
+                        for (int i = from * 8 + lane; i < upto * 8; i += 32 * kAhead) {
+                            uint4 v[kAhead];
+                            uint32_t any = 0;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if ((x[e] & kExp) == kExp) {
-                                        x[e] &= 0xFFFF0000u;
-                                        change = bad = true;
-                                    }
-                                    if ((x[e] >> 16 & kExp) == kExp) {
-                                        x[e] &= 0xFFFFu;
-                                        change = bad = true;
-                                    }
-                                }
+                            for (int k = 0; k < kAhead; ++k)
+                                v[k] = i + 32 * k < upto * 8 ? tile[i + 32 * k]
+                                                             : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                            for (int k = 0; k < kAhead; ++k)
+                                any |= flags(v[k].x) | flags(v[k].y) | flags(v[k].z) |
+                                       flags(v[k].w);
+                            if (any == 0) continue;
+                            bad = true;
+#pragma unroll
+                            for (int k = 0; k < kAhead; ++k) {
+                                auto cleared = [&](uint32_t x) {
+                                    return x & ~((flags(x) >> 15) * 0xFFFFu);
+                                };
+                                if (i + 32 * k < upto * 8)
+                                    tile[i + 32 * k] = make_uint4(cleared(v[k].x), cleared(v[k].y),
+                                                                  cleared(v[k].z), cleared(v[k].w));
                             }
-                            if (change) *at = v;
                         }
+                        for (int i = max(upto, 0) * 8 + lane; i < kTile * 8; i += 32)
+                            tile[i] = make_uint4(0, 0, 0, 0);
                     }
                     if (bad) bad_s[seg & 1] = 1;
                     __threadfence_block();
@@ -706,9 +763,11 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
         const uint32_t o_at = s_at + S::kOut;
         const float c = args.c;
         uint32_t seg = 0, count = 0;
-        Cut cut = {};
-        cut.last = -1;
-        while (walk.next(s)) {
+        if (threadIdx.x == 0) static_cast<Cut*>(a.workspace)[blockIdx.x].last = -1;
+        for (;;) {
+            named_barrier<288>(3);
+            if (!*static_cast<volatile int*>(&more_s[seg & 1])) break;
+            const volatile Segment& s = seg_s[seg & 1];
             const int n = s.k1 - s.k0;
             constexpr bool kSplit = S::kParts == 2;   // both groups have the same rows
             const int row0 = s.pair && !kSplit ? w * kTile : 0;   // the group's in the unit
@@ -764,11 +823,14 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             const int step = s.pair ? 1 : 2;
             bool begun = false;
             for (int j = s.pair ? 0 : w; j < n; j += step) {
+                const int first = (s.k0 + j) * kTile;
+                const bool masked = first + kTile > s.q.ctx;
+                MaskWindow window;
+                if (masked && here)
+                    window = mask_window(mask, mask_word, a.mask_words, s.q.ctx, first);
                 if (!mbar_wait(&s_full[w], count & 1, failed)) break;
                 tmem_fence_after();
                 if (active) {
-                    const int first = (s.k0 + j) * kTile;
-                    const bool masked = first + kTile > s.q.ctx;
                     // The row's scores are walked twice, 64 columns at a time: the
                     // upper half and then the lower for the maximum, the lower, still in
                     // registers, and the upper again for the weights.  All 128 would
@@ -777,8 +839,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     if (masked) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            bits[q] = here ? seen_bits(mask, mask_word, a.mask_words, s.q.ctx,
-                                                       s.q.length, first + 32 * q)
+                            bits[q] = here ? seen_bits(window, a.mask_words, s.q.ctx, s.q.length,
+                                                       first + 32 * q)
                                            : 0u;
                         __syncwarp();
                     }
@@ -922,12 +984,14 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 const bool whole = s.k0 == 0 && s.k1 == s.q.tiles;
                 if (threadIdx.x == 0 && s.k0 == 0 && !whole) {
-                    cut.last = share_of(share_s.total, walk.at - 1 + (s.q.tiles - s.k1),
+                    Cut cut = {};
+                    cut.last = share_of(share_s.total, end_s[seg & 1] - 1 + (s.q.tiles - s.k1),
                                         share_s.shares);
                     cut.rows = s.rows;
                     cut.begin = s.q.begin;
                     cut.first_row = s.unit * args.unit_rows;
                     cut.head = s.head;
+                    static_cast<Cut*>(a.workspace)[blockIdx.x] = cut;
                 }
                 const bool spoiled = *failed;
                 if (spoiled) sum = __int_as_float(0x7FC00000);  // NaN, not an unfinished sum
@@ -970,12 +1034,13 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                             // that see them: infinities and NaN
                             for (int slot = max(s.q.ctx, s.k0 * kTile);
                                  slot < min(s.q.length, s.k1 * kTile); ++slot) {
-                                if (!(seen_bits(mask, mask_word, a.mask_words, s.q.ctx, s.q.length,
-                                                slot) & 1))
+                                const MaskWindow one = mask_window(mask, mask_word, a.mask_words,
+                                                                   s.q.ctx, slot);
+                                if (!(seen_bits(one, a.mask_words, s.q.ctx, s.q.length, slot) & 1))
                                     continue;
                                 const int64_t at = slot_offset(
                                     a.page_table, a.max_pages, a.page_size, a.num_pages,
-                                    a.page_stride, a.slot_stride, walk.r, slot);
+                                    a.page_stride, a.slot_stride, s.r, slot);
                                 if (at < 0) continue;
                                 const unsigned short* vrow =
                                     static_cast<const unsigned short*>(a.v_cache) + at +
@@ -1025,7 +1090,6 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
             named_barrier<256>(2);
             ++seg;
         }
-        if (threadIdx.x == 0) static_cast<Cut*>(a.workspace)[blockIdx.x] = cut;
     }
 
     tmem_fence_before();

@@ -624,6 +624,25 @@ def test_attention_masks_bits_past_the_nodes_are_ignored():
     assert all(torch.equal(a, b) for a, b in zip(out, plain))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_of_long_drafts(D, dtype):
+    # masks of any bits in eight words, drafted tiles at odd places in them, and values that
+    # are not finite in a few nodes' first, last and middle elements
+    rng = np.random.default_rng(17)
+    q, cache, ctx, cu, masks = attention_inputs(rng, [512, 300, 65], [77, 1000, 191], 2, 1, D, 16,
+                                                dtype)
+    masks = rng.integers(-2 ** 63, 2 ** 63, masks.shape, dtype=np.int64)
+    masks[rng.random(masks.shape) < 0.3] = 0
+    check_attention(q, cache, ctx, cu, masks)
+    for r, node, element, bad in [(0, 511, D - 1, np.inf), (0, 200, 3, -np.inf),
+                                  (0, 63, 0, np.nan), (1, 299, D // 2, np.inf), (1, 0, 7, np.nan),
+                                  (2, 64, D - 2, -np.inf)]:
+        p, s = cache.where(r, int(ctx[r]) + node)
+        cache.v[int(p), :, s, element] = float(bad)
+    check_attention(q, cache, ctx, cu, masks, sanitize=True)
+
+
 @pytest.mark.parametrize("D", [64, 128, 96, 160])
 def test_attention_pages_outside_the_cache_read_as_zeros(D):
     rng = np.random.default_rng(13)
