@@ -488,6 +488,9 @@ def ple_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                 size = max(lib().ple_tree_attention_workspace(T, Hq, Hk, D), 0)
             _workspace_sizes[sizes] = size
         workspace = _empty(size, dtype=torch.uint8, device=device)
+        if stream is not None:
+            # freed on return, while the kernels on the other stream use it
+            workspace.record_stream(stream)
     args = _ATTENTION.pack(
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), strides[0],
         strides[1], strides[2], pages, page_table.data_ptr(), ctx_lens.data_ptr(),

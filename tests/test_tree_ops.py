@@ -661,6 +661,29 @@ def test_attention_pages_outside_the_cache_read_as_zeros(D):
     assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[2])
 
 
+def test_attention_on_another_stream_keeps_its_workspace():
+    # the call's own workspace is not handed out again while the other stream still needs it
+    rng = np.random.default_rng(18)
+    args = attention_inputs(rng, [20], [3001], 8, 2, 64, 16, torch.bfloat16)
+    q, cache, ctx, cu, masks = args
+    call = (q, cache.k, cache.v, dev(cache.table), dev(ctx), dev(cu), dev(masks))
+    out, want = torch.empty_like(q), ple.ple_tree_attention(*call)
+    size = ple.ple_tree_attention_workspace(20, 8, 2, 64).shape[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    block = torch.empty(size, dtype=torch.uint8, device=DEV)
+    taken = block.data_ptr()
+    del block
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # some tens of ms
+    ple.ple_tree_attention(*call, out=out, stream=side)
+    again = torch.empty(size, dtype=torch.uint8, device=DEV)
+    assert not side.query() and again.data_ptr() != taken
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_attention_strided_queries_and_preallocated_outputs():
     rng = np.random.default_rng(14)
     q, cache, ctx, cu, masks = attention_inputs(rng, [9, 30], [77, 500], 8, 4, 64, 32,
