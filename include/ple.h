@@ -448,7 +448,10 @@ int64_t ple_small_batch_max_rows(void);
  * or written, whatever the page table holds: at another page number, or past
  * the table's max_pages, an append or a move is dropped and keys and values
  * read as zeros; tokens past max_pages * page_size are not seen.  No page may
- * hold tokens of two requests that one call writes.
+ * hold tokens of two requests that one call writes.  Tokens from cu_seqlens[B]
+ * on (padding, as of a captured graph's fixed T) are nodes of no request:
+ * nothing is appended for them, and what the other calls write for them is
+ * unspecified.
  */
 
 /*

@@ -206,11 +206,13 @@ qk_norm_rope_kernel(const __grid_constant__ ple_qk_norm_rope_args a, const RowPl
         for (int k = warp; k < nt; k += kWarps) {
             const int r = warp_request(a.cu_seqlens, a.num_requests, t0 + k, lane);
             if (lane == 0) {
+                // a token past the last request's is padding: it has no slot
                 const int64_t place = t0 + k - max(__ldg(a.cu_seqlens + r), 0);
-                dst_s[k] = place < 0 ? -1
-                                     : slot_offset(a.page_table, a.max_pages, a.page_size,
-                                                   a.num_pages, a.page_stride, a.slot_stride, r,
-                                                   __ldg(a.ctx_lens + r) + place);
+                const bool node = place >= 0 && t0 + k < __ldg(a.cu_seqlens + r + 1);
+                dst_s[k] = node ? slot_offset(a.page_table, a.max_pages, a.page_size, a.num_pages,
+                                              a.page_stride, a.slot_stride, r,
+                                              __ldg(a.ctx_lens + r) + place)
+                                : -1;
             }
         }
     }

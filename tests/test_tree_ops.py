@@ -332,6 +332,20 @@ def test_append_outside_the_page_table_is_dropped():
     assert torch.equal(cache.v[int(cache.table[0, 0]), 0, 4:], v[:12, 0])
 
 
+def test_padding_tokens_append_nothing():
+    # seven tokens of a fixed shape, four of them nodes; the last request has room behind its own
+    rng = np.random.default_rng(19)
+    q, k, v = (rows(rng, (7, 1, 64), torch.float16) for _ in range(3))
+    cache = Cache(rng, [16, 32], 16, 1, 64, torch.float16)
+    ple.ple_qk_norm_rope(q, k, v, None, None, k_cache=cache.k, v_cache=cache.v,
+                         page_table=dev(cache.table), ctx_lens=dev(np.array([4, 9], np.int32)),
+                         cu_seqlens=dev(np.array([0, 3, 4], np.int32)))
+    assert int((~cache.v.isnan().all(-1)).sum()) == 4
+    assert int((~cache.k.isnan().all(-1)).sum()) == 4
+    assert torch.equal(cache.v[int(cache.table[0, 0]), 0, 4:7], v[:3, 0])
+    assert torch.equal(cache.v[int(cache.table[1, 0]), 0, 9], v[3, 0])
+
+
 # ------------------------------------------------------------------ attention
 
 
