@@ -580,7 +580,10 @@ ple_status ple_qk_norm_rope(const ple_qk_norm_rope_args* args, void* stream);
  * that is not seen holds (infinities and NaN too) has no effect.  A request of
  * one node is an ordinary decode step.
  * Scores, the softmax's maximum and sum, and the output are held in 32 bits;
- * the weights p enter the product with v in the element dtype.
+ * the weights p enter the product with v in the element dtype: to 2^-8 of a
+ * weight in bfloat16; in float16 to 2^-11 of it, or to 2^-28 of the largest
+ * among the 128 slots around it, however far below the row's largest those
+ * are (not under 2^-50 of the row's sum).
  */
 typedef struct {
     const void* q;                  /* [T, q_heads, D], last dimension contiguous */

@@ -9,9 +9,9 @@
 //   P = exp2(c S - c m), m the running row maximum, c = scale * log2(e)
 //   O = O + P V      (P written over S in tensor memory, O beside it)
 // with the row sums of P kept in registers: the one-pass softmax of Milakov and
-// Gimelshein (2018).  O is scaled anew only when a row's maximum has grown by
-// more than 8 in the exponent since it was last set: until then P stays below
-// 2^8 and the sum and O share the old maximum, so nothing is lost.
+// Gimelshein (2018).  As is known of it, m need not be the maximum: any reference
+// that the sum and O share will do, so O is scaled anew only when a tile's maximum
+// is more than a few binades away from the row's reference (Reference below).
 //
 // Blocks.  One block an SM: two warps that copy key and value tiles into a ring
 // of shared memory (tiled bulk copies, page by page, 128-byte swizzle), a warp
@@ -31,7 +31,7 @@
 // unit behind a few places for what it costs besides its tiles, and cut into equal
 // shares, one a block, so ragged requests and few long ones fill the device
 // alike.  A block writes a unit that it has whole; of a cut unit it writes the
-// state (row maximum, sum, O in 32 bits) to the workspace, and a second kernel
+// state (row reference, sum, O in 32 bits) to the workspace, and a second kernel
 // joins the states in block order: results do not depend on timing.
 //
 // Measured (bf16, heads of 128, 8 key heads, 64-slot pages, the join with it).  Up
@@ -64,7 +64,27 @@ constexpr int kTile = 128;           // keys a tile, rows a matrix instruction
 constexpr int kThreads = 384;        // two groups of 128 and four warps of a task each
 constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10, kWalkWarp = 11;
 constexpr int kMaxBlocks = 1024;     // blocks of a launch: an SM's number of them is far below
-constexpr float kLag = 8.0f;         // how far, in the exponent, a maximum may lag
+
+// How far a tile's largest weight may lie above and below 1 (in the exponent of 2)
+// before the row's reference moves to it, and where weights are placed in the element
+// type: P = 2^kBias times the weight.  bfloat16 has the exponents of 32 bits, so a
+// reference only ever rises.  float16 ends at 2^16 and 2^-25: weights are placed
+// under its upper end, and the reference also falls to a tile whose largest weight is
+// small, so that a weight enters the product to 2^-11 of itself or to 2^-28 of its
+// tile's largest, however far below the row's largest that lies (behind an attention
+// sink all of them do).  Closer limits cost more moves, wider ones more of the small
+// weights.  512 rows over 131000 slots in float16, scores of a standard deviation of
+// 1.5: 212 us with these limits and with a rise of 8 alone; of 6: 231 to 243 against 217
+// to 226.
+template <bool kBf16>
+struct Reference {
+    static constexpr float kRise = kBf16 ? 8.0f : 5.0f;
+    static constexpr float kFall = 7.0f;
+    static constexpr float kBias = kBf16 ? 0.0f : 10.0f;
+};
+// A reference falls only while the row's sum stays below this: a tile that would take
+// it further has no weight above 2^-50 of the row's, and O stays far inside 32 bits.
+constexpr float kMostSum = 0x1p60f;
 
 // D is a head's width in shared memory: 64, 128 or 256.
 __host__ __device__ constexpr int padded_width(int head_dim) {
@@ -289,7 +309,7 @@ struct Cut {
 
 // The workspace: each block's cut, then two states a block (0: a unit begun
 // before the block, 1: a unit that starts in it).  A state is a pair
-// (row maximum in the exponent of 2, row sum) for each row, then the accumulators
+// (row reference in the exponent of 2, row sum) for each row, then the accumulators
 // as [D / 8][row][8]: neighbouring threads write, and a row's readers read, whole
 // 32-byte sectors.
 __host__ __device__ __forceinline__ int64_t state_at(int64_t block, int slot, int rows_cap,
@@ -405,6 +425,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                          const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map) {
     using S = Shape<D>;
+    using R = Reference<kBf16>;
     const ple_tree_attention_args& a = args.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
@@ -873,11 +894,15 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                         m = max3(m, m0, m1);
                     }
-                    // a new maximum only where it grew by more than kLag
-                    const bool grow = here && (m - top) * c > kLag;
+                    // a new reference only where the tile's maximum is far from it
+                    const bool grow = here && (m - top) * c > R::kRise;
                     const bool set = here && top == -INFINITY && m > -INFINITY;
-                    if (__any_sync(0xffffffffu, grow || set)) {
-                        const bool move = grow || set;
+                    bool move = grow || set;
+                    if constexpr (!kBf16) {
+                        const float fall = (top - m) * c;
+                        move |= here && fall > R::kFall && sum * exp2_fast(fall) < kMostSum;
+                    }
+                    if (__any_sync(0xffffffffu, move)) {
                         const float f = move ? (set ? 0.f : exp2_fast((top - m) * c)) : 1.f;
                         if (move) top = m;
                         sum *= f;
@@ -898,7 +923,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     }
                     // rows that have seen nothing yet have only -infinities:
                     // exponents relative to 0 make zeros of them
-                    const float shift = top == -INFINITY ? 0.f : top * c;
+                    const float shift = top == -INFINITY ? 0.f : fmaf(top, c, -R::kBias);
                     const uint64_t c2 = pack_f32(c, c), shift2 = pack_f32(-shift, -shift);
                     uint64_t part[2] = {0, 0};
 #pragma unroll
@@ -1077,11 +1102,13 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                     }
                     if (here && column0 == 0) {
                         if (!whole) {
-                            pairs[0] = top == -INFINITY ? -INFINITY : top * c;
+                            pairs[0] = fmaf(top, c, -R::kBias);
                             pairs[1] = sum;
                         } else if (a.lse != nullptr) {
-                            a.lse[o_row] = sum == 0.f ? -INFINITY
-                                                      : top * c * 0.69314718055994531f + logf(sum);
+                            a.lse[o_row] = sum == 0.f
+                                               ? -INFINITY
+                                               : fmaf(top, c, -R::kBias) * 0.69314718055994531f +
+                                                     logf(sum);
                         }
                     }
                 }
