@@ -145,6 +145,21 @@ def _stream_handle(stream, device) -> int:
     return int(stream.cuda_stream)
 
 
+def _lend(stream, device, *tensors):
+    """Let a call on `stream` use tensors that it took from the current stream's
+    memory: their blocks may still be in use by work queued there, so `stream`
+    waits for it, and they are not handed out again before `stream` is done
+    with them.  A call that allocates nothing makes no stream wait."""
+    if stream is None or not tensors:
+        return
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return
+    stream.wait_stream(current)
+    for t in tensors:
+        t.record_stream(stream)
+
+
 def _ptr(t: torch.Tensor):
     return ctypes.c_void_p(t.data_ptr()) if t.numel() else ctypes.c_void_p(0)
 

@@ -15,6 +15,11 @@ makes most of these calls once per layer, and a small one lasts a few
 microseconds on the device, so each function first tests its arguments in one
 expression; only when that fails do the checks that name the culprit run.
 
+`stream` defaults to the device's current stream.  Outputs and workspaces that
+a call is not given come from torch's allocator, from the current stream's
+memory: on another stream such a call first makes that stream wait for the
+current one.  A caller that orders the streams itself passes them all.
+
 Caches are [pages, kv_heads, page_size, head_dim] views (for the commit of
 several layers [layers, pages, kv_heads, page_size, head_dim]): any strides
 that are multiples of 8 elements with the last dimension contiguous, the same
@@ -28,7 +33,8 @@ import struct
 import torch
 
 from .binding import (PLE_BF16, PLE_F16, PLE_HEAD_BYTES, PLE_I32, PLE_I64, PLE_OK,
-                      PLE_ROPE_BASE, PLE_ROPE_LINEAR, PLE_ROPE_PARTS, PLE_ROPE_PLAIN, _check, lib)
+                      PLE_ROPE_BASE, PLE_ROPE_LINEAR, PLE_ROPE_PARTS, PLE_ROPE_PLAIN, _check, _lend,
+                      lib)
 
 ROPE_SCALINGS = {"plain": PLE_ROPE_PLAIN, "linear": PLE_ROPE_LINEAR, "base": PLE_ROPE_BASE,
                  "parts": PLE_ROPE_PARTS}
@@ -147,10 +153,14 @@ def ple_build_tree_index(parent: torch.Tensor, cu_seqlens: torch.Tensor, ctx_len
             _table(tree_mask, _i64, T, "tree_mask", where)
             if tree_mask.shape[1] != W:
                 raise ValueError(f"{where}: tree_mask must be [T, mask_words]")
+    made = []
     if positions is None:
         positions = _empty(T, dtype=_i32, device=parent.device)
+        made.append(positions)
     if tree_mask is None:
         tree_mask = _empty((T, max(W, 0)), dtype=_i64, device=parent.device)
+        made.append(tree_mask)
+    _lend(stream, dev, *made)
     _call(where, lib().ple_build_tree_index, dev, stream, parent.data_ptr(),
           cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, T, W, positions.data_ptr(),
           tree_mask.data_ptr())
@@ -215,6 +225,7 @@ def ple_tree_row_ids(input_ids: torch.Tensor, parent: torch.Tensor, cu_seqlens: 
     L, H = shape
     if out is None:
         out = _empty((L, T, H), dtype=out_dtype, device=input_ids.device)
+        _lend(stream, dev, out)
     _call(where, lib().ple_tree_row_ids, dev, stream, input_ids.data_ptr(), ids, T,
           parent.data_ptr(), cu_seqlens.data_ptr(), ngram_context.data_ptr(), B, C, M.data_ptr(),
           vocab.data_ptr(), off.data_ptr(), H, N, int(heads_per_ngram), L, int(boundary_id),
@@ -244,6 +255,7 @@ def ple_prepare_rope(rotary_dim: int, base: float = 10000.0, scaling: str = "pla
         if device.type != "cuda":
             raise ValueError(f"{where}: the rotation is kept on a CUDA device, got {device}")
         out = torch.empty(max(R // 2, 0), dtype=torch.int64, device=device)
+        _lend(stream, device, out)
     dev = _device(where, out)
     _vector(out, torch.int64, R // 2, "out", where)
     _call(where, lib().ple_prepare_rope, dev, stream, R, float(base), ROPE_SCALINGS[scaling],
@@ -323,6 +335,7 @@ def ple_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
                  and ctx_lens.is_contiguous() and cu_seqlens.is_contiguous())
     if quick:
         q_out = _empty(q_shape, dtype=dtype, device=q.device)
+        _lend(stream, dev, q_out)
         args = _NORM_ROPE.pack(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], v_strides[0],
             v_strides[1], positions.data_ptr(), rope.data_ptr(), q_weight.data_ptr(),
@@ -346,8 +359,10 @@ def ple_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             _vector(w, dtype, D, name, where)
+    made = []
     if q_out is None:
         q_out = _empty((T, Hq, D), dtype=dtype, device=q.device)
+        made.append(q_out)
     else:
         _heads(q_out, dtype, T, Hq, D, "q_out", where)
     pages = B = 0
@@ -376,9 +391,11 @@ def ple_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
             raise ValueError(f"{where}: pass both caches or neither")
         if k_out is None:
             k_out = _empty((T, Hk, D), dtype=dtype, device=q.device)
+            made.append(k_out)
         else:
             _heads(k_out, dtype, T, Hk, D, "k_out", where)
         k_out_strides = k_out.stride()
+    _lend(stream, dev, *made)
     os = q_out.stride()
     args = _NORM_ROPE.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr() if cached else 0, qs[0], qs[1], ks[0], ks[1],
@@ -474,10 +491,13 @@ def ple_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                                       or not workspace.is_contiguous()):
             raise ValueError(f"{where}: workspace must be a contiguous uint8 tensor")
     device = q.device
+    made = []
     if out is None:
         out = _empty((T, Hq, D), dtype=dtype, device=device)
+        made.append(out)
     if lse is None and return_lse:
         lse = _empty((T, Hq), dtype=torch.float32, device=device)
+        made.append(lse)
     if workspace is None:
         sizes = (T, Hq, Hk, D, dev)
         size = _workspace_sizes.get(sizes)
@@ -488,9 +508,8 @@ def ple_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                 size = max(lib().ple_tree_attention_workspace(T, Hq, Hk, D), 0)
             _workspace_sizes[sizes] = size
         workspace = _empty(size, dtype=torch.uint8, device=device)
-        if stream is not None:
-            # freed on return, while the kernels on the other stream use it
-            workspace.record_stream(stream)
+        made.append(workspace)
+    _lend(stream, dev, *made)
     args = _ATTENTION.pack(
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), strides[0],
         strides[1], strides[2], pages, page_table.data_ptr(), ctx_lens.data_ptr(),
@@ -566,10 +585,14 @@ def ple_tree_commit(input_ids: torch.Tensor, path: torch.Tensor, accepted: torch
         if next_ctx_lens is not None:
             _vector(next_ctx_lens, _i32, B, "next_ctx_lens", where)
     C = 0 if ngram_context is None else ngram_context.shape[1]
+    made = []
     if next_context is None and ngram_context is not None:
         next_context = _empty((B, C), dtype=kind, device=input_ids.device)
+        made.append(next_context)
     if next_ctx_lens is None:
         next_ctx_lens = _empty(B, dtype=_i32, device=input_ids.device)
+        made.append(next_ctx_lens)
+    _lend(stream, dev, *made)
     L, pages, Hk, page_size, D = cache_shape
     args = _COMMIT.pack(
         input_ids.data_ptr(), path.data_ptr(), accepted.data_ptr(), cu_seqlens.data_ptr(),
