@@ -194,10 +194,13 @@ def ple_build_token_index(cu_seqlens, num_requests: int, num_tokens: int, is_dec
     dev = torch.device(device) if device is not None else _one_cuda_device(tensors, where)
     if tensors:
         _one_cuda_device(tensors + [torch.empty(0, device=dev)], where)
+    made = []
     if req is None:
         req = torch.empty(T, dtype=torch.int32, device=dev)
+        made.append(req)
     if local is None:
         local = torch.empty(T, dtype=torch.int32, device=dev)
+        made.append(local)
     for name, t in (("req", req), ("local", local)):
         _need(t, torch.int32, name, where)
         if t.numel() != T:
@@ -208,6 +211,7 @@ def ple_build_token_index(cu_seqlens, num_requests: int, num_tokens: int, is_dec
         if cu_seqlens.numel() != int(num_requests) + 1:
             raise ValueError(f"{where}: cu_seqlens must have num_requests + 1 elements")
         cu_p = _ptr(cu_seqlens)
+    _lend(stream, dev, *made)
     with torch.cuda.device(dev):
         st = lib().ple_build_token_index(cu_p, int(num_requests), T, int(bool(is_decode)),
                                          _ptr(req), _ptr(local), _stream_handle(stream, dev))
@@ -263,10 +267,13 @@ def ple_shard_inputs(input_ids: torch.Tensor, cu_seqlens: torch.Tensor,
         raise ValueError(f"{where}: cu_seqlens must have num_requests + 1 elements")
     if not 0 <= tb < te <= input_ids.numel() or rb < 0 or rc < 1 or rb + rc > B:
         raise ValueError(f"{where}: the plan does not fit this batch (or the share is empty)")
+    made = []
     if shard_cu_seqlens is None:
         shard_cu_seqlens = torch.empty(max(rc, 0) + 1, dtype=torch.int32, device=dev)
+        made.append(shard_cu_seqlens)
     if shard_context is None:
         shard_context = torch.empty((max(rc, 0), C), dtype=input_ids.dtype, device=dev)
+        made.append(shard_context)
     _one_cuda_device([input_ids, shard_cu_seqlens, shard_context], where)
     if shard_cu_seqlens.numel() != rc + 1 or tuple(shard_context.shape) != (rc, C):
         raise ValueError(f"{where}: outputs must be [request_count + 1] and [request_count, C]")
@@ -276,6 +283,7 @@ def ple_shard_inputs(input_ids: torch.Tensor, cu_seqlens: torch.Tensor,
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
     dt = PLE_I32 if input_ids.dtype == torch.int32 else PLE_I64
+    _lend(stream, dev, *made)
     with torch.cuda.device(dev):
         st = lib().ple_shard_inputs(_ptr(input_ids), dt, _ptr(cu_seqlens), _ptr(ngram_context),
                                     int(B), int(input_ids.numel()), int(C), tb, te, rb, rc,
@@ -356,6 +364,7 @@ def ple_row_ids(input_ids: torch.Tensor, req: torch.Tensor | None, local: torch.
                              f"{PLE_HEAD_BYTES}] on the ids' device")
     if out is None:
         out = torch.empty((L, T, H), dtype=out_dtype, device=dev)
+        _lend(stream, dev, out)
     else:
         _need(out, out_dtype, "out", where)
         if tuple(out.shape) not in ((L, T, H),) + (((T, H),) if L == 1 else ()):
@@ -412,6 +421,7 @@ def ple_prepare_heads(vocab_sizes: torch.Tensor, offsets: torch.Tensor,
     L, H = vocab.shape
     if out is None:
         out = torch.empty((L, H, PLE_HEAD_BYTES), dtype=torch.uint8, device=dev)
+        _lend(stream, dev, out)
     else:
         _need(out, torch.uint8, "out", where)
         if tuple(out.shape) != (L, H, PLE_HEAD_BYTES):
@@ -463,6 +473,7 @@ def ple_row_embed(input_ids: torch.Tensor, req: torch.Tensor | None, local: torc
             _need(t, torch.int32, name, where)
     if out is None:
         out = torch.empty((L, T, D), dtype=torch.float32, device=dev)
+        _lend(stream, dev, out)
     else:
         _need(out, torch.float32, "out", where)
         if tuple(out.shape) != (L, T, D):
@@ -507,6 +518,7 @@ def ple_validate_index(cu_seqlens, num_requests: int, num_tokens: int, is_decode
     if not is_decode:
         _need(cu_seqlens, torch.int32, "cu_seqlens", where)
         cu_p = _ptr(cu_seqlens)
+    _lend(stream, dev, first_bad)  # filled on the current stream
     with torch.cuda.device(dev):
         st = lib().ple_validate_index(cu_p, int(num_requests), int(num_tokens),
                                       int(bool(is_decode)), _ptr(req), _ptr(local),
@@ -525,6 +537,7 @@ def ple_selftest_floor_mod(x: torch.Tensor, v: torch.Tensor, stream=None):
         raise ValueError(f"{where}: x and v must have one shape")
     fast = torch.empty_like(x)
     ref = torch.empty_like(x)
+    _lend(stream, dev, fast, ref)
     with torch.cuda.device(dev):
         st = lib().ple_selftest_floor_mod(_ptr(x), _ptr(v), x.numel(), _ptr(fast), _ptr(ref),
                                           _stream_handle(stream, dev))
