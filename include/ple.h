@@ -631,6 +631,9 @@ int64_t ple_tree_attention_workspace(int64_t num_tokens, int32_t q_heads, int32_
  * path[r] lists nodes of the request in ascending order.  accepted is clamped
  * to [0, path_len] and to the request's nodes; an entry of path below its own
  * place or past the request's nodes leaves its slot as it is.
+ * next_ctx_lens and next_context overlap none of the arguments that are read,
+ * nor each other (PLE_ERR_SIZE): a step that keeps its state in one place
+ * copies them there afterwards.
  */
 typedef struct {
     const void* input_ids;          /* [T], id_dtype */
@@ -638,9 +641,9 @@ typedef struct {
     const int32_t* accepted;        /* [B] */
     const int32_t* cu_seqlens;      /* [B + 1] */
     const void* ngram_context;      /* [B, ctx_len], id_dtype; NULL: no context is carried */
-    void* next_context;             /* [B, ctx_len], not overlapping ngram_context */
+    void* next_context;             /* [B, ctx_len] */
     const int32_t* ctx_lens;        /* [B] */
-    int32_t* next_ctx_lens;         /* [B]; must not overlap ctx_lens */
+    int32_t* next_ctx_lens;         /* [B] */
     const int32_t* page_table;      /* [B, max_pages] */
     void *k_cache, *v_cache;        /* num_layers caches each, layer_stride elements apart */
     int64_t layer_stride, page_stride, head_stride, slot_stride;

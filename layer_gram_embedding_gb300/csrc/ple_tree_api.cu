@@ -36,6 +36,12 @@ bool cache_sizes_ok(int64_t num_pages, int64_t page_stride, int64_t head_stride,
     return span <= INT64_MAX / 8 && (int64_t)max_pages * page_size <= INT32_MAX;
 }
 
+// Whether [a, a + n) and [b, b + m), in bytes, share one.
+bool overlap(const void* a, __int128 n, const void* b, __int128 m) {
+    const __int128 x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
 bool rows_ok(int64_t T, int64_t token, int32_t heads, int64_t head, int32_t dim) {
     if (token < 0 || head < 0) return false;
     return heads == 0 || (__int128)(T - 1) * token + (__int128)(heads - 1) * head + dim <=
@@ -260,6 +266,25 @@ extern "C" ple_status ple_tree_commit(const ple_tree_commit_args* args, void* st
                              !aligned(a.ngram_context, id_bytes) ||
                              !aligned(a.next_context, id_bytes))))
         return PLE_ERR_ALIGN;
+    // a request's blocks, one a layer and cache, run in any order: what one of them
+    // writes for the next step may be nothing that another still reads
+    const __int128 B = a.num_requests;
+    const __int128 context = a.ngram_context ? B * a.ctx_len * id_bytes : 0;
+    const struct {
+        const void* at;
+        __int128 bytes;
+    } out[] = {{a.next_ctx_lens, 4 * B}, {a.next_context, context}},
+      in[] = {{a.input_ids, context ? (__int128)a.num_tokens * id_bytes : 0},
+              {a.path, 4 * B * a.path_len},
+              {a.accepted, 4 * B},
+              {a.cu_seqlens, 4 * (B + 1)},
+              {a.ngram_context, context},
+              {a.ctx_lens, 4 * B},
+              {a.page_table, 4 * B * a.max_pages}};
+    if (overlap(out[0].at, out[0].bytes, out[1].at, out[1].bytes)) return PLE_ERR_SIZE;
+    for (const auto& o : out)
+        for (const auto& i : in)
+            if (overlap(o.at, o.bytes, i.at, i.bytes)) return PLE_ERR_SIZE;
     ple::DeviceFacts dev;
     if (ple_status st = with_device(&dev); st != PLE_OK) return st;
     return finish(ple::launch_tree_commit(a, dev, static_cast<cudaStream_t>(stream)));

@@ -117,6 +117,13 @@ def _caches(k: torch.Tensor, v: torch.Tensor, dtype, dims: int, where: str):
     return strides
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two contiguous tensors share a byte."""
+    x, y = a.data_ptr(), b.data_ptr()
+    n, m = a.numel() * a.element_size(), b.numel() * b.element_size()
+    return n > 0 and m > 0 and x < y + m and y < x + n
+
+
 def _element(t: torch.Tensor, name: str, where: str) -> int:
     code = _ELEMENTS.get(t.dtype)
     if code is None:
@@ -534,7 +541,9 @@ def ple_tree_commit(input_ids: torch.Tensor, path: torch.Tensor, accepted: torch
     kv_heads, page_size, head_dim], or one layer's four dimensions), in place;
     next_ctx_lens [B] is the cached length after that, and next_context
     [B, ngram_size - 1] what the next step passes as its ngram_context (None
-    when ngram_context is None)."""
+    when ngram_context is None).  Where given, the two must not overlap each
+    other or an argument that is read, ctx_lens and ngram_context among them:
+    a captured step copies them back behind the call."""
     where = "ple_tree_commit"
     dev = input_ids.get_device()
     if k_cache.dim() == 4 and v_cache.dim() == 4:
@@ -584,6 +593,13 @@ def ple_tree_commit(input_ids: torch.Tensor, path: torch.Tensor, accepted: torch
             raise ValueError(f"{where}: next_context needs ngram_context")
         if next_ctx_lens is not None:
             _vector(next_ctx_lens, _i32, B, "next_ctx_lens", where)
+        for name, t in (("next_context", next_context), ("next_ctx_lens", next_ctx_lens)):
+            for other, u in (("input_ids", input_ids), ("path", path), ("accepted", accepted),
+                             ("cu_seqlens", cu_seqlens), ("ngram_context", ngram_context),
+                             ("ctx_lens", ctx_lens), ("page_table", page_table),
+                             ("next_ctx_lens", next_ctx_lens)):
+                if t is not None and u is not None and name != other and _overlap(t, u):
+                    raise ValueError(f"{where}: {name} must not overlap {other}")
     C = 0 if ngram_context is None else ngram_context.shape[1]
     made = []
     if next_context is None and ngram_context is not None:
