@@ -423,6 +423,21 @@ def ple_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
 _workspace_sizes: dict = {}
 
 
+def _workspace_size(*sizes) -> int:
+    """The bytes of a call's own workspace.  A query that failed is no answer:
+    it is not kept, and the call itself says what is wrong."""
+    size = _workspace_sizes.get(sizes)
+    if size is None:
+        with torch.cuda.device(sizes[4]):
+            size = lib().ple_tree_attention_workspace(*sizes[:4])
+        if size < 0:
+            return 0
+        if len(_workspace_sizes) >= 4096:
+            _workspace_sizes.clear()
+        _workspace_sizes[sizes] = size
+    return size
+
+
 def ple_tree_attention_workspace(num_tokens: int, q_heads: int, kv_heads: int, head_dim: int,
                                  device=None) -> torch.Tensor:
     """A uint8 workspace for ple_tree_attention calls of these sizes (or fewer
@@ -506,15 +521,7 @@ def ple_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         lse = _empty((T, Hq), dtype=torch.float32, device=device)
         made.append(lse)
     if workspace is None:
-        sizes = (T, Hq, Hk, D, dev)
-        size = _workspace_sizes.get(sizes)
-        if size is None:
-            if len(_workspace_sizes) >= 4096:
-                _workspace_sizes.clear()
-            with torch.cuda.device(dev):
-                size = max(lib().ple_tree_attention_workspace(T, Hq, Hk, D), 0)
-            _workspace_sizes[sizes] = size
-        workspace = _empty(size, dtype=torch.uint8, device=device)
+        workspace = _empty(_workspace_size(T, Hq, Hk, D, dev), dtype=torch.uint8, device=device)
         made.append(workspace)
     _lend(stream, dev, *made)
     args = _ATTENTION.pack(
