@@ -637,7 +637,7 @@ int64_t ple_tree_attention_workspace(int64_t num_tokens, int32_t q_heads, int32_
  */
 typedef struct {
     const void* input_ids;          /* [T], id_dtype */
-    const int32_t* path;            /* [B, path_len] */
+    const int32_t* path;            /* [B, path_len]; NULL when path_len is 0 */
     const int32_t* accepted;        /* [B] */
     const int32_t* cu_seqlens;      /* [B + 1] */
     const void* ngram_context;      /* [B, ctx_len], id_dtype; NULL: no context is carried */
@@ -650,7 +650,7 @@ typedef struct {
     int64_t num_pages;
     int64_t num_tokens;             /* T, 0 <= T <= INT32_MAX */
     int32_t num_requests;           /* B >= 0; 0: nothing to do */
-    int32_t path_len;               /* >= 1 */
+    int32_t path_len;               /* >= 0; 0: no node is kept */
     int32_t id_dtype;               /* ple_id_dtype */
     int32_t ctx_len;                /* 1 .. PLE_MAX_NGRAM - 1 (with a context) */
     int32_t num_layers;             /* 1 .. 65535 */

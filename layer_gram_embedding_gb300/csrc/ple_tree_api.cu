@@ -242,9 +242,9 @@ extern "C" ple_status ple_tree_attention(const ple_tree_attention_args* args, vo
 extern "C" ple_status ple_tree_commit(const ple_tree_commit_args* args, void* stream) {
     if (!args) return PLE_ERR_NULL;
     const ple_tree_commit_args& a = *args;
-    if (a.num_tokens < 0 || a.num_tokens > INT32_MAX || a.num_requests < 0 || a.path_len < 1 ||
-        a.num_layers < 1 || a.num_layers > 65535 || !head_dim_ok(a.head_dim) ||
-        a.layer_stride < 0 ||
+    if (a.num_tokens < 0 || a.num_tokens > INT32_MAX || a.num_requests < 0 || a.path_len < 0 ||
+        (a.path_len == 0 && a.path) || a.num_layers < 1 || a.num_layers > 65535 ||
+        !head_dim_ok(a.head_dim) || a.layer_stride < 0 ||
         !cache_sizes_ok(a.num_pages, a.page_stride, a.head_stride, a.slot_stride, a.kv_heads,
                         a.page_size, a.max_pages, a.head_dim) ||
         (__int128)(a.num_layers - 1) * a.layer_stride > INT64_MAX / 16)
@@ -253,8 +253,8 @@ extern "C" ple_status ple_tree_commit(const ple_tree_commit_args* args, void* st
     if (a.ngram_context && a.id_dtype != PLE_I32 && a.id_dtype != PLE_I64) return PLE_ERR_DTYPE;
     if (!dtype_ok(a.dtype)) return PLE_ERR_ELEMENT;
     if (a.num_requests == 0) return PLE_OK;
-    if (!a.path || !a.accepted || !a.cu_seqlens || !a.ctx_lens || !a.next_ctx_lens ||
-        !a.page_table || !a.k_cache || !a.v_cache ||
+    if ((!a.path && a.path_len) || !a.accepted || !a.cu_seqlens || !a.ctx_lens ||
+        !a.next_ctx_lens || !a.page_table || !a.k_cache || !a.v_cache ||
         (a.ngram_context && ((!a.input_ids && a.num_tokens) || !a.next_context)))
         return PLE_ERR_NULL;
     const int id_bytes = a.id_dtype == PLE_I32 ? 4 : 8;

@@ -542,8 +542,8 @@ def ple_tree_commit(input_ids: torch.Tensor, path: torch.Tensor, accepted: torch
                     next_ctx_lens: torch.Tensor | None = None, stream=None):
     """(next_context, next_ctx_lens): keep the accepted branches.
 
-    path [B, P] int32: the kept nodes of each request, ascending; accepted [B]
-    int32: how many of them.  Their keys and values move together behind the
+    path [B, P] int32: the kept nodes of each request, ascending (P may be 0);
+    accepted [B] int32: how many of them.  Their keys and values move together behind the
     request's cached tokens, in every layer of the caches ([layers, pages,
     kv_heads, page_size, head_dim], or one layer's four dimensions), in place;
     next_ctx_lens [B] is the cached length after that, and next_context
@@ -618,9 +618,9 @@ def ple_tree_commit(input_ids: torch.Tensor, path: torch.Tensor, accepted: torch
     _lend(stream, dev, *made)
     L, pages, Hk, page_size, D = cache_shape
     args = _COMMIT.pack(
-        input_ids.data_ptr(), path.data_ptr(), accepted.data_ptr(), cu_seqlens.data_ptr(),
-        0 if C == 0 else ngram_context.data_ptr(), 0 if C == 0 else next_context.data_ptr(),
-        ctx_lens.data_ptr(), next_ctx_lens.data_ptr(), page_table.data_ptr(), k_cache.data_ptr(),
+        input_ids.data_ptr(), path.data_ptr() if path_shape[1] else 0, accepted.data_ptr(),
+        cu_seqlens.data_ptr(), 0 if C == 0 else ngram_context.data_ptr(),
+        0 if C == 0 else next_context.data_ptr(), ctx_lens.data_ptr(), next_ctx_lens.data_ptr(), page_table.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), strides[0], strides[1], strides[2], strides[3], pages, T, B,
         path_shape[1], ids, C, L, table_shape[1], page_size, Hk, D, element)
     _call(where, lib().ple_tree_commit, dev, stream, args)
