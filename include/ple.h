@@ -505,8 +505,15 @@ ple_status ple_tree_row_ids(const void* input_ids, int32_t id_dtype, int64_t num
  *                    trained context and g = clamp((r_i - beta_slow) /
  *                    (beta_fast - beta_slow), 0, 1): g w_i + (1 - g) w_i / s
  *                    (interpolation "by parts", Peng et al. 2023).
+ * The ramp of the last one runs over turns, as that paper defines it.  Code in
+ * use for checkpoints with such a scaling may ramp over the pairs' indices
+ * instead, between the pairs that make beta_fast and beta_slow turns: those are
+ * other angles (with 32 and 1, a pair of 5.7 turns mixes 0.15 here, 0.5 there),
+ * and take a table of their own.
  * It is kept as a whole number of 2^-64 turns, so that the angle at any
- * position is one wrapping 64-bit product, with no loss at long contexts.
+ * position is one wrapping 64-bit product, with no loss at long contexts.  A
+ * caller with other frequencies fills the table itself: entry i is
+ * w_i / 2 pi * 2^64 modulo 2^64, w_i in radians a position.
  *
  *   rotary_dim   R, even, 2 <= R <= PLE_MAX_HEAD_DIM.
  *   base >= 1, factor >= 1; with PLE_ROPE_PARTS trained_positions > 0 and
@@ -584,6 +591,8 @@ ple_status ple_qk_norm_rope(const ple_qk_norm_rope_args* args, void* stream);
  * weight in bfloat16; in float16 to 2^-11 of it, or to 2^-28 of the largest
  * among the 128 slots around it, however far below the row's largest those
  * are (not under 2^-50 of the row's sum).
+ * The kernels' waits end after about a second, which no sound run comes near;
+ * the rows of a block in which one ran out are NaN.
  */
 typedef struct {
     const void* q;                  /* [T, q_heads, D], last dimension contiguous */

@@ -20,7 +20,9 @@
 // side by side, else four and the four half the rotary part behind them.  A block
 // takes up to eight tokens: their sines and cosines are computed once and shared
 // by all their heads.  Bound by the rows' bytes, each read and written once: 64
-// drafted trees (43 MB, in L2) take 13.5 us, one token 3.0.
+// drafted trees (43 MB, in L2) take 13.5 us, one token 3.0.  The trees' 1057 tokens
+// go one to a block, and as many blocks are 1.4 times what the device holds at once:
+// the second wave, mostly empty, is a part of that time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -38,10 +38,10 @@
 // to 128 rows a unit the keys' and values' bytes bound it: 4 rows over 32 x 16384
 // slots 316 us (6.8 TB/s), 128 rows 335 us.  Above, the chain of one group's softmax, its second
 // product and its next first one does (some 3500 clocks a tile, 2048 of them the
-// tensor cores' for both groups): 256 rows 391 us (1.4 PFLOP/s), 512 rows over
-// 1 x 131000 slots 208 us (1.3 PFLOP/s).  Few keys are a latency: 4 rows over 701
-// slots 11 us.  Heads of 256: 4 rows over 32 x 8192 slots 353 us (6.1 TB/s), 128
-// rows 384, 64 rows over 4 x 8192 slots 73 (4.8 ms on the kernel without tensor
+// tensor cores' for both groups): 256 rows 399 to 409 us (1.4 PFLOP/s), 512 rows over
+// 1 x 131000 slots 204 to 215 us (1.3 PFLOP/s).  Few keys are a latency: 4 rows over 701
+// slots 11 us.  Heads of 256: 4 rows over 32 x 8192 slots 350 us (6.1 TB/s), 128
+// rows 380, 64 rows over 4 x 8192 slots 69 (4.8 ms on the kernel without tensor
 // cores).
 //
 // What is not seen.  Scores outside the mask are replaced by -infinity before
@@ -364,6 +364,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return v;
 }
 
+// The weights are rounded to the element type before the second product, since a
+// matrix instruction's operands share the values' type; the row sums take them as
+// they were.  Two products, the rest of each weight in the second, would cost what
+// the first costs, which is what bounds calls of many rows.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
     uint32_t v;
@@ -664,7 +668,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcArgs args,
                 // lane are looked at together: one by one, behind each other's
                 // stores, a tile took some 5000 clocks and was what long drafts waited
                 // for (512 nodes for each of 8 requests over 512 slots: 187 us, 126 with
-                // this and the masks' words fetched ahead)
+                // this and the masks' words fetched ahead; 142 behind other calls' memory)
                 auto clean = [&](int j, uint32_t slot) {
                     const int first = (s.k0 + j) * kTile;
                     if (first + kTile <= s.q.ctx) return;

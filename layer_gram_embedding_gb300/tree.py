@@ -20,6 +20,10 @@ a call is not given come from torch's allocator, from the current stream's
 memory: on another stream such a call first makes that stream wait for the
 current one.  A caller that orders the streams itself passes them all.
 
+These operators serve and are no part of autograd's graph: outputs never require
+gradients, whatever the inputs do, and what a call writes into caches and given
+outputs does not move their version counters.
+
 Caches are [pages, kv_heads, page_size, head_dim] views (for the commit of
 several layers [layers, pages, kv_heads, page_size, head_dim]): any strides
 that are multiples of 8 elements with the last dimension contiguous, the same
@@ -252,7 +256,12 @@ def ple_prepare_rope(rotary_dim: int, base: float = 10000.0, scaling: str = "pla
     "base" raises the base so that the slowest pair slows by factor, "parts"
     keeps the pairs that turn more than beta_fast times over
     trained_positions, divides those that turn less than beta_slow times, and
-    mixes between (then 0.1 * ln(factor) + 1 is the usual rope_scale)."""
+    mixes between (then 0.1 * ln(factor) + 1 is the usual rope_scale).
+
+    The mix goes linearly over turns (Peng et al. 2023).  A checkpoint whose
+    code ramps linearly over the pairs' indices instead has other angles, and
+    like any other frequencies w [rotary_dim / 2] below pi radians a position they
+    make a table of their own: (w.double() / (2 * pi) * 2.0 ** 64).long()."""
     where = "ple_prepare_rope"
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"{where}: scaling must be one of {sorted(ROPE_SCALINGS)}")
