@@ -674,6 +674,168 @@ typedef struct {
 ple_status ple_tree_commit(const ple_tree_commit_args* args, void* stream);
 
 /*
+ * The cache in 8 bits.  Keys and values may be kept as 8-bit floats (e4m3: bytes of
+ * a sign, four exponent and three significand bits, at most 448, no infinities) with
+ * a scale for each block of tokens and head: a slot stands for element * scale.  The
+ * caches are paged as above, an element a byte, with strides that are multiples of 16
+ * and rows of a multiple of 16 elements.  The scale of head h for slots
+ * [b * block, (b + 1) * block) of page p is at p * page_stride + h * head_stride + b
+ * (+ l * layer_stride in layer l's cache) in elements of the scales, which keys and
+ * values have each for themselves with the same strides.  A scale is positive and
+ * finite; those that the calls write are powers of two, so that a block whose scale
+ * grows keeps its elements but for their least bits.  What the scale of a block holds
+ * of which no slot is seen has no effect.
+ */
+typedef struct {
+    void *k, *v;                    /* bfloat16, 2-byte aligned; attention only reads them */
+    int64_t layer_stride, page_stride, head_stride;  /* in scales; layer_stride: of a commit */
+    int32_t block;                  /* 16, 32, 64 or 128 tokens, a divisor of page_size */
+} ple_cache_scales;
+
+/*
+ * ple_qk_norm_rope_fp8 -- ple_qk_norm_rope with the append to a cache in 8 bits.
+ *
+ * Query rows as there.  For every block of a request's slots that some of its new
+ * tokens go to, and for the keys (after norm and rotation, in 32 bits) and the values
+ * of each head apart:
+ *   s = the least power of two, at least 2^-100, for which no finite amount among the
+ *       block's new tokens is above 448 s;
+ *   where slots below ctx_lens[r] lie in the block, s = max(s, the block's scale), and
+ *   if that grew these slots' elements e become e * (the block's scale / s), rounded;
+ *   element = x / s, rounded to nearest, ties to even; NaN where x is not finite.
+ * Slots behind the request's new tokens keep their bytes.
+ * base.k_out is not looked at; base's caches are required, q_out and q as there.
+ */
+typedef struct {
+    ple_qk_norm_rope_args base;
+    ple_cache_scales scales;
+} ple_qk_norm_rope_fp8_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_ELEMENT, PLE_ERR_NULL, PLE_ERR_ALIGN,
+ * PLE_ERR_CUDA.  One kernel launch. */
+ple_status ple_qk_norm_rope_fp8(const ple_qk_norm_rope_fp8_args* args, void* stream);
+
+/*
+ * ple_tree_attention_fp8 -- ple_tree_attention over a cache in 8 bits.
+ *
+ * Arguments and results as there, base.dtype that of q and out.  Queries enter the
+ * products as halves: exactly in float16, in bfloat16 to 2^-40 of the row's largest
+ * element; elements exactly; scales, scores, the softmax's maximum and sum and the
+ * output are held in 32 bits.  A weight times its value's scale enters the product
+ * with the elements to 2^-11 of itself, or to 2^-27 of the largest such among the
+ * 128 slots around it, however far below the row's largest those are (not under
+ * 2^-50 of the row's sum).  A slot that is seen and holds a NaN makes the row NaN.
+ */
+typedef struct {
+    ple_tree_attention_args base;
+    ple_cache_scales scales;
+} ple_tree_attention_fp8_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_ELEMENT, PLE_ERR_NULL, PLE_ERR_ALIGN,
+ * PLE_ERR_CUDA.  At most two kernel launches. */
+ple_status ple_tree_attention_fp8(const ple_tree_attention_fp8_args* args, void* stream);
+
+/* Its workspace, as ple_tree_attention_workspace. */
+int64_t ple_tree_attention_fp8_workspace(int64_t num_tokens, int32_t q_heads, int32_t kv_heads,
+                                         int32_t head_dim);
+
+/*
+ * ple_tree_commit_fp8 -- ple_tree_commit in caches in 8 bits.
+ *
+ * Slots, lengths and contexts move as there (base.dtype is not looked at).  The
+ * scale of a block that holds slots below ctx_lens[r] + accepted[r], from the block
+ * of slot ctx_lens[r] on, becomes the largest among the scales under which what these
+ * slots now hold was kept; their elements e become e * (that scale / the new one),
+ * rounded to nearest.  Other slots keep their bytes.
+ */
+typedef struct {
+    ple_tree_commit_args base;
+    ple_cache_scales scales;
+} ple_tree_commit_fp8_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_DTYPE, PLE_ERR_NULL, PLE_ERR_ALIGN, PLE_ERR_CUDA.
+ * One kernel launch. */
+ple_status ple_tree_commit_fp8(const ple_tree_commit_fp8_args* args, void* stream);
+
+/*
+ * ple_plan_pages -- the page tables of the next step: requests that go on, fork, end
+ * or begin, the pages that their new tokens need, and pages packed below a limit.
+ *
+ * Row i of the next batch takes over the request source[i] of the old one
+ * (0 <= source[i] < num_requests) with its ctx_lens cached tokens (clamped to
+ * [0, max_pages * page_size]), or begins empty (any other source); a request that no
+ * row takes over has ended.  With c = next_ctx_lens[i], n = max(want[i], 0):
+ *   row i carries the first ceil(c / page_size) entries of its request; numbers outside
+ *   [0, num_pages) among them become -1;
+ *   if n > 0 and c is no multiple of page_size, the last of these is written: the row
+ *   keeps that page only if no row carries it unwritten and no lower row writes it,
+ *   else it gets a new one and the page is to be copied there (copy on write);
+ *   entries from ceil(c / page_size) up to ceil((c + n) / page_size), at most
+ *   max_pages, get new pages; all others are -1.
+ * A page is in use when a row keeps it.  Pages in use numbered page_limit or more move
+ * below it, and new pages lie below it: the free pages there, in ascending order, go
+ * first to the pages that move, in ascending order, then to the rows' new entries, in
+ * row order.  Where they run out, pages stay where they are and entries become -1; the
+ * plan's counts say so, and the old tables are still there to plan anew from.
+ *
+ *   copies   [num_rows + num_pages - page_limit, 2] int32: (from, to) of the pages
+ *            to copy, those that move first, then the doubled ones in row order; the
+ *            rest (-1, -1).  No page is in it both as source and as destination.
+ *   counts   [3] int32: copies; pages in use; pages that were missing.
+ */
+typedef struct {
+    const int32_t* page_table;      /* [B, max_pages] */
+    const int32_t* ctx_lens;        /* [B] */
+    const int32_t* source;          /* [N] */
+    const int32_t* want;            /* [N] */
+    int32_t* next_table;            /* [N, max_pages]; none of the outputs overlaps an input */
+    int32_t* next_ctx_lens;         /* [N] */
+    int32_t* copies;
+    int32_t* counts;
+    void* workspace;                /* 16-byte aligned; need not be cleared */
+    int64_t workspace_bytes;        /* >= ple_plan_pages_workspace's */
+    int32_t num_requests;           /* B >= 0 */
+    int32_t num_rows;               /* N >= 1 */
+    int32_t max_pages, page_size;   /* >= 1; max_pages * page_size <= INT32_MAX */
+    int32_t num_pages;              /* >= 1 */
+    int32_t page_limit;             /* 0 <= page_limit <= num_pages */
+} ple_plan_pages_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_NULL, PLE_ERR_ALIGN, PLE_ERR_CUDA.  One kernel
+ * launch. */
+ple_status ple_plan_pages(const ple_plan_pages_args* args, void* stream);
+
+/* The workspace of such a call in bytes, or -1; not for calls that can run at the
+ * same time. */
+int64_t ple_plan_pages_workspace(int32_t num_rows, int32_t num_pages);
+
+/*
+ * ple_copy_pages -- whole pages copied in the caches of all layers.
+ *
+ * copies [num_copies, 2]: page copies[i][0] of every layer's keys and values (all
+ * heads, slots and elements; with scales.k, their scales too) goes to page
+ * copies[i][1].  Entries with a number outside [0, num_pages) are passed over.  No
+ * page may be both a source and a destination of one call, or twice a destination.
+ */
+typedef struct {
+    const int32_t* copies;
+    void *k_cache, *v_cache;        /* 16-byte aligned */
+    int64_t layer_stride, page_stride, head_stride, slot_stride;  /* in elements */
+    ple_cache_scales scales;        /* of caches in 8 bits; k and v NULL: none */
+    int64_t num_pages;
+    int32_t num_copies;             /* >= 0 */
+    int32_t num_layers;             /* 1 .. 65535 */
+    int32_t kv_heads;               /* 1 .. 65535 */
+    int32_t page_size;              /* >= 1 */
+    int32_t head_dim;               /* 1 .. PLE_MAX_HEAD_DIM; rows of a multiple of 16 bytes */
+    int32_t element_bytes;          /* 1 or 2; rows and strides are multiples of 16 bytes */
+} ple_copy_pages_args;
+
+/* Errors: PLE_ERR_SIZE, PLE_ERR_NULL, PLE_ERR_ALIGN, PLE_ERR_CUDA.  One kernel
+ * launch. */
+ple_status ple_copy_pages(const ple_copy_pages_args* args, void* stream);
+
+/*
  * ple_set_programmatic_launch -- process-wide switch for programmatic
  * dependent launch (on by default); returns the previous setting (1 or 0).
  *

@@ -15,6 +15,8 @@ from .binding import (PLE_BF16, PLE_ERR_ALIGN, PLE_ERR_CUDA, PLE_ERR_DTYPE, PLE_
                       ple_selftest_floor_mod, ple_validate_index, set_programmatic_launch,
                       small_batch_max_rows, status_string)
 
+from .cache import (ple_copy_pages, ple_plan_pages, ple_qk_norm_rope_fp8, ple_tree_attention_fp8,
+                    ple_tree_attention_fp8_workspace, ple_tree_commit_fp8)
 from .index_cache import TokenIndexCache
 from .tree import (ple_build_tree_index, ple_prepare_rope, ple_qk_norm_rope, ple_tree_attention,
                    ple_tree_attention_workspace, ple_tree_commit, ple_tree_row_ids)
@@ -32,4 +34,6 @@ __all__ = [
     "PLE_BF16", "PLE_F16", "PLE_ERR_ELEMENT", "PLE_MAX_TREE_WORDS", "PLE_MAX_HEAD_DIM",
     "ple_build_tree_index", "ple_tree_row_ids", "ple_prepare_rope", "ple_qk_norm_rope",
     "ple_tree_attention", "ple_tree_attention_workspace", "ple_tree_commit",
+    "ple_qk_norm_rope_fp8", "ple_tree_attention_fp8", "ple_tree_attention_fp8_workspace",
+    "ple_tree_commit_fp8", "ple_plan_pages", "ple_copy_pages",
 ]

@@ -77,6 +77,13 @@ SIGNATURES = {
     "ple_tree_attention": (_I32, [_ARGS, _P]),
     "ple_tree_attention_workspace": (_I64, [_I64, _I32, _I32, _I32]),
     "ple_tree_commit": (_I32, [_ARGS, _P]),
+    "ple_qk_norm_rope_fp8": (_I32, [_ARGS, _P]),
+    "ple_tree_attention_fp8": (_I32, [_ARGS, _P]),
+    "ple_tree_attention_fp8_workspace": (_I64, [_I64, _I32, _I32, _I32]),
+    "ple_tree_commit_fp8": (_I32, [_ARGS, _P]),
+    "ple_plan_pages": (_I32, [_ARGS, _P]),
+    "ple_plan_pages_workspace": (_I64, [_I32, _I32]),
+    "ple_copy_pages": (_I32, [_ARGS, _P]),
 }
 
 _lock = threading.Lock()

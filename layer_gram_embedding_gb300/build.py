@@ -26,7 +26,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 SOURCES = ["ple_api.cu", "ple_rowids_fixed.cu", "ple_rowids_headlane.cu", "ple_rowids_runtime.cu",
            "ple_rowids_small.cu", "ple_embed.cu", "ple_index.cu", "ple_tree_api.cu",
            "ple_tree_index.cu", "ple_tree_rowids.cu", "ple_norm_rope.cu",
-           "ple_tree_attention.cu", "ple_tree_attention_tc.cu"]
+           "ple_tree_attention.cu", "ple_tree_attention_tc.cu", "ple_cache_api.cu",
+           "ple_norm_rope_fp8.cu", "ple_tree_attention_fp8.cu", "ple_pages.cu"]
 
 
 def nvcc() -> str:

@@ -1,0 +1,305 @@
+// Norms of queries and keys, their rotation, and the append of keys and values in 8
+// bits to the paged cache, in one pass, on sm_103a.
+//
+// Query rows are those of ple_norm_rope.cuh.  Keys (after norm and rotation, in 32
+// bits) and values become elements of e4m3 under one scale for each block of slots and
+// head: the least power of two that takes the block's largest finite amount to at most
+// 448.  Where a block held tokens before, its scale never falls, and where it grows
+// their elements are rounded anew: a power of two only moves their exponents, so all
+// but those near the elements' least keep their values.
+//
+// Layout.  A block of threads takes the cache's blocks that begin among its tokens (or
+// go on with a request's first one): their tokens' sines and cosines are computed once,
+// and a warp takes one head's keys or values of a cache block, rows as in
+// ple_norm_rope.cuh, twice: once for the largest amount and, with the scale known, once
+// for the elements.  The rows stay in registers in between where they are few.  Bound
+// by the rows' bytes.
+#include "ple_fp8.cuh"
+#include "ple_norm_rope.cuh"
+#include "ple_tree_fp8_internal.h"
+
+namespace ple {
+namespace {
+
+constexpr int kAppendBlocks = 4;    // resident blocks an SM
+constexpr int kHeldRows = 4;        // of a lane, in registers
+constexpr int kAppendTokens = 16;   // most tokens a block of threads looks for blocks among
+
+struct AppendPlan {
+    RowPlan rows;          // the queries'
+    int32_t kv_blocks;     // blocks of threads that append; behind them those of queries
+    int32_t kv_tokens;     // each one's tokens
+    int32_t shift;         // log2 of a cache block's tokens
+};
+
+// A lane's eight values as elements, four and four.
+__device__ __forceinline__ uint2 row_elements(const Pair (&x)[4], float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        split(x[i], lo, hi);
+        // what is not finite is NaN, not the largest element
+        lo = fabsf(lo) < INFINITY ? lo * inv : __int_as_float(0x7FC00000);
+        hi = fabsf(hi) < INFINITY ? hi * inv : __int_as_float(0x7FC00000);
+        w[i] = elements_of(lo, hi);
+    }
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+__device__ __forceinline__ float finite_amount(const Pair (&x)[4]) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        split(x[i], lo, hi);
+        lo = fabsf(lo);
+        hi = fabsf(hi);
+        most = fmaxf(most, fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f));
+    }
+    return most;
+}
+
+template <typename E, int LPR, int kLayout>
+__device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f,
+                                              const AppendPlan& plan, int block_x, int block_y,
+                                              int grid_y) {
+    constexpr int RPW = 32 / LPR;
+    constexpr int kWarps = kNormThreads / 32;
+    constexpr int kPitch = 2 * LPR;   // a token's angles, 16-byte words
+    extern __shared__ __align__(16) float4 angles[];
+    __shared__ float row_s[kLayout == kPairsAnyHalves ? kNormThreads * 8 : 1];
+    const ple_qk_norm_rope_args& a = f.base;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = lane % LPR, in_group = lane / LPR;
+    const bool live = sub * 8 < a.head_dim;
+    const int pairs = a.rotary_dim >> 1;
+    const bool turns = kLayout == kPairsHalves ? sub * 8 < a.rotary_dim : true;
+    const int first = kLayout == kPairsHalves && turns ? sub * 4 : sub * 8;
+    const int second = kLayout == kPairsHalves && turns ? pairs : 4;
+    const float inv_d = 1.0f / (float)a.head_dim;
+    const int size = 1 << plan.shift;
+
+    wait_grid_before();
+    int64_t t = (int64_t)block_x * plan.kv_tokens;
+    const int64_t t_end = min(t + plan.kv_tokens, a.num_tokens);
+    int r = warp_request(a.cu_seqlens, a.num_requests, t, lane);
+    int32_t begin, end;
+    request_nodes(a.cu_seqlens, r, a.num_tokens, begin, end);
+    while (t < t_end) {
+        while (t >= end && r + 1 < a.num_requests)
+            request_nodes(a.cu_seqlens, ++r, a.num_tokens, begin, end);
+        if (t >= end) break;                      // padding
+        if (t < begin) {
+            t = begin;
+            continue;
+        }
+        const int64_t ctx = max(__ldg(a.ctx_lens + r), 0);
+        const int64_t slot = ctx + (t - begin);
+        const int into = (int)(slot & (size - 1));
+        if (t > begin && into != 0) {             // another block of threads has it
+            t = min(t + (size - into), (int64_t)end);
+            continue;
+        }
+        const int count = (int)min((int64_t)(size - into), end - t);
+        const int64_t page_at = slot / a.page_size;
+        int32_t page = -1;
+        if (page_at < a.max_pages) page = __ldg(a.page_table + (int64_t)r * a.max_pages + page_at);
+        if (page < 0 || page >= a.num_pages) {    // dropped
+            t += count;
+            continue;
+        }
+        const int in_page = (int)(slot - page_at * a.page_size);
+        __syncthreads();
+        for (int i = threadIdx.x; i < count * pairs; i += kNormThreads) {
+            const int k = i / pairs, p = i - k * pairs;
+            const uint64_t phase = (uint64_t)(int64_t)__ldg(a.positions + t + k) *
+                                   (uint64_t)__ldg(reinterpret_cast<const long long*>(a.rope) + p);
+            // 2^-32 turns, signed; sincospif takes half turns, and what the float of them
+            // lacks comes in by the first order: keys near the border between two
+            // elements stay on their side
+            const int32_t turns32 = (int32_t)(uint32_t)(phase >> 32);
+            const float near = (float)turns32;
+            const float rest = (float)((int64_t)turns32 - (int64_t)near) +
+                               (float)(uint32_t)phase * 0x1p-32f;
+            float sn, cs;
+            sincospif(near * 0x1p-31f, &sn, &cs);
+            const float off = rest * (0x1p-31f * 3.14159265358979f);
+            const float sn0 = sn;
+            sn = fmaf(cs, off, sn);
+            cs = fmaf(-sn0, off, cs);
+            float* word = reinterpret_cast<float*>(&angles[k * kPitch + (p >> 1)]);
+            word[p & 1] = cs * a.rope_scale;
+            word[2 + (p & 1)] = sn * a.rope_scale;
+        }
+        __syncthreads();
+        for (int task = block_y * kWarps + warp; task < 2 * a.kv_heads; task += kWarps * grid_y) {
+            const bool is_k = task < a.kv_heads;
+            const int head = is_k ? task : task - a.kv_heads;
+            const int64_t step = is_k ? a.k_token : a.v_token;
+            const unsigned short* src =
+                static_cast<const unsigned short*>(is_k ? a.k : a.v) +
+                (t + in_group) * step + head * (is_k ? a.k_head : a.v_head) + first;
+            uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) +
+                           page * a.page_stride + head * a.head_stride +
+                           (in_page + in_group) * a.slot_stride + first;
+            unsigned short* scale_at =
+                static_cast<unsigned short*>(is_k ? f.scales.k : f.scales.v) +
+                page * f.scales.page_stride + head * f.scales.head_stride +
+                (in_page >> plan.shift);
+            const bool normed = is_k && a.k_weight != nullptr;
+            Pair w[4];
+            {
+                Row row = {};
+                if (normed && live) {
+                    const unsigned short* from =
+                        static_cast<const unsigned short*>(a.k_weight) + first;
+                    row.a = __ldg(reinterpret_cast<const uint2*>(from));
+                    row.b = __ldg(reinterpret_cast<const uint2*>(from + second));
+                }
+                unpack_row<E>(row, w);
+            }
+            unsigned short before = 0;
+            if (into != 0) before = *scale_at;
+            Row held[kHeldRows];
+            auto load = [&](int i0) {
+#pragma unroll
+                for (int i = 0; i < kHeldRows; ++i) {
+                    held[i] = Row{};
+                    const int k = i0 + i * RPW;
+                    if (live && k + in_group < count) held[i] = load_row(src + k * step, second);
+                }
+            };
+            auto turned = [&](int i0, int i, Pair (&x)[4]) {
+                unpack_row<E>(held[i], x);
+                if (is_k)
+                    turn_row<LPR, kLayout>(
+                        x, w, normed, inv_d, a.eps,
+                        angles + min(i0 + i * RPW + in_group, count - 1) * kPitch, sub, pairs,
+                        turns, row_s);
+            };
+            float most = 0.f;
+            for (int i0 = 0; i0 < count; i0 += kHeldRows * RPW) {
+                load(i0);
+#pragma unroll
+                for (int i = 0; i < kHeldRows; ++i) {
+                    if (i0 + i * RPW >= count) break;
+                    Pair x[4];
+                    turned(i0, i, x);
+                    most = fmaxf(most, finite_amount(x));
+                }
+            }
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1)
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+            float scale = __uint_as_float((uint32_t)(127 + exponent_for(most)) << 23);
+            if (into != 0) {
+                const float old = scale_value(before);
+                if (scale > old) {
+                    // the tokens that the block holds, under the new scale
+                    const float shrink = old / scale;
+                    uint8_t* row = dst - (int64_t)into * a.slot_stride - first + sub * 8;
+                    for (int k = 0; k + in_group < into; k += RPW) {
+                        if (!live) break;
+                        uint2* at = reinterpret_cast<uint2*>(row + k * a.slot_stride);
+                        const uint2 v = *at;
+                        *at = make_uint2(scaled_elements(v.x, shrink), scaled_elements(v.y, shrink));
+                    }
+                } else {
+                    scale = old;
+                }
+            }
+            const float inv = 1.0f / scale;
+            for (int i0 = 0; i0 < count; i0 += kHeldRows * RPW) {
+                if (count > kHeldRows * RPW) load(i0);
+#pragma unroll
+                for (int i = 0; i < kHeldRows; ++i) {
+                    if (i0 + i * RPW >= count) break;
+                    Pair x[4];
+                    turned(i0, i, x);
+                    const uint2 e = row_elements(x, inv);
+                    const int k = i0 + i * RPW;
+                    if (live && k + in_group < count) {
+                        *reinterpret_cast<uint32_t*>(dst + k * a.slot_stride) = e.x;
+                        *reinterpret_cast<uint32_t*>(dst + k * a.slot_stride + second) = e.y;
+                    }
+                }
+            }
+            if (lane == 0) *scale_at = (unsigned short)(__float_as_uint(scale) >> 16);
+        }
+        t += count;
+    }
+}
+
+template <typename E, int LPR, int kLayout>
+__global__ void __launch_bounds__(kNormThreads, kAppendBlocks)
+qk_norm_rope_fp8_kernel(const __grid_constant__ ple_qk_norm_rope_fp8_args f,
+                        const __grid_constant__ ple_qk_norm_rope_args queries,
+                        const __grid_constant__ AppendPlan plan) {
+    if ((int)blockIdx.x < plan.kv_blocks)
+        append_blocks<E, LPR, kLayout>(f, plan, blockIdx.x, blockIdx.y, gridDim.y);
+    else
+        norm_rope_rows<E, LPR, kLayout>(queries, plan.rows, blockIdx.x - plan.kv_blocks,
+                                        blockIdx.y, gridDim.y);
+}
+
+template <typename E, int LPR>
+cudaError_t launch_rows(const ple_qk_norm_rope_fp8_args& f, const DeviceFacts& dev,
+                        cudaStream_t stream) {
+    constexpr int RPW = 32 / LPR;
+    constexpr int kWarps = kNormThreads / 32;
+    const ple_qk_norm_rope_args& a = f.base;
+    AppendPlan plan;
+    plan.shift = f.scales.block == 16 ? 4 : f.scales.block == 32 ? 5 : f.scales.block == 64 ? 6 : 7;
+    plan.rows.q_groups = (a.q_heads + RPW - 1) / RPW;
+    plan.rows.kv_groups = 0;
+    const int64_t resident = kAppendBlocks * (int64_t)dev.sm_count;
+    auto tokens = [&](int64_t most) {
+        const int64_t n = a.num_tokens / resident;
+        return n < 1 ? 1 : n > most ? most : n;
+    };
+    plan.rows.tokens = (int)tokens(kNormTokens);
+    plan.kv_tokens = (int)tokens(kAppendTokens);
+    const int64_t q_blocks =
+        a.q_heads ? (a.num_tokens + plan.rows.tokens - 1) / plan.rows.tokens : 0;
+    plan.kv_blocks = (int)((a.num_tokens + plan.kv_tokens - 1) / plan.kv_tokens);
+    const int64_t blocks = q_blocks + plan.kv_blocks;
+    // few tokens: a token's heads spread over several blocks too
+    int64_t split = resident / blocks;
+    const int groups = plan.rows.q_groups > 2 * a.kv_heads ? plan.rows.q_groups : 2 * a.kv_heads;
+    const int64_t most = (groups + kWarps - 1) / kWarps;
+    split = split < 1 ? 1 : split > most ? most : split;
+    auto* fn = a.rotary_dim && a.interleaved
+                   ? qk_norm_rope_fp8_kernel<E, LPR, kPairsInterleaved>
+               : a.rotary_dim % 8 == 0 ? qk_norm_rope_fp8_kernel<E, LPR, kPairsHalves>
+                                       : qk_norm_rope_fp8_kernel<E, LPR, kPairsAnyHalves>;
+    const int smem = a.rotary_dim ? f.scales.block * 2 * LPR * 16 : 0;
+    if (smem > 16384) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    ple_qk_norm_rope_args queries = a;
+    queries.kv_heads = 0;
+    queries.k_cache = queries.v_cache = nullptr;
+    return launch_kernel(fn, dim3((unsigned)blocks, (unsigned)split), dim3(kNormThreads), smem,
+                         stream, programmatic_launch(), f, queries, plan);
+}
+
+template <typename E>
+cudaError_t launch_element(const ple_qk_norm_rope_fp8_args& f, const DeviceFacts& dev,
+                           cudaStream_t stream) {
+    if (f.base.head_dim <= 64) return launch_rows<E, 8>(f, dev, stream);
+    if (f.base.head_dim <= 128) return launch_rows<E, 16>(f, dev, stream);
+    return launch_rows<E, 32>(f, dev, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope_fp8(const ple_qk_norm_rope_fp8_args& f, const DeviceFacts& dev,
+                                    cudaStream_t stream) {
+    return f.base.dtype == PLE_BF16 ? launch_element<__nv_bfloat16>(f, dev, stream)
+                                    : launch_element<__half>(f, dev, stream);
+}
+
+}  // namespace ple

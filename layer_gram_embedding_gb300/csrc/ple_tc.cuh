@@ -89,6 +89,17 @@ __device__ __forceinline__ bool elect_lane() {
     return chosen != 0;
 }
 
+// A warpgroup's registers a thread, fewer or more than at launch: the sum over the
+// block's warpgroups may not pass what it was launched with.
+template <int kCount>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+template <int kCount>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+
 template <int kThreads>
 __device__ __forceinline__ void named_barrier(int id) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
