@@ -27,7 +27,8 @@ SOURCES = ["ple_api.cu", "ple_rowids_fixed.cu", "ple_rowids_headlane.cu", "ple_r
            "ple_rowids_small.cu", "ple_embed.cu", "ple_index.cu", "ple_tree_api.cu",
            "ple_tree_index.cu", "ple_tree_rowids.cu", "ple_norm_rope.cu",
            "ple_tree_attention.cu", "ple_tree_attention_tc.cu", "ple_cache_api.cu",
-           "ple_norm_rope_fp8.cu", "ple_tree_attention_fp8.cu", "ple_pages.cu"]
+           "ple_norm_rope_fp8.cu", "ple_tree_attention_fp8.cu",
+           "ple_tree_attention_fp8_tc.cu", "ple_pages.cu"]
 
 
 def nvcc() -> str:

@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "ple.h"
+
 namespace ple {
 namespace {
 
@@ -41,6 +43,13 @@ __device__ __forceinline__ uint32_t scaled_elements(uint32_t w, float f) {
     return elements_of(a.x * f, a.y * f) | elements_of(b.x * f, b.y * f) << 16;
 }
 
+// The same where infinities are NaN too.
+__device__ __forceinline__ uint32_t nearest_elements(float lo, float hi) {
+    lo = fabsf(lo) < INFINITY ? lo : __int_as_float(0x7FC00000);
+    hi = fabsf(hi) < INFINITY ? hi : __int_as_float(0x7FC00000);
+    return elements_of(lo, hi);
+}
+
 // Which of a word's four elements are NaN: their top bits.
 __device__ __forceinline__ uint32_t nan_flags(uint32_t w) {
     return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
@@ -51,12 +60,91 @@ __device__ __forceinline__ float scale_value(unsigned short bits) {
     return __uint_as_float((uint32_t)bits << 16);
 }
 
+// log2 of a scale (the bits of a bfloat16), exact for a power of two; of 0 a finite
+// number, less than that of any other.
+__device__ __forceinline__ float scale_log(uint32_t bits) {
+    const float scale = scale_value((unsigned short)bits);
+    if ((bits & 0x7F) == 0 && bits - 0x80 < 0x7F00) return (float)((int)(bits >> 7) - 127);
+    float l;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(l) : "f"(scale));
+    return scale == 0.f ? -1000.f : l;
+}
+
+// Where the attention kernels find scales.
+struct Scales {
+    const unsigned short *k, *v;
+    int64_t page, head;       // strides
+    int32_t shift;            // log2 of a block's tokens
+    // x / page_size below 2^31 as (x + high word of x * page_magic) >> page_shift: division
+    // by a constant (Granlund and Montgomery 1994)
+    uint32_t page_magic;
+    int32_t page_shift;
+
+    __device__ __forceinline__ uint32_t page_of(uint32_t slot) const {
+        return (__umulhi(slot, page_magic) + slot) >> page_shift;
+    }
+    // The scales of a slot's keys (low half) and values, its page being `number`.
+    __device__ __forceinline__ uint32_t both(int number, int of_head, uint32_t slot,
+                                             int page_size) const {
+        const int64_t at = number * page + of_head * head +
+                           ((slot - page_of(slot) * page_size) >> shift);
+        return __ldg(k + at) | (uint32_t)__ldg(v + at) << 16;
+    }
+};
+
+inline int block_shift(int block) {
+    return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+}
+
+inline Scales scales_of(const ple_tree_attention_fp8_args& f) {
+    Scales s;
+    s.k = static_cast<const unsigned short*>(f.scales.k);
+    s.v = static_cast<const unsigned short*>(f.scales.v);
+    s.page = f.scales.page_stride;
+    s.head = f.scales.head_stride;
+    s.shift = block_shift(f.scales.block);
+    // with l bits of the divisor d: floor(2^32 (2^l - d) / d) + 1
+    const uint64_t d = f.base.page_size;
+    int l = 0;
+    while ((uint64_t)1 << l < d) ++l;
+    s.page_shift = l;
+    s.page_magic = (uint32_t)(((uint64_t)1 << 32) * (((uint64_t)1 << l) - d) / d + 1);
+    return s;
+}
+
 // The exponent of the least power of two, at least 2^kLeastExponent, that takes a
 // finite amount up to 448 of it: 448 is 1.75 * 2^8.
 __device__ __forceinline__ int exponent_for(float most) {
     const uint32_t b = __float_as_uint(most);
     const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return max(e, kLeastExponent);
+}
+
+// A row's queries as sums of elements: times 2^-shift, so that the largest is in
+// [128, 256).
+__device__ __forceinline__ int term_shift(float most) {
+    const int e = (int)(__float_as_uint(most) >> 23) - 127;
+    return e > 127 ? 0 : max(e - 7, -100);
+}
+
+// Two 16-bit values of a word.
+template <bool kBf16>
+__device__ __forceinline__ void widen_pair(uint32_t v, float& lo, float& hi) {
+    if constexpr (kBf16) {
+        lo = __uint_as_float(v << 16);
+        hi = __uint_as_float(v & 0xFFFF0000u);
+    } else {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        lo = x.x;
+        hi = x.y;
+    }
+}
+
+// A row's queries as halves: those of float16 as they are, those of bfloat16 times
+// 2^-shift so that the largest is near 2^15: the rest lose what lies below 2^-40 of it.
+__device__ __forceinline__ int query_shift(uint32_t most) {
+    const int e = (int)(most >> 23) - 127;
+    return e > 127 ? 0 : max(e - 14, -100);
 }
 
 }  // namespace

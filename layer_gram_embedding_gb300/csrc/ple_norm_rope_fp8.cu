@@ -250,7 +250,7 @@ cudaError_t launch_rows(const ple_qk_norm_rope_fp8_args& f, const DeviceFacts& d
     constexpr int kWarps = kNormThreads / 32;
     const ple_qk_norm_rope_args& a = f.base;
     AppendPlan plan;
-    plan.shift = f.scales.block == 16 ? 4 : f.scales.block == 32 ? 5 : f.scales.block == 64 ? 6 : 7;
+    plan.shift = block_shift(f.scales.block);
     plan.rows.q_groups = (a.q_heads + RPW - 1) / RPW;
     plan.rows.kv_groups = 0;
     const int64_t resident = kAppendBlocks * (int64_t)dev.sm_count;

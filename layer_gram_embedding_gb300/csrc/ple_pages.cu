@@ -462,11 +462,10 @@ int64_t page_parts(const ple_copy_pages_args& a) {
 }  // namespace
 
 cudaError_t launch_tree_commit_fp8(const ple_tree_commit_fp8_args& f, cudaStream_t stream) {
-    const int block = f.scales.block;
     return launch_kernel(tree_commit_fp8_kernel,
                          dim3((unsigned)f.base.num_requests, (unsigned)f.base.num_layers, 2),
                          dim3(kCommitThreads), 0, stream, programmatic_launch(), f,
-                         block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7);
+                         block_shift(f.scales.block));
 }
 
 int64_t plan_pages_workspace(int32_t num_rows, int32_t num_pages) {

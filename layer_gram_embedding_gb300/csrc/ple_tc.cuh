@@ -191,6 +191,20 @@ __device__ __forceinline__ void tmem_load_max(uint32_t at, uint32_t (&v)[32], fl
                  : "r"(at));
 }
 
+// Sixteen columns with their largest, into v[at..at + 15].
+__device__ __forceinline__ void tmem_load_max16(uint32_t from, uint32_t (&v)[32], const int at,
+                                                float& most) {
+    asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15}, %16, [%17];"
+                 : "=r"(v[at]), "=r"(v[at + 1]), "=r"(v[at + 2]), "=r"(v[at + 3]),
+                   "=r"(v[at + 4]), "=r"(v[at + 5]), "=r"(v[at + 6]), "=r"(v[at + 7]),
+                   "=r"(v[at + 8]), "=r"(v[at + 9]), "=r"(v[at + 10]), "=r"(v[at + 11]),
+                   "=r"(v[at + 12]), "=r"(v[at + 13]), "=r"(v[at + 14]), "=r"(v[at + 15]),
+                   "=f"(most)
+                 : "r"(from));
+}
+
 // What was loaded before a tmem_wait_load of something later.
 __device__ __forceinline__ void tmem_settle(uint32_t (&v)[32], float& most) {
     asm volatile(""
@@ -250,6 +264,15 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t at, uint32_t lead) {
            (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// The same for a tile of 8-bit elements whose rows are the swizzle's span: atoms of 8
+// rows, kAtom bytes (1024 with the 128-byte swizzle, 512 with that of 64).
+template <uint32_t kAtom>
+__device__ __forceinline__ uint64_t element_desc(uint32_t at) {
+    static_assert(kAtom == 1024 || kAtom == 512, "");
+    return (uint64_t)((at >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(kAtom >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)(kAtom == 1024 ? 2 : 4) << 61;
+}
+
 // The instruction word of kind::f16: 32-bit accumulator, both operands f16 or
 // both bf16, A with the reduction along its rows; kAcross: B's rows are the
 // reduction.
@@ -267,7 +290,17 @@ __device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// The same with A in tensor memory, two elements to a column.
+// The same of 8-bit elements (kind::f8f6f4; both e4m3 with the word of f16), 32 a step.
+__device__ __forceinline__ void mma_elements(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+                                             bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// The same as mma_smem with A in tensor memory, two elements to a column.
 __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t word,
                                          bool accumulate) {
     asm volatile(

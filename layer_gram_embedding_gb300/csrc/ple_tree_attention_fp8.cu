@@ -44,14 +44,6 @@ constexpr float kRise = 5.0f, kFall = 7.0f, kBias = 9.0f;
 // A reference falls only while the row's weights sum up to less than this.
 constexpr float kMostSum = 0x1p60f;
 
-struct Scales {
-    const unsigned short *k, *v;
-    int64_t page, head;       // strides
-    int32_t shift;            // log2 of a block's tokens
-    uint32_t page_magic;      // x / page_size = (x + high word of x * page_magic) >> page_shift
-    int32_t page_shift;
-};
-
 // W: a head's width in shared memory (64, 128 or 256); NT: tiles of eight rows; Teams: of
 // eight warps, which take the tiles in turn.
 template <int W, int NT, int Teams>
@@ -115,13 +107,6 @@ __device__ __forceinline__ uint32_t query_at(int row, int piece) {
 template <int W>
 __device__ __forceinline__ int meet_at(int row, int f) {
     return W == 64 ? f ^ (row >> 1 & 1) ^ (row & 4) : f ^ (row >> 1 & 3);
-}
-
-// A row's queries as halves: those of float16 as they are, those of bfloat16 times
-// 2^-shift so that the largest is near 2^15: the rest lose what lies below 2^-40 of it.
-__device__ __forceinline__ int query_shift(uint32_t most) {
-    const int e = (int)(most >> 23) - 127;
-    return e > 127 ? 0 : max(e - 14, -100);
 }
 
 template <int W, int NT, int Teams, bool kBf16>
@@ -263,16 +248,11 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
         // the slice's scales, asked for a tile ahead, its page two
         auto page_at = [&](int k) -> int {
             const uint32_t slot = k * kTile + slice * kSlice;
-            const uint32_t at = (__umulhi(slot, sc.page_magic) + slot) >> sc.page_shift;
-            return k < k1 && (int)slot < length ? __ldg(table + at) : -1;
+            return k < k1 && (int)slot < length ? __ldg(table + sc.page_of(slot)) : -1;
         };
         auto scales_at = [&](int k, int page) -> uint32_t {
             if (page < 0 || page >= a.num_pages) return 0x3F803F80u;  // 1 and 1
-            const uint32_t slot = k * kTile + slice * kSlice;
-            const uint32_t at = (__umulhi(slot, sc.page_magic) + slot) >> sc.page_shift;
-            const int64_t where = page * sc.page + head * sc.head +
-                                  ((slot - at * a.page_size) >> sc.shift);
-            return __ldg(sc.k + where) | (uint32_t)__ldg(sc.v + where) << 16;
+            return sc.both(page, head, k * kTile + slice * kSlice, a.page_size);
         };
         // this team's first tile
         int mine = Teams == 1 || (stage & 1) == team ? k0 : k0 + 1;
@@ -786,11 +766,17 @@ cudaError_t launch_dtype(const TcArgs& args, const Scales& sc, const CUtensorMap
     }
 }
 
+// Whether a call's key heads have so many rows that the tensor cores' kernel takes it.
+bool many_rows(const ple_tree_attention_args& a) {
+    return a.num_tokens * (a.q_heads / a.kv_heads) > 16 * (int64_t)a.num_requests;
+}
+
 }  // namespace
 
 int64_t tree_attention_fp8_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D,
                                      const DeviceFacts& dev) {
-    return 4 * state_at(tc_blocks(dev), 0, fp8_rows_cap(T, q_heads, kv_heads, D), padded_width(D));
+    // the other kernel's states are of more rows
+    return tree_attention_fp8_tc_workspace(T, q_heads, kv_heads, D, dev);
 }
 
 cudaError_t launch_tree_attention_fp8(const ple_tree_attention_fp8_args& f,
@@ -799,6 +785,7 @@ cudaError_t launch_tree_attention_fp8(const ple_tree_attention_fp8_args& f,
     CUtensorMap k, v;
     if (!encode_cache(&k, a, a.k_cache) || !encode_cache(&v, a, a.v_cache))
         return cudaErrorInvalidValue;
+    if (many_rows(a)) return launch_tree_attention_fp8_tc(f, k, v, dev, stream);
     TcArgs args;
     args.a = a;
     args.blocks = tc_blocks(dev);
@@ -812,19 +799,7 @@ cudaError_t launch_tree_attention_fp8(const ple_tree_attention_fp8_args& f,
     // a scale of 0 as the least normal number, so that exponents stay numbers
     args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     args.flip = a.scale < 0 ? 0x80008000u : 0u;
-    Scales sc;
-    sc.k = static_cast<const unsigned short*>(f.scales.k);
-    sc.v = static_cast<const unsigned short*>(f.scales.v);
-    sc.page = f.scales.page_stride;
-    sc.head = f.scales.head_stride;
-    sc.shift = f.scales.block == 16 ? 4 : f.scales.block == 32 ? 5 : f.scales.block == 64 ? 6 : 7;
-    // division by a constant below 2^31 (Granlund and Montgomery 1994): with l bits of
-    // the divisor d, floor(2^32 (2^l - d) / d) + 1
-    int bits = 0;
-    while ((int64_t)1 << bits < a.page_size) ++bits;
-    sc.page_shift = bits;
-    sc.page_magic =
-        (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << bits) - a.page_size)) / a.page_size + 1);
+    const Scales sc = scales_of(f);
     return a.dtype == PLE_BF16 ? launch_dtype<true>(args, sc, k, v, stream)
                                : launch_dtype<false>(args, sc, k, v, stream);
 }

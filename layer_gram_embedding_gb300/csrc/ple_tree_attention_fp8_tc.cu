@@ -1,0 +1,963 @@
+// Attention of drafted nodes over a paged cache in 8 bits, on the tensor cores of
+// sm_103a: the kernel for many rows a key head.
+//
+// The mathematics, scales and references are those of ple_tree_attention_fp8.cu, the
+// rows, tiles, segments and the two softmax groups those of ple_tree_attention_tc.cu:
+//   S = Q E^T           (in products of elements, accumulated in tensor memory)
+//   x = c a S           (a the key scale of a column's block, 16 columns or more)
+//   w = b exp2(x - top) * 2^(top - ref)   (b the value scale; as halves over S)
+//   O = O + w F         (value elements F as halves)
+// with the row's sum of exp2(x - top) in registers.
+//
+// Queries.  Keys enter their product as they are kept.  A row of queries, times a power
+// of two that takes its largest element to [128, 256), is written as a sum of elements:
+// the nearest one, the nearest to the rest, and for float16 the nearest to what is left
+// then.  Two hold the eight significant bits of bfloat16, three the eleven of float16, but
+// for what lies below 2^-10, 2^-17 of the row's largest.  The parts follow each other in
+// the reduction; elements multiply at twice the rate of halves, so two cost what halves
+// would, and keys need no other form.
+//
+// Blocks.  One block an SM, four warpgroups: two of softmax, a row a thread; one that
+// turns values into halves, from one ring of shared memory into another (a conversion of
+// two is one instruction, and every element is a half exactly); and a warp each to copy
+// tiles of keys, of values (tiled bulk copies, page by page), to issue the matrix
+// instructions and to walk the segments ahead.  Registers are dealt out anew among them.
+//
+// What is not seen: as in ple_tree_attention_tc.cu.  Values past the request's tokens and
+// elements of drafted nodes that are NaN are cleared as they are converted; rows that
+// see the latter become NaN at the end.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ple_fp8.cuh"
+#include "ple_tc.cuh"
+#include "ple_tree_fp8_internal.h"
+#include "ple_tree_split.cuh"
+
+namespace ple {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kKeyWarp = 8, kIssueWarp = 9, kValueWarp = 10, kWalkWarp = 11;
+constexpr int kTurnWarp = 12;                                  // the first of four
+// 512 threads are launched with 128 registers each
+constexpr int kSoftmaxRegisters = 176, kOneTaskRegisters = 64, kTurnRegisters = 96;
+static_assert(2 * kSoftmaxRegisters + kOneTaskRegisters + kTurnRegisters == 4 * 128, "");
+
+// As in ple_tree_attention_fp8.cu.
+constexpr float kRise = 5.0f, kFall = 7.0f, kBias = 9.0f;
+constexpr float kMostSum = 0x1p60f;
+
+template <int D, bool kBf16>
+struct Shape {
+    static constexpr int kParts = D > 128 ? 2 : 1;       // of a head
+    static constexpr int kWidth = D / kParts;            // elements a part
+    static constexpr int kTerms = kBf16 ? 2 : 3;         // of a query
+    static constexpr int kBytes = kTile * kWidth;        // of a part's tile of elements
+    static constexpr int kTileBytes = 2 * kBytes;        // and of halves
+    static constexpr int kHalfBytes = kTile * 128;       // a swizzled block of 64 halves a row
+    // rings: keys and values as they come, 64 KB or more of them, where an SM's share
+    // of the measured bandwidth times a memory latency of 1.2 us is 54; values as
+    // halves, those at work and the next ones
+    static constexpr int kKeys = kWidth == 64 ? 6 : kBf16 ? 3 : 2;
+    static constexpr int kValues = kKeys;
+    static constexpr int kSlots = kWidth == 64 ? 4 : 2;
+    static constexpr int kQueryBytes = 2 * kTerms * kBytes;
+    static constexpr int kSmem =
+        kQueryBytes + (kKeys + kValues) * kBytes + kSlots * kTileBytes + 1024;
+    // half of the 512 columns for each group: S (and the weights over it), O behind it
+    static constexpr uint32_t kGroupColumns = 256;
+    static constexpr uint32_t kOut = 128;
+    // rows of elements span a swizzle of 128 bytes, or of 64
+    static constexpr uint32_t kAtom = 8 * kWidth;
+};
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
+// A 16-byte piece's place in a tile of elements.
+template <int kWidth>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+    return row * kWidth + ((kWidth == 128 ? piece ^ (row & 7) : piece ^ (row >> 1 & 3)) << 4);
+}
+
+// A place in a ring, and how often it was filled before.
+template <int kPlaces>
+struct Turn {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == kPlaces) {
+            at = 0;
+            ++round;
+        }
+    }
+};
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
+                             const __grid_constant__ Scales sc,
+                             const __grid_constant__ CUtensorMap k_map,
+                             const __grid_constant__ CUtensorMap v_map) {
+    using S = Shape<D, kBf16>;
+    const ple_tree_attention_args& a = args.a;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t key_full[S::kKeys], key_empty[S::kKeys];
+    __shared__ __align__(8) uint64_t stage_full[S::kValues], stage_empty[S::kValues];
+    __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_low[2], p_high[2], pv_done[2];
+    __shared__ __align__(8) uint64_t last;
+    __shared__ int64_t scratch[kThreads / 32];
+    __shared__ Share share_s;
+    __shared__ uint32_t tmem_s;
+    __shared__ int failed_s;
+    // whether drafted values of a segment hold NaN, as each converting warp found; that
+    // warpgroup is at most three segments ahead
+    __shared__ int bad_s[4][4];
+    __shared__ float join_s[kTile][2];
+    __shared__ int8_t shift_s[2][kTile];   // of a group's rows
+    __shared__ Segment seg_s[2];
+    __shared__ int more_s[2];
+    __shared__ int64_t end_s[2];      // the place behind the segment
+    volatile int* failed = &failed_s;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023) & ~1023u) - smem_addr(smem_raw));
+    uint8_t* q_tiles = smem;
+    uint8_t* ring = smem + S::kQueryBytes;                    // values as halves
+    uint8_t* key_ring = ring + S::kSlots * S::kTileBytes;
+    uint8_t* stages = key_ring + S::kKeys * S::kBytes;         // values as they come
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kKeys; ++i) {
+            mbar_init(&key_full[i], 1);
+            mbar_init(&key_empty[i], 1);
+        }
+        for (int i = 0; i < S::kValues; ++i) {
+            mbar_init(&stage_full[i], 1);
+            mbar_init(&stage_empty[i], 4);
+        }
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(&full[i], 4);
+            mbar_init(&empty[i], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&q_full[w], 128);
+            mbar_init(&s_full[w], 1);
+            mbar_init(&p_low[w], 4);
+            mbar_init(&p_high[w], 4);
+            mbar_init(&pv_done[w], 1);
+        }
+        mbar_init(&q_empty, 1);
+        mbar_init(&last, 1);
+        failed_s = 0;
+        fence_barrier_init();
+    }
+    if (warp == kIssueWarp) tmem_alloc(&tmem_s, 512);
+    if (warp == kKeyWarp && lane == 0) {
+        prefetch_map(&k_map);
+        prefetch_map(&v_map);
+    }
+    wait_grid_before();
+
+    find_share<kThreads>(args, scratch, &share_s);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_s;
+    const int group = args.group;
+    if (warp >= kTurnWarp) {
+        // ---------------------------------------------------- values to halves
+        fewer_registers<kTurnRegisters>();
+        const int mine = warp - kTurnWarp;
+        Walk<S::kParts> walk;
+        walk.begin(args, share_s);
+        Segment s;
+        Turn<S::kValues> stage;
+        Turn<S::kSlots> slot;
+        uint32_t seg = 0;
+        // a lane's 16 elements of a row: eight lanes, or four, a row
+        constexpr int kAcross = S::kWidth / 16;
+        constexpr int kRows = 32 / kAcross;       // rows at a time
+        const int piece = lane % kAcross, row0 = mine * (kTile / 4) + lane / kAcross;
+        bool ended = false;
+        while (!ended && walk.next(args, s)) {
+            if (lane == 0) bad_s[seg & 3][mine] = 0;
+            __syncwarp();
+            for (int i = 0; i < (s.k1 - s.k0) * S::kParts; ++i) {
+                if (!mbar_wait(&stage_full[stage.at], stage.round & 1, failed) ||
+                    !mbar_wait(&empty[slot.at], (slot.round & 1) ^ 1, failed)) {
+                    ended = true;
+                    break;
+                }
+                const uint8_t* from = stages + stage.at * S::kBytes;
+                uint8_t* to = ring + slot.at * S::kTileBytes + piece / 4 * S::kHalfBytes;
+                const int first = (s.k0 + i / S::kParts) * kTile;
+                const bool look = first + kTile > s.q.ctx;
+                const int seen_to = s.q.length - first, known_to = s.q.ctx - first;
+                if (look) {
+                    // cleared where they lie, in a walk of their own: few tiles have any
+                    bool bad = false;
+#pragma unroll 1
+                    for (int k = 0; k < kTile / 4 / kRows; ++k) {
+                        const int row = row0 + k * kRows;
+                        uint4* at = reinterpret_cast<uint4*>(stages + stage.at * S::kBytes +
+                                                             piece_at<S::kWidth>(row, piece));
+                        if (row >= seen_to) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else if (row >= known_to) {
+                            uint4 v = *at;
+                            const uint32_t n[4] = {nan_flags(v.x), nan_flags(v.y), nan_flags(v.z),
+                                                   nan_flags(v.w)};
+                            if (n[0] | n[1] | n[2] | n[3]) {
+                                bad = true;
+                                *at = make_uint4(v.x & ~((n[0] >> 7) * 0xFFu),
+                                                 v.y & ~((n[1] >> 7) * 0xFFu),
+                                                 v.z & ~((n[2] >> 7) * 0xFFu),
+                                                 v.w & ~((n[3] >> 7) * 0xFFu));
+                            }
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, bad) && lane == 0) bad_s[seg & 3][mine] = 1;
+                    __syncwarp();
+                }
+#pragma unroll 4
+                for (int k = 0; k < kTile / 4 / kRows; ++k) {
+                    const int row = row0 + k * kRows;
+                    const uint4 v = *reinterpret_cast<const uint4*>(
+                        from + piece_at<S::kWidth>(row, piece));
+                    uint4 low, high;
+                    halves_of(v.x, low.x, low.y);
+                    halves_of(v.y, low.z, low.w);
+                    halves_of(v.z, high.x, high.y);
+                    halves_of(v.w, high.z, high.w);
+                    // the lanes of a row's other half store their pieces the other way
+                    // round: eight lanes meet eight banks
+                    uint8_t* at = to + row * 128;
+                    const int p0 = 2 * (piece & 3), turn = piece >> 2;
+                    *reinterpret_cast<uint4*>(at + (((p0 + turn) ^ (row & 7)) << 4)) =
+                        turn ? high : low;
+                    *reinterpret_cast<uint4*>(at + (((p0 + 1 - turn) ^ (row & 7)) << 4)) =
+                        turn ? low : high;
+                }
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&full[slot.at]);
+                    mbar_arrive(&stage_empty[stage.at]);
+                }
+                stage.next();
+                slot.next();
+            }
+            ++seg;
+        }
+    } else if (warp >= 8) {
+        fewer_registers<kOneTaskRegisters>();
+        Walk<S::kParts> walk;
+        walk.begin(args, share_s);
+        Segment s;
+        if (warp == kWalkWarp) {
+            // --------------------------- the groups' segments, one ahead
+            bool more;
+            uint32_t seg = 0;
+            do {
+                more = walk.next(args, s);
+                if (lane == 0) {
+                    seg_s[seg & 1] = s;
+                    end_s[seg & 1] = walk.at;
+                    more_s[seg & 1] = more;
+                }
+                ++seg;
+                named_barrier<288>(3);
+            } while (more);
+        } else if (warp == kKeyWarp || warp == kValueWarp) {
+            // ------------------------------------------------------- copies
+            const bool keys = warp == kKeyWarp;
+            const CUtensorMap* map = keys ? &k_map : &v_map;
+            uint64_t* filled = keys ? key_full : stage_full;
+            uint64_t* freed = keys ? key_empty : stage_empty;
+            uint8_t* places = keys ? key_ring : stages;
+            static_assert(S::kKeys == S::kValues, "one walk of both rings");
+            const int box = page_box(a.page_size);
+            const int boxes = kTile / box;     // of a tile, each in one page
+            const bool mine = lane < boxes;
+            Turn<S::kKeys> turn;
+            bool ended = false;
+            while (!ended && walk.next(args, s)) {
+                const int n = s.k1 - s.k0;
+                const int32_t* table = a.page_table + (int64_t)s.r * a.max_pages;
+                // a box past the tokens, or of a page outside the cache, is filled
+                // with zeros: its page number is outside the map
+                auto page_of = [&](int j) -> int {
+                    const int slot = (s.k0 + j) * kTile + lane * box;
+                    if (!mine || j >= n || slot >= s.q.length) return (int)a.num_pages;
+                    const int p = __ldg(table + slot / a.page_size);
+                    return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
+                };
+                // the queries come to the L2 cache before the groups read them
+                if (!keys) {
+                    const int first_row = s.unit * args.unit_rows;
+                    for (int r = lane; r < s.rows; r += 32) {
+                        const unsigned short* at = static_cast<const unsigned short*>(a.q) +
+                                                   query_row(args, s, first_row + r);
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            if (64 * h < a.head_dim) prefetch_l2(at + 64 * h);
+                    }
+                }
+                int page = page_of(0);
+                for (int j = 0; j < n && !ended; ++j) {
+                    const int after = page_of(j + 1);
+#pragma unroll
+                    for (int part = 0; part < S::kParts; ++part) {
+                        if (!mbar_wait(&freed[turn.at], (turn.round & 1) ^ 1, failed)) {
+                            ended = true;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect(&filled[turn.at], S::kBytes);
+                        __syncwarp();
+                        if (mine)
+                            copy_box(map,
+                                     smem_addr(places) + turn.at * S::kBytes +
+                                         lane * box * S::kWidth,
+                                     &filled[turn.at], part * S::kWidth,
+                                     ((s.k0 + j) * kTile + lane * box) % a.page_size, s.head, page);
+                        turn.next();
+                    }
+                    page = after;
+                }
+            }
+            if (ended) {
+                // copies may be in flight: they land before the block ends
+                for (int i = 0; i < S::kKeys; ++i) {
+                    const uint32_t rounds = turn.round + (i < turn.at);
+                    const long long start = clock64();
+                    while (rounds != 0 && !mbar_try(&filled[i], (rounds - 1) & 1) &&
+                           clock64() - start < kWaitClocks) {
+                    }
+                }
+                __syncwarp();
+            }
+        } else if (warp == kIssueWarp) {
+            // -------------------------------------------- matrix instructions
+            // the type of an element has the number that a half has among wider types
+            constexpr uint32_t kScoreWord = mma_word(false, false, kTile, kTile);
+            constexpr uint32_t kOutWord = mma_word(false, true, kTile, S::kWidth);
+            const bool elected = elect_lane();
+            const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(q_tiles);
+            const uint32_t keys_at = smem_addr(key_ring);
+            uint32_t p_count[2] = {0, 0}, pairs = 0, seg = 0;
+            Turn<S::kKeys> key;
+            Turn<S::kSlots> value;
+            auto wait_key = [&]() -> uint32_t {
+                const uint32_t at = key.at;
+                mbar_wait(&key_full[at], key.round & 1, failed);
+                key.next();
+                return at;
+            };
+            auto wait_value = [&]() -> uint32_t {
+                const uint32_t at = value.at;
+                mbar_wait(&full[at], value.round & 1, failed);
+                value.next();
+                return at;
+            };
+            // a descriptor's address counts 16 bytes and stays below 2^14, so
+            // steps within a tile add to it
+            // (the first keys' part in `slot`, a second one in `slot2`; the queries are
+            // those of group q_tile, or of both parts)
+            auto scores = [&](int w, uint32_t slot, uint32_t slot2, uint32_t q_tile, bool free) {
+                if (elected) {
+#pragma unroll
+                    for (int part = 0; part < S::kParts; ++part) {
+                        const uint64_t kd = element_desc<S::kAtom>(
+                            keys_at + (part ? slot2 : slot) * S::kBytes);
+#pragma unroll
+                        for (int term = 0; term < S::kTerms; ++term) {
+                            const uint64_t qd = element_desc<S::kAtom>(
+                                q_at + ((q_tile + part) * S::kTerms + term) * S::kBytes);
+#pragma unroll
+                            for (int k = 0; k < S::kWidth / 32; ++k)
+                                mma_elements(tmem + w * S::kGroupColumns, qd + 2 * k, kd + 2 * k,
+                                             kScoreWord, part != 0 || term != 0 || k != 0);
+                        }
+                    }
+                    mma_commit(&s_full[w]);
+                    if (free) {
+                        mma_commit(&key_empty[slot]);
+                        if (S::kParts == 2) mma_commit(&key_empty[slot2]);
+                    }
+                }
+                __syncwarp();
+            };
+            // the product of half a tile's weights
+            auto values = [&](int w, uint32_t slot, int half, bool accumulate, bool free) {
+                const uint64_t vd = operand_desc(
+                    ring_at + slot * S::kTileBytes + half * (kTile / 2) * 128, S::kHalfBytes);
+                if (elected) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 32; ++k)
+                        mma_tmem(tmem + w * S::kGroupColumns + S::kOut,
+                                 tmem + w * S::kGroupColumns + half * (kTile / 4) + k * 8,
+                                 vd + (k * 16 * 128 >> 4), kOutWord, accumulate || k != 0);
+                    if (half == 1) mma_commit(&pv_done[w]);
+                    if (free) mma_commit(&empty[slot]);
+                }
+                __syncwarp();
+            };
+            // both halves, each behind its weights: the first runs while the second's
+            // weights are computed
+            auto product = [&](int w, uint32_t slot, bool accumulate, bool free) -> bool {
+                const uint32_t parity = p_count[w]++ & 1;
+                if (!mbar_wait(&p_low[w], parity, failed)) return false;
+                tmem_fence_after();
+                values(w, slot, 0, accumulate, false);
+                if (!mbar_wait(&p_high[w], parity, failed)) return false;
+                tmem_fence_after();
+                values(w, slot, 1, true, free);
+                return true;
+            };
+            while (walk.next(args, s)) {
+                const int n = s.k1 - s.k0;
+                mbar_wait(&q_full[0], seg & 1, failed);
+                if (s.pair) mbar_wait(&q_full[1], pairs++ & 1, failed);
+                tmem_fence_after();
+                if (S::kParts == 2) {
+                    uint32_t k = wait_key(), k2 = wait_key();
+                    scores(0, k, k2, 0, false);
+                    scores(1, k, k2, 0, true);
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        const uint32_t v = wait_value();
+                        if (!product(0, v, j > 0, true)) break;
+                        if (more) {
+                            k = wait_key();
+                            k2 = wait_key();
+                            scores(0, k, k2, 0, false);
+                        }
+                        const uint32_t v2 = wait_value();
+                        if (!product(1, v2, j > 0, true)) break;
+                        if (more) scores(1, k, k2, 0, true);
+                    }
+                } else if (s.pair) {
+                    uint32_t k = wait_key();
+                    scores(0, k, 0, 0, false);
+                    scores(1, k, 0, 1, true);
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        // both are at hand before the weights are
+                        const uint32_t v = wait_value();
+                        if (more) k = wait_key();
+                        if (!product(0, v, j > 0, false)) break;
+                        if (more) scores(0, k, 0, 0, false);
+                        if (!product(1, v, j > 0, true)) break;
+                        if (more) scores(1, k, 0, 1, true);
+                    }
+                } else {
+                    for (int w = 0; w < min(2, n); ++w) scores(w, wait_key(), 0, 0, true);
+                    for (int j = 0; j < n; ++j) {
+                        const int w = j & 1;
+                        const uint32_t v = wait_value();
+                        if (!product(w, v, j > 1, true)) break;
+                        if (j + 2 < n) scores(w, wait_key(), 0, 0, true);
+                    }
+                }
+                if (elected) mma_commit(&q_empty);
+                __syncwarp();
+                ++seg;
+            }
+            // everything issued is done before the block ends, also after a failure
+            if (elected) mma_commit(&last);
+            __syncwarp();
+            const long long start = clock64();
+            while (!mbar_try(&last, 0) && clock64() - start < kWaitClocks) {
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------- softmax
+        more_registers<kSoftmaxRegisters>();
+        const int w = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + w * S::kGroupColumns + lanes;
+        const uint32_t o_at = s_at + S::kOut;
+        uint32_t seg = 0, count = 0;
+        if (threadIdx.x == 0) static_cast<Cut*>(a.workspace)[blockIdx.x].last = -1;
+        for (;;) {
+            named_barrier<288>(3);
+            if (!*static_cast<volatile int*>(&more_s[seg & 1])) break;
+            const volatile Segment& s = seg_s[seg & 1];
+            const int n = s.k1 - s.k0;
+            constexpr bool kSplit = S::kParts == 2;   // both groups have the same rows
+            const int row0 = s.pair && !kSplit ? w * kTile : 0;   // the group's in the unit
+            const int first_row = s.unit * args.unit_rows + row0;
+            const int rows = s.pair && !kSplit ? (w == 0 ? kTile : s.rows - kTile) : s.rows;
+            const int column0 = kSplit ? w * S::kWidth : 0;       // of the group's accumulators
+            const bool active = (warp & 3) * 32 < rows;   // a warp with no row only keeps step
+            const bool here = row < rows;
+            const int node = (first_row + row) / group;
+            const int64_t token = s.q.begin + node;
+            const int64_t head = (int64_t)s.head * group + (first_row + row) - node * group;
+            const unsigned long long* mask =
+                reinterpret_cast<const unsigned long long*>(a.tree_mask) +
+                (here ? token : 0) * a.mask_words;
+            // asked for long before the tiles that need it
+            const uint64_t mask_word = here ? __ldg(mask) : 0;
+
+            // The scales of a tile's blocks of 16 slots, lane b those of block b (the
+            // upper lanes the same again): asked for a tile ahead, their page two.
+            const int step = s.pair ? 1 : 2;
+            auto page_at = [&](int j) -> int {
+                const uint32_t slot = (s.k0 + j) * kTile + (lane & 7) * 16;
+                return j < n && (int)slot < s.q.length
+                           ? __ldg(a.page_table + (int64_t)s.r * a.max_pages + sc.page_of(slot))
+                           : -1;
+            };
+            auto scales_at = [&](int j, int page) -> uint32_t {
+                if (page < 0 || page >= a.num_pages) return 0x3F803F80u;  // 1 and 1
+                return sc.both(page, s.head, (s.k0 + j) * kTile + (lane & 7) * 16, a.page_size);
+            };
+            const int j0 = s.pair ? 0 : w;
+            uint32_t scales = scales_at(j0, page_at(j0));
+            int page = page_at(j0 + step);
+
+            // this group's queries, rows of the unit, into swizzled shared memory, or
+            // its part of all of them
+            if (s.pair || w == 0) {
+                if (seg > 0) mbar_wait(&q_empty, (seg - 1) & 1, failed);
+                uint8_t* tile = q_tiles + (s.pair ? w : 0) * S::kTerms * S::kBytes;
+                constexpr int kPer = S::kWidth / 8;   // lanes a row
+                constexpr int kStep = 128 / kPer;
+                const int ch = row % kPer;
+                const unsigned short* from =
+                    static_cast<const unsigned short*>(a.q) + ch * 8;
+                const bool inside = column0 + ch * 8 < a.head_dim;
+                // rows of the warp together, so that the lanes of a row meet
+#pragma unroll 4
+                for (int base = 0; base < rows; base += kStep) {
+                    const int r = base + row / kPer;
+                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                    if (r < rows) {
+                        const unsigned short* at = from + query_row(args, s, first_row + r);
+                        if (inside) x = __ldg(reinterpret_cast<const uint4*>(at + column0));
+                        // of a head in parts the other part's, for the row's largest
+                        if (kSplit && S::kWidth - column0 + ch * 8 < a.head_dim)
+                            y = __ldg(reinterpret_cast<const uint4*>(at + S::kWidth - column0));
+                    }
+                    float q[8], most = 0.f;
+                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+                    const uint32_t others[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        widen_pair<kBf16>(words[i] ^ args.flip, q[2 * i], q[2 * i + 1]);
+                        most = fmaxf(most, fmaxf(fabsf(q[2 * i]), fabsf(q[2 * i + 1])));
+                        if (kSplit) {
+                            float z0, z1;
+                            widen_pair<kBf16>(others[i], z0, z1);
+                            most = fmaxf(most, fmaxf(fabsf(z0), fabsf(z1)));
+                        }
+                    }
+#pragma unroll
+                    for (int d = kPer / 2; d >= 1; d >>= 1)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                    const int shift = term_shift(most);
+                    const float f = __uint_as_float((uint32_t)(127 - shift) << 23);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i] *= f;
+                    if (r < rows) {
+                        if (ch == 0) shift_s[w][r] = (int8_t)shift;
+                        uint8_t* to = tile + piece_at<S::kWidth>(r, ch >> 1) + 8 * (ch & 1);
+#pragma unroll
+                        for (int term = 0; term < S::kTerms; ++term) {
+                            uint32_t e[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                e[i] = nearest_elements(q[2 * i], q[2 * i + 1]);
+                                // what this term leaves
+                                const uint32_t h = halves_of((uint16_t)e[i]);
+                                const float2 z =
+                                    __half22float2(*reinterpret_cast<const __half2*>(&h));
+                                q[2 * i] -= z.x;
+                                q[2 * i + 1] -= z.y;
+                            }
+                            *reinterpret_cast<uint2*>(to + term * S::kBytes) =
+                                make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+                        }
+                    }
+                }
+                fence_async_proxy();
+                mbar_arrive(&q_full[w]);
+            }
+
+            float top = -INFINITY, sum = 0.f, ref = -INFINITY, heap = 0.f;
+            float c = 0.f;
+            bool begun = false;
+            for (int j = j0; j < n; j += step) {
+                const int first = (s.k0 + j) * kTile;
+                const bool masked = first + kTile > s.q.ctx;
+                const uint32_t scales_now = scales;
+                scales = scales_at(j + step, page);
+                page = page_at(j + 2 * step);
+                MaskWindow window;
+                if (masked && here)
+                    window = mask_window(mask, mask_word, a.mask_words, s.q.ctx, first);
+                if (!mbar_wait(&s_full[w], count & 1, failed)) break;
+                tmem_fence_after();
+                if (active) {
+                    // the queries, and with them their shifts, were there before the scores
+                    if (!begun)
+                        c = args.c *
+                            __uint_as_float(
+                                (uint32_t)(127 + *static_cast<volatile int8_t*>(
+                                                     &shift_s[s.pair ? w : 0][row])) << 23);
+                    // Scores of what is not seen become -infinity in tensor memory, in a walk
+                    // of their own: few tiles have any, and the loops below stay short
+                    if (masked) {
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t bits =
+                                here ? seen_bits(window, a.mask_words, s.q.ctx, s.q.length,
+                                                 first + 32 * q)
+                                     : 0u;
+                            __syncwarp();
+                            uint32_t x[32];
+                            tmem_load(s_at + 32 * q, x);
+                            tmem_wait_load(x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(bits >> i & 1)) x[i] = 0xFF800000u;
+                            tmem_store(s_at + 32 * q, x);
+                        }
+                        tmem_wait_store();
+                    }
+                    // lane b has block b's: the key scale, and log2 of the value scale, which
+                    // is exact for a power of two (a scale of 0 as 2^-1000)
+                    const float k_scale = scale_value((unsigned short)scales_now);
+                    const float v_log = scale_log(scales_now >> 16);
+                    // The row's scores are walked twice, 64 columns at a time: the
+                    // upper half and then the lower for the maximum, the lower, still in
+                    // registers, and the upper again for the weights.  The walks are loops:
+                    // unrolled, four roles' instructions do not stay in their cache (256
+                    // rows over 32 x 16384 slots: 538 us).  A block that the row sees nothing
+                    // of is -infinity whatever its scales (a minimum or maximum with NaN
+                    // is the other number).
+                    uint32_t v[2][32];
+                    float now = top, reach = -INFINITY;
+#pragma unroll 1
+                    for (int h = 1; h >= 0; --h) {
+                        float m[4];
+                        tmem_load_max16(s_at + 64 * h, v[0], 0, m[0]);
+                        tmem_load_max16(s_at + 64 * h + 16, v[0], 16, m[1]);
+                        tmem_load_max16(s_at + 64 * h + 32, v[1], 0, m[2]);
+                        tmem_load_max16(s_at + 64 * h + 48, v[1], 16, m[3]);
+                        tmem_wait_load(v[0]);
+                        tmem_settle(v[0], m[0]);
+                        tmem_settle(v[1], m[1]);
+                        asm volatile("" : "+f"(m[2]), "+f"(m[3]));
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const float f = fmaxf(
+                                c * __shfl_sync(0xffffffffu, k_scale, 4 * h + b), 1.17549435e-38f);
+                            const float x = m[b] * f;
+                            now = fmaxf(now, x);
+                            reach =
+                                fmaxf(reach, x + __shfl_sync(0xffffffffu, v_log, 4 * h + b));
+                        }
+                    }
+                    const float base = now == -INFINITY ? 0.f : now;
+                    sum *= exp2_fast(top - base);
+                    top = now;
+                    // a new reference only where the tile's largest weight is far from it
+                    const float fall = ref - reach;
+                    const bool move =
+                        here && (-fall > kRise ||
+                                 (fall > kFall && heap * exp2_fast(fall) < kMostSum));
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float f =
+                            move ? (ref == -INFINITY ? 0.f : exp2_fast(ref - reach)) : 1.f;
+                        if (move) ref = reach;
+                        heap *= f;
+                        if (begun) {
+                            mbar_wait(&pv_done[w], (count - 1) & 1, failed);
+                            tmem_fence_after();
+#pragma unroll 1
+                            for (int q = 0; q < S::kWidth / 32; ++q) {
+                                uint32_t o[32];
+                                tmem_load(o_at + 32 * q, o);
+                                tmem_wait_load(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_store(o_at + 32 * q, o);
+                            }
+                        }
+                    }
+                    // at most this much for the tile's 128 weights
+                    if (ref != -INFINITY) heap += exp2_fast(reach - ref + kBias + 8.f);
+                    const uint64_t base2 = pack_f32(-base, -base);
+                    const float to_ref = base - ref + kBias;
+                    uint64_t part[2] = {0, 0};
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t(&x)[32] = v[q];
+                            tmem_wait_load(x);
+                            uint32_t p[16];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int b = 4 * half + 2 * q + h;
+                                const float f =
+                                    fmaxf(c * __shfl_sync(0xffffffffu, k_scale, b), 1.17549435e-38f);
+                                // weights relative to the row's reference
+                                const float by = exp2_fast(
+                                    fminf(__shfl_sync(0xffffffffu, v_log, b) + to_ref, 126.f));
+                                const uint64_t f2 = pack_f32(f, f), by2 = pack_f32(by, by);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint64_t pair =
+                                        pack_f32(as_float(x[16 * h + 2 * i]),
+                                                 as_float(x[16 * h + 2 * i + 1]));
+                                    float x0, x1;
+                                    unpack_f32(fma_f32x2(pair, f2, base2), x0, x1);
+                                    const uint64_t e2 = pack_f32(exp2_fast(x0), exp2_fast(x1));
+                                    part[i & 1] = add_f32x2(part[i & 1], e2);
+                                    unpack_f32(mul_f32x2(e2, by2), x0, x1);
+                                    p[8 * h + i] = round_pair<false>(x0, x1);
+                                }
+                            }
+                            if (half == 0) tmem_load(s_at + 64 + 32 * q, x);
+                            // over columns whose scores have been read
+                            tmem_store(s_at + 32 * half + 16 * q, p);
+                        }
+                        tmem_wait_store();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(half ? &p_high[w] : &p_low[w]);
+                    }
+                    float p0, p1;
+                    unpack_f32(add_f32x2(part[0], part[1]), p0, p1);
+                    sum += p0 + p1;
+                } else {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&p_low[w]);
+                        mbar_arrive(&p_high[w]);
+                    }
+                }
+                begun = true;
+                ++count;
+            }
+            if (begun) mbar_wait(&pv_done[w], (count - 1) & 1, failed);
+            tmem_fence_after();
+
+            // ------------------------------------ the segment's rows go out
+            const bool join = !s.pair && n > 1;   // both groups hold states of the same rows
+            float4* exchange = reinterpret_cast<float4*>(q_tiles);
+            if (join && w == 1) {
+                mbar_wait(&q_empty, seg & 1, failed);   // the queries have been read
+                if (active) {
+                    const float f =
+                        ref == -INFINITY ? 0.f : exp2_fast(fminf(ref - kBias - top, 126.f));
+#pragma unroll 1
+                    for (int q = 0; q < S::kWidth / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_load(o_at + 32 * q, o);
+                        tmem_wait_load(o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            exchange[(q * 8 + i) * kTile + row] = make_float4(
+                                __uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                __uint_as_float(o[4 * i + 2]) * f,
+                                __uint_as_float(o[4 * i + 3]) * f);
+                    }
+                    join_s[row][0] = top;
+                    join_s[row][1] = sum;
+                }
+            }
+            if (join) named_barrier<256>(1);
+            if (s.pair || w == 0) {
+                // accumulators relative to the row's top
+                float f1 = 0.f;
+                if (join && here) {
+                    const float other = join_s[row][0];
+                    const float m = fmaxf(top, other);
+                    const float base = m == -INFINITY ? 0.f : m;
+                    f1 = exp2_fast(other - base);
+                    sum = sum * exp2_fast(top - base) + join_s[row][1] * f1;
+                    top = m;
+                }
+                const float f0 =
+                    ref == -INFINITY ? 0.f : exp2_fast(fminf(ref - kBias - top, 126.f));
+                const bool whole = s.k0 == 0 && s.k1 == s.q.tiles;
+                if (threadIdx.x == 0 && s.k0 == 0 && !whole) {
+                    Cut cut = {};
+                    cut.last = share_of(share_s.total, end_s[seg & 1] - 1 + (s.q.tiles - s.k1),
+                                        share_s.shares);
+                    cut.rows = s.rows;
+                    cut.begin = s.q.begin;
+                    cut.first_row = s.unit * args.unit_rows;
+                    cut.head = s.head;
+                    static_cast<Cut*>(a.workspace)[blockIdx.x] = cut;
+                }
+                const bool spoiled = *failed;
+                if (spoiled) sum = __int_as_float(0x7FC00000);  // NaN, not an unfinished sum
+                const volatile int* found = bad_s[seg & 3];
+                const bool bad = found[0] | found[1] | found[2] | found[3];
+                const int64_t o_row = token * a.q_heads + head;
+                float* state = static_cast<float*>(a.workspace) +
+                               state_at(blockIdx.x, s.k0 == 0 ? 1 : 0, args.rows_cap, D);
+                const int state_row = row0 + row;
+                float* pairs = state + 2 * state_row;
+                float* acc = state + (2 + column0) * args.rows_cap + 8 * state_row;
+                const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+                if (active) {
+#pragma unroll 1
+                    for (int q = 0; q < S::kWidth / 32; ++q) {
+                        const int column = column0 + 32 * q;
+                        uint32_t o[32];
+                        if (begun) {
+                            tmem_load(o_at + 32 * q, o);
+                            tmem_wait_load(o);
+                        }
+                        float x[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * f0;
+                        if (kSplit && spoiled) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = __int_as_float(0x7FC00000);
+                        }
+                        if (join) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 y = exchange[(q * 8 + i) * kTile + row];
+                                x[4 * i] = fmaf(y.x, f1, x[4 * i]);
+                                x[4 * i + 1] = fmaf(y.y, f1, x[4 * i + 1]);
+                                x[4 * i + 2] = fmaf(y.z, f1, x[4 * i + 2]);
+                                x[4 * i + 3] = fmaf(y.w, f1, x[4 * i + 3]);
+                            }
+                        }
+                        if (bad && here) {
+                            // the drafted values that were cleared, to the rows
+                            // that see them
+                            for (int slot = max(s.q.ctx, s.k0 * kTile);
+                                 slot < min(s.q.length, s.k1 * kTile); ++slot) {
+                                const MaskWindow one = mask_window(mask, mask_word, a.mask_words,
+                                                                   s.q.ctx, slot);
+                                if (!(seen_bits(one, a.mask_words, s.q.ctx, s.q.length, slot) & 1))
+                                    continue;
+                                const int64_t at = slot_offset(
+                                    a.page_table, a.max_pages, a.page_size, a.num_pages,
+                                    a.page_stride, a.slot_stride, s.r, slot);
+                                if (at < 0) continue;
+                                const uint8_t* vrow = static_cast<const uint8_t*>(a.v_cache) + at +
+                                                      s.head * a.head_stride + column;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    if (column + i >= a.head_dim) break;
+                                    if ((vrow[i] & 0x7F) == 0x7F) x[i] = __int_as_float(0x7FC00000);
+                                }
+                            }
+                        }
+                        if (here && whole) {
+                            uint4* dst = reinterpret_cast<uint4*>(
+                                static_cast<unsigned short*>(a.out) + o_row * a.head_dim + column);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (column + 8 * i >= a.head_dim) break;
+                                uint32_t y[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    y[e] = round_pair<kBf16>(x[8 * i + 2 * e] * inv,
+                                                             x[8 * i + 2 * e + 1] * inv);
+                                dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                        } else if (here) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4*>(
+                                    acc + (q * 4 + i / 2) * 8 * args.rows_cap + (i & 1) * 4) =
+                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        }
+                        __syncwarp();  // the next load is the whole warp's
+                    }
+                    if (here && column0 == 0) {
+                        if (!whole) {
+                            pairs[0] = top;
+                            pairs[1] = sum;
+                        } else if (a.lse != nullptr) {
+                            a.lse[o_row] = sum == 0.f ? -INFINITY
+                                                      : top * 0.69314718055994531f + logf(sum);
+                        }
+                    }
+                }
+            }
+            tmem_fence_before();
+            named_barrier<256>(2);
+            ++seg;
+        }
+    }
+
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kIssueWarp) tmem_free(tmem, 512);
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_tc(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
+                      const CUtensorMap& v, cudaStream_t stream) {
+    using S = Shape<D, kBf16>;
+    auto* fn = tree_attention_fp8_tc_kernel<D, kBf16>;
+    cudaError_t e =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(fn, dim3((unsigned)args.blocks), dim3(kThreads), S::kSmem, stream,
+                      programmatic_launch(), args, sc, k, v);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(
+        tree_attention_join_kernel<D, kBf16>,
+        dim3((unsigned)args.blocks, (unsigned)((args.rows_cap + kJoinRows - 1) / kJoinRows)),
+        dim3(kJoinThreads), 0, stream, programmatic_launch(), args);
+}
+
+}  // namespace
+
+int64_t tree_attention_fp8_tc_workspace(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t D,
+                                        const DeviceFacts& dev) {
+    return 4 * state_at(tc_blocks(dev), 0, tc_rows_cap(T, q_heads, kv_heads, D), padded_width(D));
+}
+
+cudaError_t launch_tree_attention_fp8_tc(const ple_tree_attention_fp8_args& f,
+                                         const CUtensorMap& k, const CUtensorMap& v,
+                                         const DeviceFacts& dev, cudaStream_t stream) {
+    const ple_tree_attention_args& a = f.base;
+    TcArgs args;
+    args.a = a;
+    args.blocks = tc_blocks(dev);
+    args.group = a.q_heads / a.kv_heads;
+    args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads, a.head_dim);
+    args.unit_rows = unit_rows(padded_width(a.head_dim));
+    args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+    args.flip = a.scale < 0 ? 0x80008000u : 0u;
+    const Scales sc = scales_of(f);
+    const bool bf16 = a.dtype == PLE_BF16;
+    switch (padded_width(a.head_dim)) {
+        case 64:
+            return bf16 ? launch_tc<64, true>(args, sc, k, v, stream)
+                        : launch_tc<64, false>(args, sc, k, v, stream);
+        case 128:
+            return bf16 ? launch_tc<128, true>(args, sc, k, v, stream)
+                        : launch_tc<128, false>(args, sc, k, v, stream);
+        default:
+            return bf16 ? launch_tc<256, true>(args, sc, k, v, stream)
+                        : launch_tc<256, false>(args, sc, k, v, stream);
+    }
+}
+
+}  // namespace ple

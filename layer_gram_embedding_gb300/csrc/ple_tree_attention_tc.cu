@@ -80,10 +80,6 @@ struct Reference {
 // it further has no weight above 2^-50 of the row's, and O stays far inside 32 bits.
 constexpr float kMostSum = 0x1p60f;
 
-__host__ __device__ constexpr int unit_rows(int width) {
-    return width > 128 ? kTile : 2 * kTile;
-}
-
 template <int D>
 struct Shape {
     static constexpr int kParts = D > 128 ? 2 : 1;   // of a head
@@ -100,19 +96,6 @@ struct Shape {
     static constexpr uint32_t kGroupColumns = 256;
     static constexpr uint32_t kOut = 128;
 };
-
-// K_j's and V_j's places in the order of copies K_0, K_1, V_0, K_2, V_1, ... of
-// a segment of n tiles: the order in which the issuing warp wants them.  Of heads
-// in parts five places hold no three tiles: K_0, V_0, K_1, V_1, ..., a part after
-// the other.
-template <int kParts>
-__device__ __forceinline__ int key_item(int j) {
-    return kParts == 2 ? 4 * j : j == 0 ? 0 : 2 * j - 1;
-}
-template <int kParts>
-__device__ __forceinline__ int value_item(int j, int n) {
-    return kParts == 2 ? 4 * j + 2 : j < n - 1 ? 2 * j + 2 : 2 * j + 1;
-}
 
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -843,12 +826,6 @@ bool encode_cache(CUtensorMap* map, const ple_tree_attention_args& a, const void
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int tc_rows_cap(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
-    const int64_t rows = T * (q_heads / kv_heads);
-    const int most = unit_rows(padded_width(head_dim));
-    return (int)(rows < most ? (rows + 3) / 4 * 4 : most);  // 16-byte rows
 }
 
 template <int D, bool kBf16>

@@ -2,6 +2,8 @@
 // pages (ple_cache_api.cu), next to ple_tree_internal.h.
 #pragma once
 
+#include <cuda.h>
+
 #include "ple_tree_internal.h"
 
 namespace ple {
@@ -13,6 +15,14 @@ int64_t tree_attention_fp8_workspace(int64_t T, int32_t q_heads, int32_t kv_head
                                      int32_t head_dim, const DeviceFacts& dev);
 cudaError_t launch_tree_attention_fp8(const ple_tree_attention_fp8_args& a,
                                       const DeviceFacts& dev, cudaStream_t stream);
+
+// Its kernel for many rows a key head (ple_tree_attention_fp8_tc.cu), on the caches' tensor
+// maps.
+int64_t tree_attention_fp8_tc_workspace(int64_t T, int32_t q_heads, int32_t kv_heads,
+                                        int32_t head_dim, const DeviceFacts& dev);
+cudaError_t launch_tree_attention_fp8_tc(const ple_tree_attention_fp8_args& a,
+                                         const CUtensorMap& k, const CUtensorMap& v,
+                                         const DeviceFacts& dev, cudaStream_t stream);
 
 cudaError_t launch_tree_commit_fp8(const ple_tree_commit_fp8_args& a, cudaStream_t stream);
 

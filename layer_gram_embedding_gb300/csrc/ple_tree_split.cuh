@@ -21,6 +21,12 @@ __host__ __device__ constexpr int padded_width(int head_dim) {
     return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
 }
 
+// Rows of a key head that go together on the tensor cores: 256, or as many as there is
+// tensor memory for accumulators of.
+__host__ __device__ constexpr int unit_rows(int width) {
+    return width > 128 ? kTile : 2 * kTile;
+}
+
 struct TcArgs {
     ple_tree_attention_args a;
     int32_t blocks;      // shares
@@ -226,6 +232,19 @@ __host__ __device__ __forceinline__ int64_t state_at(int64_t block, int slot, in
                                                      int D) {
     return kMaxBlocks * (int64_t)(sizeof(Cut) / 4) +
            (block * 2 + slot) * (int64_t)rows_cap * (D + 2);
+}
+
+// K_j's and V_j's places in the order of copies K_0, K_1, V_0, K_2, V_1, ... of
+// a segment of n tiles: the order in which the issuing warp wants them.  Of heads
+// in parts five places hold no three tiles: K_0, V_0, K_1, V_1, ..., a part after
+// the other.
+template <int kParts>
+__device__ __forceinline__ int key_item(int j) {
+    return kParts == 2 ? 4 * j : j == 0 ? 0 : 2 * j - 1;
+}
+template <int kParts>
+__device__ __forceinline__ int value_item(int j, int n) {
+    return kParts == 2 ? 4 * j + 2 : j < n - 1 ? 2 * j + 2 : 2 * j + 1;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -447,6 +466,12 @@ EncodeTiled encode_tiled() {
 
 int tc_blocks(const DeviceFacts& dev) {
     return dev.sm_count < kMaxBlocks ? dev.sm_count : kMaxBlocks;
+}
+
+int tc_rows_cap(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+    const int64_t rows = T * (q_heads / kv_heads);
+    const int most = unit_rows(padded_width(head_dim));
+    return (int)(rows < most ? (rows + 3) / 4 * 4 : most);  // 16-byte rows
 }
 
 }  // namespace
