@@ -56,18 +56,32 @@ __device__ __forceinline__ uint32_t nan_flags(uint32_t w) {
 }
 
 // A scale (bfloat16) as a float.
-__device__ __forceinline__ float scale_value(unsigned short bits) {
-    return __uint_as_float((uint32_t)bits << 16);
+__device__ __forceinline__ float scale_value(uint32_t bits) {
+    return __uint_as_float(bits << 16);
 }
 
-// log2 of a scale (the bits of a bfloat16), exact for a power of two; of 0 a finite
-// number, less than that of any other.
+// log2 of a scale (the bits of a bfloat16), exact for a power of two, and finite whatever
+// it is.
 __device__ __forceinline__ float scale_log(uint32_t bits) {
-    const float scale = scale_value((unsigned short)bits);
+    const float scale = scale_value(bits);
     if ((bits & 0x7F) == 0 && bits - 0x80 < 0x7F00) return (float)((int)(bits >> 7) - 127);
     float l;
     asm("lg2.approx.f32 %0, %1;" : "=f"(l) : "f"(scale));
-    return scale == 0.f ? -1000.f : l;
+    return fminf(fmaxf(l, -1000.f), 1000.f);
+}
+
+// Loads that are issued where they stand: what asks ahead is not moved to where its
+// answer is used.
+// (Into a whole register: two of 16 bits would be put into one, behind the loads.)
+__device__ __forceinline__ uint32_t load_now(const unsigned short* p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int load_now(const int* p) {
+    int v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
 }
 
 // Where the attention kernels find scales.
@@ -83,12 +97,21 @@ struct Scales {
     __device__ __forceinline__ uint32_t page_of(uint32_t slot) const {
         return (__umulhi(slot, page_magic) + slot) >> page_shift;
     }
-    // The scales of a slot's keys (low half) and values, its page being `number`.
-    __device__ __forceinline__ uint32_t both(int number, int of_head, uint32_t slot,
-                                             int page_size) const {
+    __device__ __forceinline__ int in_page(uint32_t slot, int page_size) const {
+        return (int)(slot - page_of(slot) * page_size);
+    }
+
+    // Asks for the scales of a slot's keys and values, its page being `number` of `pages` (of
+    // any other: 1).  Nothing here waits for them.
+    __device__ __forceinline__ void ask(int number, int64_t pages, int of_head, uint32_t slot,
+                                        int page_size, uint32_t& of_keys,
+                                        uint32_t& of_values) const {
+        of_keys = of_values = 0x3F80;
+        if (number < 0 || number >= pages) return;
         const int64_t at = number * page + of_head * head +
                            ((slot - page_of(slot) * page_size) >> shift);
-        return __ldg(k + at) | (uint32_t)__ldg(v + at) << 16;
+        of_keys = load_now(k + at);
+        of_values = load_now(v + at);
     }
 };
 

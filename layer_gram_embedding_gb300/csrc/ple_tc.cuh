@@ -57,6 +57,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     return !__any_sync(0xffffffffu, over);
 }
 
+// The same for one lane.
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+    if (mbar_try(bar, parity)) return true;
+    const long long start = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (clock64() - start > kWaitClocks) *failed = 1;
+        if (*failed) return false;
+    }
+    return true;
+}
+
 // A whole warp waits until *count has come to `least`, as mbar_wait does.
 __device__ __forceinline__ void count_wait(const volatile uint32_t* count, uint32_t least,
                                            volatile int* failed) {
@@ -113,6 +124,14 @@ __device__ __forceinline__ void copy_box(const CUtensorMap* map, uint32_t dst, u
         "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+
+// The same box to the L2 cache alone.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     map),
+                 "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
 }
 
 // Sixteen bytes to shared memory behind the thread's back, and all of them there.
@@ -264,13 +283,21 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t at, uint32_t lead) {
            (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// The same for a tile of 8-bit elements whose rows are the swizzle's span: atoms of 8
-// rows, kAtom bytes (1024 with the 128-byte swizzle, 512 with that of 64).
+// Descriptors as a low word, to which steps add, and a constant high one.  Of a tile of
+// halves whose rows are the reduction (as operand_desc), and of a tile of 8-bit elements
+// whose rows are the swizzle's span: atoms of 8 rows, kAtom bytes (1024 with the 128-byte
+// swizzle, 512 with that of 64).
+__device__ __forceinline__ uint32_t half_desc_low(uint32_t at, uint32_t lead) {
+    return ((at >> 4) & 0x3FFF) | ((lead >> 4) & 0x3FFF) << 16;
+}
+__host__ __device__ constexpr uint32_t half_desc_high() { return 1024 >> 4 | 1u << 14 | 2u << 29; }
+__device__ __forceinline__ uint32_t element_desc_low(uint32_t at) {
+    return ((at >> 4) & 0x3FFF) | 1u << 16;
+}
 template <uint32_t kAtom>
-__device__ __forceinline__ uint64_t element_desc(uint32_t at) {
+__host__ __device__ constexpr uint32_t element_desc_high() {
     static_assert(kAtom == 1024 || kAtom == 512, "");
-    return (uint64_t)((at >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(kAtom >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)(kAtom == 1024 ? 2 : 4) << 61;
+    return kAtom >> 4 | 1u << 14 | (kAtom == 1024 ? 2u : 4u) << 29;
 }
 
 // The instruction word of kind::f16: 32-bit accumulator, both operands f16 or
@@ -290,16 +317,6 @@ __device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// The same of 8-bit elements (kind::f8f6f4; both e4m3 with the word of f16), 32 a step.
-__device__ __forceinline__ void mma_elements(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
-                                             bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
-        : "memory");
-}
-
 // The same as mma_smem with A in tensor memory, two elements to a column.
 __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t word,
                                          bool accumulate) {
@@ -307,6 +324,28 @@ __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uin
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// With descriptors in words.  8-bit elements (kind::f8f6f4; both e4m3 with the word of
+// f16), 32 a step, and A of halves in tensor memory.
+template <uint32_t kWord, uint32_t kHigh>
+__device__ __forceinline__ void mma_elements_at(uint32_t d, uint32_t a, uint32_t b,
+                                                bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "n"(kWord), "r"((uint32_t)accumulate), "n"(kHigh)
+        : "memory");
+}
+template <uint32_t kWord, uint32_t kHigh>
+__device__ __forceinline__ void mma_tmem_at(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "n"(kWord), "r"((uint32_t)accumulate), "n"(kHigh)
         : "memory");
 }
 

@@ -49,10 +49,10 @@ constexpr float kMostSum = 0x1p60f;
 template <int W, int NT, int Teams>
 struct RowShape {
     static constexpr int kWarps = Teams * kTeam;
-    // a warp that copies, one that walks ahead, two that fill the warpgroup up: a
-    // register split is by warpgroups
+    // a warp that copies, one that walks ahead, one for the scales, and one that fills the
+    // warpgroup up: a register split is by warpgroups
     static constexpr int kThreads = 32 * (kWarps + 4);
-    static constexpr int kCopyWarp = kWarps, kWalkWarp = kWarps + 1;
+    static constexpr int kCopyWarp = kWarps, kWalkWarp = kWarps + 1, kScaleWarp = kWarps + 2;
     static constexpr int kRegisters = Teams == 2 ? 104 : 216, kFewRegisters = Teams == 2 ? 64 : 72;
     static constexpr int kHalves = W > 128 ? 2 : 1;     // boxes of a row
     static constexpr int kRowBytes = W / kHalves;       // 64 or 128: the swizzle's span
@@ -60,9 +60,9 @@ struct RowShape {
     // tiles of keys and values in flight: an SM's share of the measured bandwidth
     // times a memory latency of 1.2 us is 54 KB.  An even number, so that a team
     // that takes every second tile sees every round of its places
-    static constexpr int kStages = W == 64 ? 10 : W == 128 ? 4 : 2;
+    static constexpr int kStages = W == 64 ? 12 : W == 128 ? 6 : 3;
     static constexpr int kColumns = W / 8;              // of a lane
-    static constexpr int kRound = kColumns < 16 ? kColumns : 16;   // of them meet at a time
+    static constexpr int kRound = Teams == 2 ? 4 : 8;   // of them meet at a time
     static constexpr int kRounds = kColumns / kRound;
     // eight rows of every warp meet here; queries before that
     static constexpr int kMeetBytes = kWarps * 8 * 8 * kRound * 4;
@@ -102,11 +102,11 @@ __device__ __forceinline__ uint32_t query_at(int row, int piece) {
     return row * (2 * W) + ((piece ^ x) << 4);
 }
 
-// And for 16 bytes of a row of accumulators on their way to meet: two pieces and four
-// rows, every second one.
-template <int W>
+// And for 16 bytes of a row of accumulators on their way to meet: lanes that write
+// together have two pieces and four rows, every second one.
+template <int kRound>
 __device__ __forceinline__ int meet_at(int row, int f) {
-    return W == 64 ? f ^ (row >> 1 & 1) ^ (row & 4) : f ^ (row >> 1 & 3);
+    return kRound == 4 ? f ^ (row & 6) : f ^ (row >> 1 & 1) ^ (row & 4);
 }
 
 template <int W, int NT, int Teams, bool kBf16>
@@ -119,6 +119,8 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
     const ple_tree_attention_args& a = args.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages];
+    // a tile's scales, (a, log2 b) for each slice
+    __shared__ float2 scale_s[S::kStages][kTeam];
     __shared__ int64_t scratch[S::kThreads / 32];
     __shared__ Share share_s;
     __shared__ int failed_s;
@@ -136,7 +138,7 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 2);
             mbar_init(&empty[i], kTeam);
         }
         failed_s = 0;
@@ -169,6 +171,45 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
                 ++seg;
                 named_barrier<32 * (kWarps + 1)>(3);
             } while (more);
+        } else if (warp == S::kScaleWarp) {
+            // ------------------------------------------------------- scales
+            // lanes 0 to 7 a slice's each: asked for a tile ahead, their page two
+            int stage = 0;
+            uint32_t round = 0;
+            bool ended = false;
+            while (!ended && walk.next(args, s)) {
+                const int32_t* table = a.page_table + (int64_t)s.r * a.max_pages;
+                auto slice_page = [&](int k) -> int {
+                    const uint32_t slot = k * kTile + (lane & 7) * kSlice;
+                    int number = -1;
+                    if (k < s.k1 && (int)slot < s.q.length)
+                        number = load_now(table + sc.page_of(slot));
+                    return number;
+                };
+                uint32_t k_ahead, v_ahead;
+                auto ask = [&](int k, int number) {
+                    sc.ask(number, a.num_pages, s.head, k * kTile + (lane & 7) * kSlice,
+                           a.page_size, k_ahead, v_ahead);
+                };
+                ask(s.k0, slice_page(s.k0));
+                int number = slice_page(s.k0 + 1);
+                for (int k = s.k0; k < s.k1; ++k) {
+                    const float2 mine = make_float2(scale_value(k_ahead), scale_log(v_ahead));
+                    ask(k + 1, number);
+                    number = slice_page(k + 2);
+                    if (!mbar_wait(&empty[stage], (round & 1) ^ 1, failed)) {
+                        ended = true;
+                        break;
+                    }
+                    if (lane < 8) scale_s[stage][lane] = mine;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[stage]);
+                    if (++stage == S::kStages) {
+                        stage = 0;
+                        ++round;
+                    }
+                }
+            }
         } else if (warp == S::kCopyWarp) {
             // ------------------------------------------------------- copies
             const int box = page_box(a.page_size);
@@ -186,7 +227,7 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
                 auto page_of = [&](int k) -> int {
                     const int slot = k * kTile + which * box;
                     if (!mine || k >= s.k1 || slot >= s.q.length) return (int)a.num_pages;
-                    const int p = __ldg(table + slot / a.page_size);
+                    const int p = __ldg(table + sc.page_of(slot));
                     return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
                 };
                 int page = page_of(s.k0);
@@ -203,7 +244,7 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
                                  smem_addr(ring) + (2 * stage + !keys) * S::kTileBytes +
                                      half * (kTile * 128) + which * box * S::kRowBytes,
                                  &full[stage], half * 128,
-                                 (k * kTile + which * box) % a.page_size, s.head, page);
+                                 sc.in_page(k * kTile + which * box, a.page_size), s.head, page);
                     page = after;
                     if (++stage == S::kStages) {
                         stage = 0;
@@ -243,22 +284,6 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
         const int k0 = s.k0, k1 = s.k1, rows = s.rows, head = s.head;
         const int ctx = s.q.ctx, length = s.q.length;
         const int first_row = s.unit * args.unit_rows;
-        const int32_t* table = a.page_table + (int64_t)s.r * a.max_pages;
-
-        // the slice's scales, asked for a tile ahead, its page two
-        auto page_at = [&](int k) -> int {
-            const uint32_t slot = k * kTile + slice * kSlice;
-            return k < k1 && (int)slot < length ? __ldg(table + sc.page_of(slot)) : -1;
-        };
-        auto scales_at = [&](int k, int page) -> uint32_t {
-            if (page < 0 || page >= a.num_pages) return 0x3F803F80u;  // 1 and 1
-            return sc.both(page, head, k * kTile + slice * kSlice, a.page_size);
-        };
-        // this team's first tile
-        int mine = Teams == 1 || (stage & 1) == team ? k0 : k0 + 1;
-        uint32_t scales = scales_at(mine, page_at(mine));
-        int page = page_at(mine + Teams);
-
         // the rows' queries as halves in shared memory: a warp a row at a time
         for (int r = warp; r < 8 * NT; r += kWarps) {
             constexpr int kPer = W / 32;                 // elements a lane: 2, 4 or 8
@@ -333,9 +358,6 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
 
         for (int k = k0; k < k1; ++k) {
             if (Teams == 1 || (stage & 1) == team) {
-                const uint32_t scales_now = scales;
-                scales = scales_at(k + Teams, page);
-                page = page_at(k + 2 * Teams);
                 if (!mbar_wait(&full[stage], round & 1, failed)) break;
                 const uint8_t* keys = ring + 2 * stage * S::kTileBytes;
                 const uint8_t* vals = keys + S::kTileBytes;
@@ -397,14 +419,8 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
                         }
                     }
                     // ------------------------------------------- softmax
-                    const float k_scale = scale_value((unsigned short)scales_now);
-                    // the value scale as 2^v_log times a number of [1, 2)
-                    const uint32_t v_bits = scales_now & 0xFFFF0000u;
-                    const float v_log = (float)((int)(v_bits >> 23 & 255) - 127);
-                    const float v_rest = v_bits >> 23 == 0 ? 0.f
-                                         : v_bits >> 23 >= 255
-                                             ? __uint_as_float(v_bits)
-                                             : __uint_as_float((v_bits & 0x7FFFFFu) | 127u << 23);
+                    const float2 scales = scale_s[stage][slice];
+                    const float k_scale = scales.x, v_log = scales.y;
                     uint32_t seen[NT][2];
                     if (masked) {
 #pragma unroll
@@ -493,7 +509,7 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
                         for (int e = 0; e < 2; ++e) {
                             const float base = top[n][e] == -INFINITY ? 0.f : top[n][e];
                             const float f =
-                                exp2_fast(fminf(base + v_log - ref[n][e] + kBias, 126.f)) * v_rest;
+                                exp2_fast(fminf(base + v_log - ref[n][e] + kBias, 126.f));
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {
                                 const float weight = exp2_fast(x[n][e][z] - base);
@@ -637,7 +653,7 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
 #pragma unroll
                     for (int q = 0; q < S::kRound / 4; ++q) {
                         const int t = (part * S::kRound + 4 * q) / 2;
-                        put[meet_at<W>(2 * c + e, (S::kRound / 4) * g + q)] =
+                        put[meet_at<S::kRound>(2 * c + e, (S::kRound / 4) * g + q)] =
                             make_float4(o[n][t][e] * f, o[n][t][2 + e] * f, o[n][t + 1][e] * f,
                                         o[n][t + 1][2 + e] * f);
                     }
@@ -656,7 +672,7 @@ tree_attention_fp8_kernel(const __grid_constant__ TcArgs args, const __grid_cons
                     for (int w = 0; w < kWarps; ++w) {
                         total = fmaf(sum_s[w][row], exp2_fast(top_s[w][row] - base), total);
                         const float4 v = reinterpret_cast<const float4*>(
-                            meet)[(w * 8 + r) * kAcross + meet_at<W>(r, piece)];
+                            meet)[(w * 8 + r) * kAcross + meet_at<S::kRound>(r, piece)];
                         acc.x += v.x;
                         acc.y += v.y;
                         acc.z += v.z;

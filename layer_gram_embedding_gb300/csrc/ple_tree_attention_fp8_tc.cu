@@ -44,11 +44,15 @@ constexpr int kTurnWarp = 12;                                  // the first of f
 constexpr int kSoftmaxRegisters = 176, kOneTaskRegisters = 64, kTurnRegisters = 96;
 static_assert(2 * kSoftmaxRegisters + kOneTaskRegisters + kTurnRegisters == 4 * 128, "");
 
+constexpr int kScaleTiles = 16;
+
 // As in ple_tree_attention_fp8.cu.
 constexpr float kRise = 5.0f, kFall = 7.0f, kBias = 9.0f;
 constexpr float kMostSum = 0x1p60f;
 
-template <int D, bool kBf16>
+// kPairs: units of up to 256 rows (heads of up to 128 elements), 128 for each group; else
+// of up to 128, and the groups take the tiles in turn.
+template <int D, bool kBf16, bool kPairs>
 struct Shape {
     static constexpr int kParts = D > 128 ? 2 : 1;       // of a head
     static constexpr int kWidth = D / kParts;            // elements a part
@@ -56,15 +60,19 @@ struct Shape {
     static constexpr int kBytes = kTile * kWidth;        // of a part's tile of elements
     static constexpr int kTileBytes = 2 * kBytes;        // and of halves
     static constexpr int kHalfBytes = kTile * 128;       // a swizzled block of 64 halves a row
-    // rings: keys and values as they come, 64 KB or more of them, where an SM's share
-    // of the measured bandwidth times a memory latency of 1.2 us is 54; values as
-    // halves, those at work and the next ones
-    static constexpr int kKeys = kWidth == 64 ? 6 : kBf16 ? 3 : 2;
-    static constexpr int kValues = kKeys;
+    static constexpr int kQueryBytes = (kPairs ? 2 : 1) * kTerms * kBytes;
+    // rings of values as halves, those at work and the next ones, and of keys and values as
+    // they come, with what is left.  An SM's share of the measured bandwidth is 45 GB/s, a
+    // loaded memory answers in 2 us, and a place of the keys is taken up until its
+    // scores are done: with three of 16 KB 32 rows over 32 x 16384 slots take
+    // 264 us, with five KEYS5 us.
     static constexpr int kSlots = kWidth == 64 ? 4 : 2;
-    static constexpr int kQueryBytes = 2 * kTerms * kBytes;
-    static constexpr int kSmem =
-        kQueryBytes + (kKeys + kValues) * kBytes + kSlots * kTileBytes + 1024;
+    // 227 KB less the barriers and what else is shared
+    static constexpr int kRings = (kWidth == 64 ? 216 : 208) * 1024;
+    static constexpr int kPlaces = (kRings - kQueryBytes - kSlots * kTileBytes) / kBytes;
+    static constexpr int kKeys = (kPlaces + 1) / 2 + (kPlaces > 6 ? 1 : 0);
+    static constexpr int kValues = kPlaces - kKeys;
+    static constexpr int kSmem = kQueryBytes + kSlots * kTileBytes + kPlaces * kBytes + 1024;
     // half of the 512 columns for each group: S (and the weights over it), O behind it
     static constexpr uint32_t kGroupColumns = 256;
     static constexpr uint32_t kOut = 128;
@@ -72,16 +80,23 @@ struct Shape {
     static constexpr uint32_t kAtom = 8 * kWidth;
 };
 
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-    uint64_t v;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
-
 // A 16-byte piece's place in a tile of elements.
 template <int kWidth>
 __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
     return row * kWidth + ((kWidth == 128 ? piece ^ (row & 7) : piece ^ (row >> 1 & 3)) << 4);
+}
+
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at));
+    return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
 }
 
 // A place in a ring, and how often it was filled before.
@@ -97,13 +112,13 @@ struct Turn {
     }
 };
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                              const __grid_constant__ Scales sc,
                              const __grid_constant__ CUtensorMap k_map,
                              const __grid_constant__ CUtensorMap v_map) {
-    using S = Shape<D, kBf16>;
+    using S = Shape<D, kBf16, kPairs>;
     const ple_tree_attention_args& a = args.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t key_full[S::kKeys], key_empty[S::kKeys];
@@ -111,6 +126,11 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
     __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
     __shared__ __align__(8) uint64_t q_full[2], q_empty, s_full[2], p_low[2], p_high[2], pv_done[2];
     __shared__ __align__(8) uint64_t last;
+    // Tiles' scales, (a, log2 b) for each block of 16 slots, written as a tile is copied:
+    // more tiles than are ever on their way from there to the softmax.
+    __shared__ __align__(16) float2 scale_s[kScaleTiles][kTile / 16];
+    __shared__ __align__(8) uint64_t scale_full[kScaleTiles];
+    static_assert(S::kKeys + 4 <= kScaleTiles, "");
     __shared__ int64_t scratch[kThreads / 32];
     __shared__ Share share_s;
     __shared__ uint32_t tmem_s;
@@ -141,6 +161,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             mbar_init(&stage_full[i], 1);
             mbar_init(&stage_empty[i], 4);
         }
+        for (int i = 0; i < kScaleTiles; ++i) mbar_init(&scale_full[i], 1);
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(&full[i], 4);
             mbar_init(&empty[i], 1);
@@ -180,10 +201,18 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
         Turn<S::kValues> stage;
         Turn<S::kSlots> slot;
         uint32_t seg = 0;
-        // a lane's 16 elements of a row: eight lanes, or four, a row
-        constexpr int kAcross = S::kWidth / 16;
-        constexpr int kRows = 32 / kAcross;       // rows at a time
-        const int piece = lane % kAcross, row0 = mine * (kTile / 4) + lane / kAcross;
+        // A lane's 16 elements of a row, and its rows: of each eight in turn the rows first
+        // and first ^ 2 (of rows of 64 bytes: first alone).  Eight lanes that access
+        // memory together have four pieces of rows r and r ^ 5, and so meet eight banks in
+        // both tiles; a row two further on is an exclusive or on every address.
+        constexpr bool kWide = S::kWidth == 128;
+        const int piece = kWide ? (lane & 3) + (lane >> 1 & 4) : lane & 3;
+        const int first_row = mine * (kTile / 4) +
+                              (kWide ? (lane >> 4) ^ (lane >> 2 & 1) * 5 : lane >> 2);
+        const uint32_t from0 = piece_at<S::kWidth>(first_row, piece);
+        const uint32_t to0 = piece / 4 * S::kHalfBytes + first_row * 128 +
+                             ((2 * (piece & 3) ^ (first_row & 7)) << 4);
+        const uint32_t stages_at = smem_addr(stages), ring_at = smem_addr(ring);
         bool ended = false;
         while (!ended && walk.next(args, s)) {
             if (lane == 0) bad_s[seg & 3][mine] = 0;
@@ -194,23 +223,24 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                     ended = true;
                     break;
                 }
-                const uint8_t* from = stages + stage.at * S::kBytes;
-                uint8_t* to = ring + slot.at * S::kTileBytes + piece / 4 * S::kHalfBytes;
+                const uint32_t from = stages_at + stage.at * S::kBytes + from0;
+                const uint32_t to = ring_at + slot.at * S::kTileBytes + to0;
                 const int first = (s.k0 + i / S::kParts) * kTile;
-                const bool look = first + kTile > s.q.ctx;
-                const int seen_to = s.q.length - first, known_to = s.q.ctx - first;
-                if (look) {
-                    // cleared where they lie, in a walk of their own: few tiles have any
+                if (first + kTile > s.q.ctx) {
+                    // Values past the request's tokens, and NaN of drafted ones, cleared
+                    // where they lie, in a walk of their own: few tiles have any
+                    const int seen_to = s.q.length - first, known_to = s.q.ctx - first;
                     bool bad = false;
 #pragma unroll 1
-                    for (int k = 0; k < kTile / 4 / kRows; ++k) {
-                        const int row = row0 + k * kRows;
+                    for (int k = 0; k < 32; ++k) {
+                        const int row = mine * (kTile / 4) + k;
+                        if (row < known_to || lane >= S::kWidth / 16) continue;
                         uint4* at = reinterpret_cast<uint4*>(stages + stage.at * S::kBytes +
-                                                             piece_at<S::kWidth>(row, piece));
+                                                             row * S::kWidth) + lane;
                         if (row >= seen_to) {
                             *at = make_uint4(0, 0, 0, 0);
-                        } else if (row >= known_to) {
-                            uint4 v = *at;
+                        } else {
+                            const uint4 v = *at;
                             const uint32_t n[4] = {nan_flags(v.x), nan_flags(v.y), nan_flags(v.z),
                                                    nan_flags(v.w)};
                             if (n[0] | n[1] | n[2] | n[3]) {
@@ -225,24 +255,20 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                     if (__any_sync(0xffffffffu, bad) && lane == 0) bad_s[seg & 3][mine] = 1;
                     __syncwarp();
                 }
-#pragma unroll 4
-                for (int k = 0; k < kTile / 4 / kRows; ++k) {
-                    const int row = row0 + k * kRows;
-                    const uint4 v = *reinterpret_cast<const uint4*>(
-                        from + piece_at<S::kWidth>(row, piece));
-                    uint4 low, high;
-                    halves_of(v.x, low.x, low.y);
-                    halves_of(v.y, low.z, low.w);
-                    halves_of(v.z, high.x, high.y);
-                    halves_of(v.w, high.z, high.w);
-                    // the lanes of a row's other half store their pieces the other way
-                    // round: eight lanes meet eight banks
-                    uint8_t* at = to + row * 128;
-                    const int p0 = 2 * (piece & 3), turn = piece >> 2;
-                    *reinterpret_cast<uint4*>(at + (((p0 + turn) ^ (row & 7)) << 4)) =
-                        turn ? high : low;
-                    *reinterpret_cast<uint4*>(at + (((p0 + 1 - turn) ^ (row & 7)) << 4)) =
-                        turn ? low : high;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int odd = 0; odd < (kWide ? 2 : 1); ++odd) {
+                        const uint32_t turn = odd ? 2 * 128 + (2 << 4) : 0;
+                        const uint4 v = load_shared((from ^ turn) + k * 8 * S::kWidth);
+                        uint4 low, high;
+                        halves_of(v.x, low.x, low.y);
+                        halves_of(v.y, low.z, low.w);
+                        halves_of(v.z, high.x, high.y);
+                        halves_of(v.w, high.z, high.w);
+                        store_shared((to ^ turn) + k * 8 * 128, low);
+                        store_shared((to ^ turn ^ 16) + k * 8 * 128, high);
+                    }
                 }
                 fence_async_proxy();
                 __syncwarp();
@@ -281,11 +307,12 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             uint64_t* filled = keys ? key_full : stage_full;
             uint64_t* freed = keys ? key_empty : stage_empty;
             uint8_t* places = keys ? key_ring : stages;
-            static_assert(S::kKeys == S::kValues, "one walk of both rings");
+            const int most = keys ? S::kKeys : S::kValues;
             const int box = page_box(a.page_size);
             const int boxes = kTile / box;     // of a tile, each in one page
             const bool mine = lane < boxes;
-            Turn<S::kKeys> turn;
+            int at = 0;
+            uint32_t round = 0, tiles = 0;
             bool ended = false;
             while (!ended && walk.next(args, s)) {
                 const int n = s.k1 - s.k0;
@@ -295,7 +322,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                 auto page_of = [&](int j) -> int {
                     const int slot = (s.k0 + j) * kTile + lane * box;
                     if (!mine || j >= n || slot >= s.q.length) return (int)a.num_pages;
-                    const int p = __ldg(table + slot / a.page_size);
+                    const int p = __ldg(table + sc.page_of(slot));
                     return p < 0 || p >= a.num_pages ? (int)a.num_pages : p;
                 };
                 // the queries come to the L2 cache before the groups read them
@@ -309,32 +336,65 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                             if (64 * h < a.head_dim) prefetch_l2(at + 64 * h);
                     }
                 }
+                // the warp of the keys also hands over the scales: lanes 0 to 7 a block of 16
+                // slots each, asked for a tile ahead, their page two
+                auto block_slot = [&](int j) -> uint32_t {
+                    return (s.k0 + j) * kTile + (lane & 7) * 16;
+                };
+                auto block_page = [&](int j) -> int {
+                    const uint32_t slot = block_slot(j);
+                    int number = -1;
+                    if (keys && j < n && (int)slot < s.q.length)
+                        number = load_now(table + sc.page_of(slot));
+                    return number;
+                };
+                uint32_t k_ahead, v_ahead;
+                auto ask = [&](int j, int number) {
+                    sc.ask(number, a.num_pages, s.head, block_slot(j), a.page_size, k_ahead,
+                           v_ahead);
+                };
+                ask(0, block_page(0));
+                int number = block_page(1);
                 int page = page_of(0);
                 for (int j = 0; j < n && !ended; ++j) {
                     const int after = page_of(j + 1);
+                    if (keys) {
+                        const uint32_t entry = tiles++ % kScaleTiles;
+                        if (lane < 8)
+                            scale_s[entry][lane] =
+                                make_float2(scale_value(k_ahead), scale_log(v_ahead));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&scale_full[entry]);
+                        ask(j + 1, number);
+                        number = block_page(j + 2);
+                    }
 #pragma unroll
                     for (int part = 0; part < S::kParts; ++part) {
-                        if (!mbar_wait(&freed[turn.at], (turn.round & 1) ^ 1, failed)) {
+                        if (!mbar_wait(&freed[at], (round & 1) ^ 1, failed)) {
                             ended = true;
                             break;
                         }
-                        if (lane == 0) mbar_arrive_expect(&filled[turn.at], S::kBytes);
+                        if (lane == 0) mbar_arrive_expect(&filled[at], S::kBytes);
                         __syncwarp();
                         if (mine)
                             copy_box(map,
-                                     smem_addr(places) + turn.at * S::kBytes +
+                                     smem_addr(places) + at * S::kBytes +
                                          lane * box * S::kWidth,
-                                     &filled[turn.at], part * S::kWidth,
-                                     ((s.k0 + j) * kTile + lane * box) % a.page_size, s.head, page);
-                        turn.next();
+                                     &filled[at], part * S::kWidth,
+                                     sc.in_page((s.k0 + j) * kTile + lane * box, a.page_size), s.head,
+                                     page);
+                        if (++at == most) {
+                            at = 0;
+                            ++round;
+                        }
                     }
                     page = after;
                 }
             }
             if (ended) {
                 // copies may be in flight: they land before the block ends
-                for (int i = 0; i < S::kKeys; ++i) {
-                    const uint32_t rounds = turn.round + (i < turn.at);
+                for (int i = 0; i < most; ++i) {
+                    const uint32_t rounds = round + (i < at);
                     const long long start = clock64();
                     while (rounds != 0 && !mbar_try(&filled[i], (rounds - 1) & 1) &&
                            clock64() - start < kWaitClocks) {
@@ -344,136 +404,101 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             }
         } else if (warp == kIssueWarp) {
             // -------------------------------------------- matrix instructions
-            // the type of an element has the number that a half has among wider types
+            // One lane does all of it.  A tile is 32 instructions and six waits, and what
+            // stands between them is what the tensor cores wait for: descriptors are a
+            // base and constants, and nothing is shared with the warp's other lanes.
+            // The type of an element has the number that a half has among wider types.
             constexpr uint32_t kScoreWord = mma_word(false, false, kTile, kTile);
             constexpr uint32_t kOutWord = mma_word(false, true, kTile, S::kWidth);
-            const bool elected = elect_lane();
-            const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(q_tiles);
-            const uint32_t keys_at = smem_addr(key_ring);
-            uint32_t p_count[2] = {0, 0}, pairs = 0, seg = 0;
-            Turn<S::kKeys> key;
-            Turn<S::kSlots> value;
-            auto wait_key = [&]() -> uint32_t {
-                const uint32_t at = key.at;
-                mbar_wait(&key_full[at], key.round & 1, failed);
-                key.next();
-                return at;
-            };
-            auto wait_value = [&]() -> uint32_t {
-                const uint32_t at = value.at;
-                mbar_wait(&full[at], value.round & 1, failed);
-                value.next();
-                return at;
-            };
-            // a descriptor's address counts 16 bytes and stays below 2^14, so
-            // steps within a tile add to it
-            // (the first keys' part in `slot`, a second one in `slot2`; the queries are
-            // those of group q_tile, or of both parts)
-            auto scores = [&](int w, uint32_t slot, uint32_t slot2, uint32_t q_tile, bool free) {
-                if (elected) {
+            if (elect_lane()) {
+                const uint32_t values_at = half_desc_low(smem_addr(ring), S::kHalfBytes);
+                const uint32_t keys_at = element_desc_low(smem_addr(key_ring));
+                const uint32_t q_at = element_desc_low(smem_addr(q_tiles));
+                uint32_t p_count[2] = {0, 0}, pairs = 0, seg = 0;
+                Turn<S::kKeys> key;
+                Turn<S::kSlots> value;
+                auto wait_key = [&]() -> uint32_t {
+                    const uint32_t at = key.at;
+                    lane_wait(&key_full[at], key.round & 1, failed);
+                    key.next();
+                    return at;
+                };
+                auto wait_value = [&]() -> uint32_t {
+                    const uint32_t at = value.at;
+                    lane_wait(&full[at], value.round & 1, failed);
+                    value.next();
+                    return at;
+                };
+                while (walk.next(args, s)) {
+                    const int n = s.k1 - s.k0;
+                    lane_wait(&q_full[0], seg & 1, failed);
+                    if (s.pair) lane_wait(&q_full[1], pairs++ & 1, failed);
+                    tmem_fence_after();
+                    // Every step takes a group's weights and gives it its next scores: a
+                    // tile for both groups in two steps, or tiles in turn
+                    const bool both = S::kParts == 2 || (kPairs && s.pair);
+                    const int steps = both ? 2 * n : n;
+                    uint32_t k = 0, k2 = 0, v = 0;
+#pragma unroll 1
+                    for (int i = -2; i < steps; ++i) {
+                        const int w = i & 1;
+                        const uint32_t at = tmem + w * S::kGroupColumns;
+                        if (i >= 0) {
+                            if (!both || S::kParts == 2 || w == 0) v = wait_value();
+                            const uint32_t vd = values_at + (v * S::kTileBytes >> 4);
+                            const uint32_t parity = p_count[w]++ & 1;
+                            // the first half's product runs while the second's weights
+                            // are computed
 #pragma unroll
-                    for (int part = 0; part < S::kParts; ++part) {
-                        const uint64_t kd = element_desc<S::kAtom>(
-                            keys_at + (part ? slot2 : slot) * S::kBytes);
+                            for (int half = 0; half < 2; ++half) {
+                                if (!lane_wait(half ? &p_high[w] : &p_low[w], parity, failed))
+                                    break;
+                                tmem_fence_after();
 #pragma unroll
-                        for (int term = 0; term < S::kTerms; ++term) {
-                            const uint64_t qd = element_desc<S::kAtom>(
-                                q_at + ((q_tile + part) * S::kTerms + term) * S::kBytes);
+                                for (int c = 0; c < kTile / 32; ++c)
+                                    mma_tmem_at<kOutWord, half_desc_high()>(
+                                        at + S::kOut, at + half * (kTile / 4) + c * 8,
+                                        vd + ((half * (kTile / 2) + c * 16) * 128 >> 4),
+                                        half != 0 || c != 0 || i >= 2);
+                            }
+                            if (*failed) break;
+                            mma_commit(&pv_done[w]);
+                            if (!both || S::kParts == 2 || w == 1) mma_commit(&empty[v]);
+                        }
+                        if (i + 2 < steps) {
+                            if (!both || w == 0) {
+                                k = wait_key();
+                                if (S::kParts == 2) k2 = wait_key();
+                            }
+                            const uint32_t q_tile = both && S::kParts == 1 ? w : 0;
 #pragma unroll
-                            for (int k = 0; k < S::kWidth / 32; ++k)
-                                mma_elements(tmem + w * S::kGroupColumns, qd + 2 * k, kd + 2 * k,
-                                             kScoreWord, part != 0 || term != 0 || k != 0);
+                            for (int part = 0; part < S::kParts; ++part) {
+                                const uint32_t kd = keys_at + ((part ? k2 : k) * S::kBytes >> 4);
+                                const uint32_t qd =
+                                    q_at + ((q_tile + part) * S::kTerms * S::kBytes >> 4);
+#pragma unroll
+                                for (int term = 0; term < S::kTerms; ++term)
+#pragma unroll
+                                    for (int c = 0; c < S::kWidth / 32; ++c)
+                                        mma_elements_at<kScoreWord, element_desc_high<S::kAtom>()>(
+                                            at, qd + (term * S::kBytes >> 4) + 2 * c, kd + 2 * c,
+                                            part != 0 || term != 0 || c != 0);
+                            }
+                            mma_commit(&s_full[w]);
+                            if (!both || w == 1) {
+                                mma_commit(&key_empty[k]);
+                                if (S::kParts == 2) mma_commit(&key_empty[k2]);
+                            }
                         }
                     }
-                    mma_commit(&s_full[w]);
-                    if (free) {
-                        mma_commit(&key_empty[slot]);
-                        if (S::kParts == 2) mma_commit(&key_empty[slot2]);
-                    }
+                    mma_commit(&q_empty);
+                    ++seg;
                 }
-                __syncwarp();
-            };
-            // the product of half a tile's weights
-            auto values = [&](int w, uint32_t slot, int half, bool accumulate, bool free) {
-                const uint64_t vd = operand_desc(
-                    ring_at + slot * S::kTileBytes + half * (kTile / 2) * 128, S::kHalfBytes);
-                if (elected) {
-#pragma unroll
-                    for (int k = 0; k < kTile / 32; ++k)
-                        mma_tmem(tmem + w * S::kGroupColumns + S::kOut,
-                                 tmem + w * S::kGroupColumns + half * (kTile / 4) + k * 8,
-                                 vd + (k * 16 * 128 >> 4), kOutWord, accumulate || k != 0);
-                    if (half == 1) mma_commit(&pv_done[w]);
-                    if (free) mma_commit(&empty[slot]);
+                // everything issued is done before the block ends, also after a failure
+                mma_commit(&last);
+                const long long start = clock64();
+                while (!mbar_try(&last, 0) && clock64() - start < kWaitClocks) {
                 }
-                __syncwarp();
-            };
-            // both halves, each behind its weights: the first runs while the second's
-            // weights are computed
-            auto product = [&](int w, uint32_t slot, bool accumulate, bool free) -> bool {
-                const uint32_t parity = p_count[w]++ & 1;
-                if (!mbar_wait(&p_low[w], parity, failed)) return false;
-                tmem_fence_after();
-                values(w, slot, 0, accumulate, false);
-                if (!mbar_wait(&p_high[w], parity, failed)) return false;
-                tmem_fence_after();
-                values(w, slot, 1, true, free);
-                return true;
-            };
-            while (walk.next(args, s)) {
-                const int n = s.k1 - s.k0;
-                mbar_wait(&q_full[0], seg & 1, failed);
-                if (s.pair) mbar_wait(&q_full[1], pairs++ & 1, failed);
-                tmem_fence_after();
-                if (S::kParts == 2) {
-                    uint32_t k = wait_key(), k2 = wait_key();
-                    scores(0, k, k2, 0, false);
-                    scores(1, k, k2, 0, true);
-                    for (int j = 0; j < n; ++j) {
-                        const bool more = j + 1 < n;
-                        const uint32_t v = wait_value();
-                        if (!product(0, v, j > 0, true)) break;
-                        if (more) {
-                            k = wait_key();
-                            k2 = wait_key();
-                            scores(0, k, k2, 0, false);
-                        }
-                        const uint32_t v2 = wait_value();
-                        if (!product(1, v2, j > 0, true)) break;
-                        if (more) scores(1, k, k2, 0, true);
-                    }
-                } else if (s.pair) {
-                    uint32_t k = wait_key();
-                    scores(0, k, 0, 0, false);
-                    scores(1, k, 0, 1, true);
-                    for (int j = 0; j < n; ++j) {
-                        const bool more = j + 1 < n;
-                        // both are at hand before the weights are
-                        const uint32_t v = wait_value();
-                        if (more) k = wait_key();
-                        if (!product(0, v, j > 0, false)) break;
-                        if (more) scores(0, k, 0, 0, false);
-                        if (!product(1, v, j > 0, true)) break;
-                        if (more) scores(1, k, 0, 1, true);
-                    }
-                } else {
-                    for (int w = 0; w < min(2, n); ++w) scores(w, wait_key(), 0, 0, true);
-                    for (int j = 0; j < n; ++j) {
-                        const int w = j & 1;
-                        const uint32_t v = wait_value();
-                        if (!product(w, v, j > 1, true)) break;
-                        if (j + 2 < n) scores(w, wait_key(), 0, 0, true);
-                    }
-                }
-                if (elected) mma_commit(&q_empty);
-                __syncwarp();
-                ++seg;
-            }
-            // everything issued is done before the block ends, also after a failure
-            if (elected) mma_commit(&last);
-            __syncwarp();
-            const long long start = clock64();
-            while (!mbar_try(&last, 0) && clock64() - start < kWaitClocks) {
             }
             __syncwarp();
         }
@@ -485,7 +510,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + w * S::kGroupColumns + lanes;
         const uint32_t o_at = s_at + S::kOut;
-        uint32_t seg = 0, count = 0;
+        uint32_t seg = 0, count = 0, tiles = 0;   // tiles: of the segments before
         if (threadIdx.x == 0) static_cast<Cut*>(a.workspace)[blockIdx.x].last = -1;
         for (;;) {
             named_barrier<288>(3);
@@ -508,22 +533,10 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             // asked for long before the tiles that need it
             const uint64_t mask_word = here ? __ldg(mask) : 0;
 
-            // The scales of a tile's blocks of 16 slots, lane b those of block b (the
-            // upper lanes the same again): asked for a tile ahead, their page two.
             const int step = s.pair ? 1 : 2;
-            auto page_at = [&](int j) -> int {
-                const uint32_t slot = (s.k0 + j) * kTile + (lane & 7) * 16;
-                return j < n && (int)slot < s.q.length
-                           ? __ldg(a.page_table + (int64_t)s.r * a.max_pages + sc.page_of(slot))
-                           : -1;
-            };
-            auto scales_at = [&](int j, int page) -> uint32_t {
-                if (page < 0 || page >= a.num_pages) return 0x3F803F80u;  // 1 and 1
-                return sc.both(page, s.head, (s.k0 + j) * kTile + (lane & 7) * 16, a.page_size);
-            };
+            // what every tile asks for stays in registers: shared memory is busy
+            const int k0 = s.k0, ctx = s.q.ctx, length = s.q.length;
             const int j0 = s.pair ? 0 : w;
-            uint32_t scales = scales_at(j0, page_at(j0));
-            int page = page_at(j0 + step);
 
             // this group's queries, rows of the unit, into swizzled shared memory, or
             // its part of all of them
@@ -597,15 +610,16 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             float c = 0.f;
             bool begun = false;
             for (int j = j0; j < n; j += step) {
-                const int first = (s.k0 + j) * kTile;
-                const bool masked = first + kTile > s.q.ctx;
-                const uint32_t scales_now = scales;
-                scales = scales_at(j + step, page);
-                page = page_at(j + 2 * step);
+                const int first = (k0 + j) * kTile;
+                const bool masked = first + kTile > ctx;
                 MaskWindow window;
                 if (masked && here)
-                    window = mask_window(mask, mask_word, a.mask_words, s.q.ctx, first);
+                    window = mask_window(mask, mask_word, a.mask_words, ctx, first);
                 if (!mbar_wait(&s_full[w], count & 1, failed)) break;
+                // these came before the keys that the scores are of
+                const uint32_t entry = (tiles + j) % kScaleTiles;
+                if (!mbar_wait(&scale_full[entry], (tiles + j) / kScaleTiles & 1, failed)) break;
+                const float4* scales = reinterpret_cast<const float4*>(scale_s[entry]);
                 tmem_fence_after();
                 if (active) {
                     // the queries, and with them their shifts, were there before the scores
@@ -620,7 +634,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t bits =
-                                here ? seen_bits(window, a.mask_words, s.q.ctx, s.q.length,
+                                here ? seen_bits(window, a.mask_words, ctx, length,
                                                  first + 32 * q)
                                      : 0u;
                             __syncwarp();
@@ -634,38 +648,39 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                         tmem_wait_store();
                     }
-                    // lane b has block b's: the key scale, and log2 of the value scale, which
-                    // is exact for a power of two (a scale of 0 as 2^-1000)
-                    const float k_scale = scale_value((unsigned short)scales_now);
-                    const float v_log = scale_log(scales_now >> 16);
                     // The row's scores are walked twice, 64 columns at a time: the
                     // upper half and then the lower for the maximum, the lower, still in
-                    // registers, and the upper again for the weights.  The walks are loops:
-                    // unrolled, four roles' instructions do not stay in their cache (256
-                    // rows over 32 x 16384 slots: 538 us).  A block that the row sees nothing
-                    // of is -infinity whatever its scales (a minimum or maximum with NaN
-                    // is the other number).
+                    // registers, and the upper again for the weights.  A block that the row
+                    // sees nothing of is -infinity whatever its scales (a minimum or
+                    // maximum with NaN is the other number).
+                    // a block's factor from score to exponent of 2, and that log
+                    float factor[8], place[8];
                     uint32_t v[2][32];
                     float now = top, reach = -INFINITY;
-#pragma unroll 1
+#pragma unroll
                     for (int h = 1; h >= 0; --h) {
                         float m[4];
                         tmem_load_max16(s_at + 64 * h, v[0], 0, m[0]);
                         tmem_load_max16(s_at + 64 * h + 16, v[0], 16, m[1]);
                         tmem_load_max16(s_at + 64 * h + 32, v[1], 0, m[2]);
                         tmem_load_max16(s_at + 64 * h + 48, v[1], 16, m[3]);
+#pragma unroll
+                        for (int b = 4 * h; b < 4 * h + 4; b += 2) {
+                            const float4 two = scales[b / 2];
+                            factor[b] = fmaxf(c * two.x, 1.17549435e-38f);
+                            place[b] = two.y;
+                            factor[b + 1] = fmaxf(c * two.z, 1.17549435e-38f);
+                            place[b + 1] = two.w;
+                        }
                         tmem_wait_load(v[0]);
                         tmem_settle(v[0], m[0]);
                         tmem_settle(v[1], m[1]);
                         asm volatile("" : "+f"(m[2]), "+f"(m[3]));
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const float f = fmaxf(
-                                c * __shfl_sync(0xffffffffu, k_scale, 4 * h + b), 1.17549435e-38f);
-                            const float x = m[b] * f;
+                            const float x = m[b] * factor[4 * h + b];
                             now = fmaxf(now, x);
-                            reach =
-                                fmaxf(reach, x + __shfl_sync(0xffffffffu, v_log, 4 * h + b));
+                            reach = fmaxf(reach, x + place[4 * h + b]);
                         }
                     }
                     const float base = now == -INFINITY ? 0.f : now;
@@ -698,50 +713,50 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                     }
                     // at most this much for the tile's 128 weights
                     if (ref != -INFINITY) heap += exp2_fast(reach - ref + kBias + 8.f);
-                    const uint64_t base2 = pack_f32(-base, -base);
-                    const float to_ref = base - ref + kBias;
-                    uint64_t part[2] = {0, 0};
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
+                    // Weights with their value scale relative to the row's reference; the
+                    // sum takes a block's together, that scale out again.  A scale 2^-100
+                    // of what the reference stands for counts as that: its weights, which
+                    // the sum needs, would be lost, and its values are nothing to the row.
+                    const float to_ref = ref == -INFINITY ? 0.f : kBias - ref, least = -100.f - base;
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t(&x)[32] = v[q];
-                            tmem_wait_load(x);
-                            uint32_t p[16];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t(&x)[32] = v[q & 1];
+                        if (q > 1) tmem_wait_load(x);
+                        uint32_t p[16];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int b = 4 * half + 2 * q + h;
-                                const float f =
-                                    fmaxf(c * __shfl_sync(0xffffffffu, k_scale, b), 1.17549435e-38f);
-                                // weights relative to the row's reference
-                                const float by = exp2_fast(
-                                    fminf(__shfl_sync(0xffffffffu, v_log, b) + to_ref, 126.f));
-                                const uint64_t f2 = pack_f32(f, f), by2 = pack_f32(by, by);
+                        for (int h = 0; h < 2; ++h) {
+                            const int b = 2 * q + h;
+                            const float f = factor[b];
+                            const float at = fmaxf(place[b] + to_ref, least);
+                            const uint64_t f2 = pack_f32(f, f), at2 = pack_f32(at, at);
+                            uint64_t part[2];
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const uint64_t pair =
-                                        pack_f32(as_float(x[16 * h + 2 * i]),
-                                                 as_float(x[16 * h + 2 * i + 1]));
-                                    float x0, x1;
-                                    unpack_f32(fma_f32x2(pair, f2, base2), x0, x1);
-                                    const uint64_t e2 = pack_f32(exp2_fast(x0), exp2_fast(x1));
-                                    part[i & 1] = add_f32x2(part[i & 1], e2);
-                                    unpack_f32(mul_f32x2(e2, by2), x0, x1);
-                                    p[8 * h + i] = round_pair<false>(x0, x1);
-                                }
+                            for (int i = 0; i < 8; ++i) {
+                                const uint64_t pair =
+                                    pack_f32(as_float(x[16 * h + 2 * i]),
+                                             as_float(x[16 * h + 2 * i + 1]));
+                                float x0, x1;
+                                unpack_f32(fma_f32x2(pair, f2, at2), x0, x1);
+                                x0 = exp2_fast(x0);
+                                x1 = exp2_fast(x1);
+                                const uint64_t e2 = pack_f32(x0, x1);
+                                part[i & 1] = i < 2 ? e2 : add_f32x2(part[i & 1], e2);
+                                p[8 * h + i] = round_pair<false>(x0, x1);
                             }
-                            if (half == 0) tmem_load(s_at + 64 + 32 * q, x);
-                            // over columns whose scores have been read
-                            tmem_store(s_at + 32 * half + 16 * q, p);
+                            float p0, p1;
+                            unpack_f32(add_f32x2(part[0], part[1]), p0, p1);
+                            sum = fmaf(p0 + p1, exp2_fast(-(at + base)), sum);
                         }
-                        tmem_wait_store();
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(half ? &p_high[w] : &p_low[w]);
+                        if (q < 2) tmem_load(s_at + 32 * (q + 2), x);
+                        // over columns whose scores have been read
+                        tmem_store(s_at + 16 * q, p);
+                        if (q & 1) {
+                            tmem_wait_store();
+                            tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(q == 1 ? &p_low[w] : &p_high[w]);
+                        }
                     }
-                    float p0, p1;
-                    unpack_f32(add_f32x2(part[0], part[1]), p0, p1);
-                    sum += p0 + p1;
                 } else {
                     tmem_fence_before();
                     __syncwarp();
@@ -755,19 +770,22 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             }
             if (begun) mbar_wait(&pv_done[w], (count - 1) & 1, failed);
             tmem_fence_after();
+            tiles += n;
 
             // ------------------------------------ the segment's rows go out
-            const bool join = !s.pair && n > 1;   // both groups hold states of the same rows
+            // Where both groups hold states of the same rows, group 1's go to group 0
+            // through the queries' memory, half the columns at a time.
+            const bool join = !s.pair && n > 1;
             float4* exchange = reinterpret_cast<float4*>(q_tiles);
-            if (join && w == 1) {
-                mbar_wait(&q_empty, seg & 1, failed);   // the queries have been read
-                if (active) {
+            constexpr int kChunks = S::kWidth / 64;   // of 32 columns, in a half
+            auto hand_over = [&](int part) {
+                if (w == 1 && active) {
                     const float f =
                         ref == -INFINITY ? 0.f : exp2_fast(fminf(ref - kBias - top, 126.f));
 #pragma unroll 1
-                    for (int q = 0; q < S::kWidth / 32; ++q) {
+                    for (int q = 0; q < kChunks; ++q) {
                         uint32_t o[32];
-                        tmem_load(o_at + 32 * q, o);
+                        tmem_load(o_at + 32 * (part * kChunks + q), o);
                         tmem_wait_load(o);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -776,15 +794,24 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                                 __uint_as_float(o[4 * i + 2]) * f,
                                 __uint_as_float(o[4 * i + 3]) * f);
                     }
-                    join_s[row][0] = top;
-                    join_s[row][1] = sum;
                 }
+                named_barrier<256>(1);
+            };
+            if (join) {
+                if (w == 1) {
+                    mbar_wait(&q_empty, seg & 1, failed);   // the queries have been read
+                    if (active) {
+                        join_s[row][0] = top;
+                        join_s[row][1] = sum;
+                    }
+                }
+                hand_over(0);
             }
-            if (join) named_barrier<256>(1);
-            if (s.pair || w == 0) {
+            {
+                const bool out = s.pair || w == 0;   // whether these rows are this group's
                 // accumulators relative to the row's top
                 float f1 = 0.f;
-                if (join && here) {
+                if (join && w == 0 && here) {
                     const float other = join_s[row][0];
                     const float m = fmaxf(top, other);
                     const float base = m == -INFINITY ? 0.f : m;
@@ -816,9 +843,15 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                 float* pairs = state + 2 * state_row;
                 float* acc = state + (2 + column0) * args.rows_cap + 8 * state_row;
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                if (active) {
 #pragma unroll 1
-                    for (int q = 0; q < S::kWidth / 32; ++q) {
+                for (int part = 0; part < 2; ++part) {
+                    if (join && part == 1) {
+                        named_barrier<256>(1);
+                        hand_over(1);
+                    }
+                    if (!out || !active) continue;
+#pragma unroll 1
+                    for (int q = part * kChunks; q < (part + 1) * kChunks; ++q) {
                         const int column = column0 + 32 * q;
                         uint32_t o[32];
                         if (begun) {
@@ -835,7 +868,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                         if (join) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 y = exchange[(q * 8 + i) * kTile + row];
+                                const float4 y = exchange[(q % kChunks * 8 + i) * kTile + row];
                                 x[4 * i] = fmaf(y.x, f1, x[4 * i]);
                                 x[4 * i + 1] = fmaf(y.y, f1, x[4 * i + 1]);
                                 x[4 * i + 2] = fmaf(y.z, f1, x[4 * i + 2]);
@@ -886,14 +919,14 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                         __syncwarp();  // the next load is the whole warp's
                     }
-                    if (here && column0 == 0) {
-                        if (!whole) {
-                            pairs[0] = top;
-                            pairs[1] = sum;
-                        } else if (a.lse != nullptr) {
-                            a.lse[o_row] = sum == 0.f ? -INFINITY
-                                                      : top * 0.69314718055994531f + logf(sum);
-                        }
+                }
+                if (out && here && column0 == 0) {
+                    if (!whole) {
+                        pairs[0] = top;
+                        pairs[1] = sum;
+                    } else if (a.lse != nullptr) {
+                        a.lse[o_row] =
+                            sum == 0.f ? -INFINITY : top * 0.69314718055994531f + logf(sum);
                     }
                 }
             }
@@ -909,11 +942,11 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
     if (warp == kIssueWarp) tmem_free(tmem, 512);
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kPairs>
 cudaError_t launch_tc(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
                       const CUtensorMap& v, cudaStream_t stream) {
-    using S = Shape<D, kBf16>;
-    auto* fn = tree_attention_fp8_tc_kernel<D, kBf16>;
+    using S = Shape<D, kBf16, kPairs>;
+    auto* fn = tree_attention_fp8_tc_kernel<D, kBf16, kPairs>;
     cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
@@ -924,6 +957,22 @@ cudaError_t launch_tc(const TcArgs& args, const Scales& sc, const CUtensorMap& k
         tree_attention_join_kernel<D, kBf16>,
         dim3((unsigned)args.blocks, (unsigned)((args.rows_cap + kJoinRows - 1) / kJoinRows)),
         dim3(kJoinThreads), 0, stream, programmatic_launch(), args);
+}
+
+template <bool kBf16>
+cudaError_t launch_dtype(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
+                         const CUtensorMap& v, cudaStream_t stream) {
+    const bool pairs = args.unit_rows > kTile;
+    switch (padded_width(args.a.head_dim)) {
+        case 64:
+            return pairs ? launch_tc<64, kBf16, true>(args, sc, k, v, stream)
+                         : launch_tc<64, kBf16, false>(args, sc, k, v, stream);
+        case 128:
+            return pairs ? launch_tc<128, kBf16, true>(args, sc, k, v, stream)
+                         : launch_tc<128, kBf16, false>(args, sc, k, v, stream);
+        default:  // both parts' queries, as of two groups
+            return launch_tc<256, kBf16, true>(args, sc, k, v, stream);
+    }
 }
 
 }  // namespace
@@ -942,22 +991,15 @@ cudaError_t launch_tree_attention_fp8_tc(const ple_tree_attention_fp8_args& f,
     args.blocks = tc_blocks(dev);
     args.group = a.q_heads / a.kv_heads;
     args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads, a.head_dim);
+    // units of two groups' rows where a request's are so many on the average
     args.unit_rows = unit_rows(padded_width(a.head_dim));
+    if (a.num_tokens * args.group <= kTile * (int64_t)a.num_requests) args.unit_rows = kTile;
+    if (args.rows_cap > args.unit_rows) args.rows_cap = args.unit_rows;
     args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     args.flip = a.scale < 0 ? 0x80008000u : 0u;
     const Scales sc = scales_of(f);
-    const bool bf16 = a.dtype == PLE_BF16;
-    switch (padded_width(a.head_dim)) {
-        case 64:
-            return bf16 ? launch_tc<64, true>(args, sc, k, v, stream)
-                        : launch_tc<64, false>(args, sc, k, v, stream);
-        case 128:
-            return bf16 ? launch_tc<128, true>(args, sc, k, v, stream)
-                        : launch_tc<128, false>(args, sc, k, v, stream);
-        default:
-            return bf16 ? launch_tc<256, true>(args, sc, k, v, stream)
-                        : launch_tc<256, false>(args, sc, k, v, stream);
-    }
+    return a.dtype == PLE_BF16 ? launch_dtype<true>(args, sc, k, v, stream)
+                               : launch_dtype<false>(args, sc, k, v, stream);
 }
 
 }  // namespace ple
