@@ -57,12 +57,14 @@ struct RowShape {
     static constexpr int kHalves = W > 128 ? 2 : 1;     // boxes of a row
     static constexpr int kRowBytes = W / kHalves;       // 64 or 128: the swizzle's span
     static constexpr int kTileBytes = kTile * W;
-    // tiles of keys and values in flight: an SM's share of the measured bandwidth
-    // times a memory latency of 1.2 us is 54 KB.  An even number, so that a team
-    // that takes every second tile sees every round of its places
-    static constexpr int kStages = W == 64 ? 12 : W == 128 ? 6 : 3;
+    // tiles of keys and values in flight: an SM's share of the measured bandwidth is
+    // 45 GB/s, and a loaded memory answers in 2 us.  An even number, so that a team that
+    // takes every second tile sees every round of its places
+    static constexpr int kStages = W == 64 ? 10 : W == 128 ? 4 : 3;
     static constexpr int kColumns = W / 8;              // of a lane
-    static constexpr int kRound = Teams == 2 ? 4 : 8;   // of them meet at a time
+    // of them meet at a time: in rounds of 4, for two more tiles in flight, 256 decodes over
+    // 512 slots take 128 us instead of 96, and long contexts what they took
+    static constexpr int kRound = W == 128 ? 16 : 8;
     static constexpr int kRounds = kColumns / kRound;
     // eight rows of every warp meet here; queries before that
     static constexpr int kMeetBytes = kWarps * 8 * 8 * kRound * 4;
@@ -106,7 +108,7 @@ __device__ __forceinline__ uint32_t query_at(int row, int piece) {
 // together have two pieces and four rows, every second one.
 template <int kRound>
 __device__ __forceinline__ int meet_at(int row, int f) {
-    return kRound == 4 ? f ^ (row & 6) : f ^ (row >> 1 & 1) ^ (row & 4);
+    return kRound == 16 ? f ^ (row >> 1 & 3) : f ^ (row >> 1 & 1) ^ (row & 4);
 }
 
 template <int W, int NT, int Teams, bool kBf16>

@@ -62,10 +62,8 @@ struct Shape {
     static constexpr int kHalfBytes = kTile * 128;       // a swizzled block of 64 halves a row
     static constexpr int kQueryBytes = (kPairs ? 2 : 1) * kTerms * kBytes;
     // rings of values as halves, those at work and the next ones, and of keys and values as
-    // they come, with what is left.  An SM's share of the measured bandwidth is 45 GB/s, a
-    // loaded memory answers in 2 us, and a place of the keys is taken up until its
-    // scores are done: with three of 16 KB 32 rows over 32 x 16384 slots take
-    // 264 us, with five KEYS5 us.
+    // they come, with what is left (an SM's share of the measured bandwidth is 45 GB/s,
+    // and a loaded memory answers in 2 us)
     static constexpr int kSlots = kWidth == 64 ? 4 : 2;
     // 227 KB less the barriers and what else is shared
     static constexpr int kRings = (kWidth == 64 ? 216 : 208) * 1024;
@@ -543,62 +541,80 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             if (s.pair || w == 0) {
                 if (seg > 0) mbar_wait(&q_empty, (seg - 1) & 1, failed);
                 uint8_t* tile = q_tiles + (s.pair ? w : 0) * S::kTerms * S::kBytes;
-                constexpr int kPer = S::kWidth / 8;   // lanes a row
-                constexpr int kStep = 128 / kPer;
+                constexpr int kPer = S::kWidth / 8;      // lanes a row
+                constexpr int kAtOnce = 128 / kPer;      // rows
+                // rows in flight: one by one, a segment's queries took 10 us
+                constexpr int kAhead = kSplit ? 4 : 8;
                 const int ch = row % kPer;
                 const unsigned short* from =
                     static_cast<const unsigned short*>(a.q) + ch * 8;
                 const bool inside = column0 + ch * 8 < a.head_dim;
-                // rows of the warp together, so that the lanes of a row meet
-#pragma unroll 4
-                for (int base = 0; base < rows; base += kStep) {
-                    const int r = base + row / kPer;
-                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    if (r < rows) {
-                        const unsigned short* at = from + query_row(args, s, first_row + r);
-                        if (inside) x = __ldg(reinterpret_cast<const uint4*>(at + column0));
-                        // of a head in parts the other part's, for the row's largest
-                        if (kSplit && S::kWidth - column0 + ch * 8 < a.head_dim)
-                            y = __ldg(reinterpret_cast<const uint4*>(at + S::kWidth - column0));
-                    }
-                    float q[8], most = 0.f;
-                    const uint32_t words[4] = {x.x, x.y, x.z, x.w};
-                    const uint32_t others[4] = {y.x, y.y, y.z, y.w};
+                const int q_rows = rows;
+                // (rows of the warp together, so that the lanes of a row meet)
+#pragma unroll 1
+                for (int base = 0; base < q_rows; base += kAhead * kAtOnce) {
+                    uint4 x[kAhead], y[kSplit ? kAhead : 1];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        widen_pair<kBf16>(words[i] ^ args.flip, q[2 * i], q[2 * i + 1]);
-                        most = fmaxf(most, fmaxf(fabsf(q[2 * i]), fabsf(q[2 * i + 1])));
-                        if (kSplit) {
-                            float z0, z1;
-                            widen_pair<kBf16>(others[i], z0, z1);
-                            most = fmaxf(most, fmaxf(fabsf(z0), fabsf(z1)));
+                    for (int z = 0; z < kAhead; ++z) {
+                        const int r = base + z * kAtOnce + row / kPer;
+                        x[z] = make_uint4(0, 0, 0, 0);
+                        if constexpr (kSplit) y[z] = make_uint4(0, 0, 0, 0);
+                        if (r < q_rows) {
+                            const unsigned short* at = from + query_row(args, s, first_row + r);
+                            if (inside) x[z] = __ldg(reinterpret_cast<const uint4*>(at + column0));
+                            // of a head in parts the other part's, for the row's largest
+                            if constexpr (kSplit)
+                                if (S::kWidth - column0 + ch * 8 < a.head_dim)
+                                    y[z] = __ldg(reinterpret_cast<const uint4*>(at + S::kWidth -
+                                                                                column0));
                         }
                     }
 #pragma unroll
-                    for (int d = kPer / 2; d >= 1; d >>= 1)
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-                    const int shift = term_shift(most);
-                    const float f = __uint_as_float((uint32_t)(127 - shift) << 23);
+                    for (int z = 0; z < kAhead; ++z) {
+                        const int r = base + z * kAtOnce + row / kPer;
+                        if (base + z * kAtOnce >= q_rows) break;
+                        float q[8], most = 0.f;
+                        const uint32_t words[4] = {x[z].x, x[z].y, x[z].z, x[z].w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) q[i] *= f;
-                    if (r < rows) {
-                        if (ch == 0) shift_s[w][r] = (int8_t)shift;
-                        uint8_t* to = tile + piece_at<S::kWidth>(r, ch >> 1) + 8 * (ch & 1);
-#pragma unroll
-                        for (int term = 0; term < S::kTerms; ++term) {
-                            uint32_t e[4];
+                        for (int i = 0; i < 4; ++i) {
+                            widen_pair<kBf16>(words[i] ^ args.flip, q[2 * i], q[2 * i + 1]);
+                            most = fmaxf(most, fmaxf(fabsf(q[2 * i]), fabsf(q[2 * i + 1])));
+                        }
+                        if constexpr (kSplit) {
+                            const uint32_t others[4] = {y[z].x, y[z].y, y[z].z, y[z].w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                e[i] = nearest_elements(q[2 * i], q[2 * i + 1]);
-                                // what this term leaves
-                                const uint32_t h = halves_of((uint16_t)e[i]);
-                                const float2 z =
-                                    __half22float2(*reinterpret_cast<const __half2*>(&h));
-                                q[2 * i] -= z.x;
-                                q[2 * i + 1] -= z.y;
+                                float z0, z1;
+                                widen_pair<kBf16>(others[i], z0, z1);
+                                most = fmaxf(most, fmaxf(fabsf(z0), fabsf(z1)));
                             }
-                            *reinterpret_cast<uint2*>(to + term * S::kBytes) =
-                                make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+                        }
+#pragma unroll
+                        for (int d = kPer / 2; d >= 1; d >>= 1)
+                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                        const int shift = term_shift(most);
+                        const float f = __uint_as_float((uint32_t)(127 - shift) << 23);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) q[i] *= f;
+                        if (r < q_rows) {
+                            if (ch == 0) shift_s[w][r] = (int8_t)shift;
+                            uint8_t* to = tile + piece_at<S::kWidth>(r, ch >> 1) + 8 * (ch & 1);
+#pragma unroll
+                            for (int term = 0; term < S::kTerms; ++term) {
+                                uint32_t e[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    e[i] = nearest_elements(q[2 * i], q[2 * i + 1]);
+                                    // what this term leaves
+                                    const uint32_t h = halves_of((uint16_t)e[i]);
+                                    const float2 left =
+                                        __half22float2(*reinterpret_cast<const __half2*>(&h));
+                                    q[2 * i] -= left.x;
+                                    q[2 * i + 1] -= left.y;
+                                }
+                                *reinterpret_cast<uint2*>(to + term * S::kBytes) =
+                                    make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+                            }
                         }
                     }
                 }
