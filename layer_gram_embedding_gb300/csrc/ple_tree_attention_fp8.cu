@@ -739,15 +739,6 @@ bool encode_cache(CUtensorMap* map, const ple_tree_attention_args& a, const void
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows that go together: as many as a lane's registers hold accumulators of.
-int fp8_rows(int width) { return width > 128 ? 16 : 32; }
-
-int fp8_rows_cap(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
-    const int64_t rows = T * (q_heads / kv_heads);
-    const int most = fp8_rows(padded_width(head_dim));
-    return (int)(rows < most ? (rows + 3) / 4 * 4 : most);  // 16-byte rows
-}
-
 template <int W, int NT, int Teams, bool kBf16>
 cudaError_t launch_rows(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
                         const CUtensorMap& v, cudaStream_t stream) {
@@ -769,9 +760,7 @@ template <int W, bool kBf16>
 cudaError_t launch_width(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
                          const CUtensorMap& v, cudaStream_t stream) {
     if (args.unit_rows <= 8) return launch_rows<W, 1, W == 256 ? 1 : 2, kBf16>(args, sc, k, v, stream);
-    if (args.unit_rows <= 16) return launch_rows<W, 2, 1, kBf16>(args, sc, k, v, stream);
-    if constexpr (W <= 128) return launch_rows<W, 4, 1, kBf16>(args, sc, k, v, stream);
-    return cudaErrorInvalidValue;
+    return launch_rows<W, 2, 1, kBf16>(args, sc, k, v, stream);
 }
 
 template <bool kBf16>
@@ -808,12 +797,11 @@ cudaError_t launch_tree_attention_fp8(const ple_tree_attention_fp8_args& f,
     args.a = a;
     args.blocks = tc_blocks(dev);
     args.group = a.q_heads / a.kv_heads;
-    args.rows_cap = fp8_rows_cap(a.num_tokens, a.q_heads, a.kv_heads, a.head_dim);
-    // rows of one node a request, or of few in all, need no more tiles of rows
-    const int64_t rows = a.num_tokens <= a.num_requests ? args.group : args.rows_cap;
-    const int most = fp8_rows(padded_width(a.head_dim));
-    args.unit_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : most;
-    if (args.rows_cap > args.unit_rows) args.rows_cap = args.unit_rows;
+    // rows that go together: as many as a request's key heads have on the average (of a
+    // request with more, several units)
+    const int64_t rows = a.num_tokens * args.group;
+    args.unit_rows = rows <= 8 * (int64_t)a.num_requests ? 8 : 16;
+    args.rows_cap = (int)(rows < args.unit_rows ? (rows + 3) / 4 * 4 : args.unit_rows);
     // a scale of 0 as the least normal number, so that exponents stay numbers
     args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     args.flip = a.scale < 0 ? 0x80008000u : 0u;
