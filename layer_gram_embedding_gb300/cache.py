@@ -431,6 +431,8 @@ def ple_plan_pages(page_table: torch.Tensor, ctx_lens: torch.Tensor, source: tor
             raise ValueError(f"{where}: the next batch must have a row")
         if not 0 <= L <= P:
             raise ValueError(f"{where}: limit must be from 0 to num_pages")
+    if not 0 < page_size < 2 ** 31:
+        raise ValueError(f"{where}: page_size must be positive, below 2^31")
     device, M = page_table.device, table_shape[1]
     if N * M > 2 ** 31 - 1 - P:
         raise ValueError(f"{where}: num_rows * max_pages + num_pages must stay below 2^31")

@@ -32,17 +32,19 @@ struct AppendPlan {
     int32_t shift;         // log2 of a cache block's tokens
 };
 
-// A lane's eight values as elements, four and four.
-__device__ __forceinline__ uint2 row_elements(const Pair (&x)[4], float inv) {
+// A lane's eight values as elements, four and four.  The reciprocal of a power of two is
+// exact; another scale, which a cache may have been filled with, divides: a quotient
+// beside the border of two elements stays on its side in 32 bits, a product need not.
+__device__ __forceinline__ uint2 row_elements(const Pair (&x)[4], float scale, float inv) {
+    const bool power = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float lo, hi;
         split(x[i], lo, hi);
         // what is not finite is NaN, not the largest element
-        lo = fabsf(lo) < INFINITY ? lo * inv : __int_as_float(0x7FC00000);
-        hi = fabsf(hi) < INFINITY ? hi * inv : __int_as_float(0x7FC00000);
-        w[i] = elements_of(lo, hi);
+        w[i] = power ? nearest_elements(lo, hi, inv)
+                     : nearest_elements(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale), 1.0f);
     }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
@@ -217,7 +219,7 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
                     if (i0 + i * RPW >= count) break;
                     Pair x[4];
                     turned(i0, i, x);
-                    const uint2 e = row_elements(x, inv);
+                    const uint2 e = row_elements(x, scale, inv);
                     const int k = i0 + i * RPW;
                     if (live && k + in_group < count) {
                         *reinterpret_cast<uint32_t*>(dst + k * a.slot_stride) = e.x;

@@ -126,14 +126,6 @@ __device__ __forceinline__ void copy_box(const CUtensorMap* map, uint32_t dst, u
         : "memory");
 }
 
-// The same box to the L2 cache alone.
-__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int x, int y, int z, int w) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                     map),
-                 "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
-}
-
 // Sixteen bytes to shared memory behind the thread's back, and all of them there.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
