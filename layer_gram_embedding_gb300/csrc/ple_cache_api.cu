@@ -149,7 +149,9 @@ extern "C" ple_status ple_tree_commit_fp8(const ple_tree_commit_fp8_args* args, 
                              !aligned(a.next_context, id_bytes))))
         return PLE_ERR_ALIGN;
     if (commit_outputs_overlap(a)) return PLE_ERR_SIZE;
-    return finish(ple::launch_tree_commit_fp8(*args, static_cast<cudaStream_t>(stream)));
+    ple::DeviceFacts dev;
+    if (ple_status st = with_device(&dev); st != PLE_OK) return st;
+    return finish(ple::launch_tree_commit_fp8(*args, dev, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int64_t ple_plan_pages_workspace(int32_t num_rows, int32_t num_pages) {

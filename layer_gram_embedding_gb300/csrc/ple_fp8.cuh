@@ -43,10 +43,10 @@ __device__ __forceinline__ uint32_t scaled_elements(uint32_t w, float f) {
     return elements_of(a.x * f, a.y * f) | elements_of(b.x * f, b.y * f) << 16;
 }
 
-// Two values times f as elements; NaN where they are not finite.
-__device__ __forceinline__ uint32_t nearest_elements(float lo, float hi, float f) {
-    lo = fabsf(lo) < INFINITY ? lo * f : __int_as_float(0x7FC00000);
-    hi = fabsf(hi) < INFINITY ? hi * f : __int_as_float(0x7FC00000);
+// The same where infinities are NaN too.
+__device__ __forceinline__ uint32_t nearest_elements(float lo, float hi) {
+    lo = fabsf(lo) < INFINITY ? lo : __int_as_float(0x7FC00000);
+    hi = fabsf(hi) < INFINITY ? hi : __int_as_float(0x7FC00000);
     return elements_of(lo, hi);
 }
 

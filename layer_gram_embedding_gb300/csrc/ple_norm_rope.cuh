@@ -114,27 +114,32 @@ __device__ __forceinline__ Row pack_row(const Pair (&x)[4]) {
     return Row{make_uint2(w[0], w[1]), make_uint2(w[2], w[3])};
 }
 
-// A row's norm (where `normed`) with weight w, and its rotation by a token's angles.
-// row_s: eight floats a thread, for kPairsAnyHalves.
+// What a row's norm multiplies it with.
+template <int LPR>
+__device__ __forceinline__ float norm_factor(const Pair (&x)[4], float inv_d, float eps) {
+    Pair sq = x[0] * x[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) sq = fma_pair(x[i], x[i], sq);
+    float lo, hi;
+    split(sq, lo, hi);
+    lo += hi;
+#pragma unroll
+    for (int m = LPR / 2; m >= 1; m >>= 1)
+        lo += __shfl_xor_sync(0xffffffffu, lo, m);
+    return rsqrtf(fmaf(lo, inv_d, eps));
+}
+
+__device__ __forceinline__ void scale_row(Pair (&x)[4], const Pair (&w)[4], float inv) {
+    const Pair inv2 = make_pair(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = x[i] * (inv2 * w[i]);
+}
+
+// A row's rotation by a token's angles.  row_s: eight floats a thread, for
+// kPairsAnyHalves.
 template <int LPR, int kLayout>
-__device__ __forceinline__ void turn_row(Pair (&x)[4], const Pair (&w)[4], bool normed,
-                                         float inv_d, float eps, const float4* turn, int sub,
-                                         int pairs, bool turns, float* row_s) {
-    if (normed) {
-        Pair sq = x[0] * x[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i) sq = fma_pair(x[i], x[i], sq);
-        float lo, hi;
-        split(sq, lo, hi);
-        lo += hi;
-#pragma unroll
-        for (int m = LPR / 2; m >= 1; m >>= 1)
-            lo += __shfl_xor_sync(0xffffffffu, lo, m);
-        const float inv = rsqrtf(fmaf(lo, inv_d, eps));
-        const Pair inv2 = make_pair(inv, inv);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = x[i] * (inv2 * w[i]);
-    }
+__device__ __forceinline__ void rotate_row(Pair (&x)[4], const float4* turn, int sub, int pairs,
+                                           bool turns, float* row_s) {
     if constexpr (kLayout == kPairsHalves) {
         if (turns) {
 #pragma unroll
@@ -186,6 +191,15 @@ __device__ __forceinline__ void turn_row(Pair (&x)[4], const Pair (&w)[4], bool 
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = make_pair(z[2 * i], z[2 * i + 1]);
     }
+}
+
+// A row's norm (where `normed`) with weight w, and its rotation.
+template <int LPR, int kLayout>
+__device__ __forceinline__ void turn_row(Pair (&x)[4], const Pair (&w)[4], bool normed,
+                                         float inv_d, float eps, const float4* turn, int sub,
+                                         int pairs, bool turns, float* row_s) {
+    if (normed) scale_row(x, w, norm_factor<LPR>(x, inv_d, eps));
+    rotate_row<LPR, kLayout>(x, turn, sub, pairs, turns, row_s);
 }
 
 // A token's rows come in groups of as many as a warp holds, all of one kind:

@@ -24,6 +24,7 @@ namespace {
 constexpr int kAppendBlocks = 4;    // resident blocks an SM
 constexpr int kHeldRows = 4;        // of a lane, in registers
 constexpr int kAppendTokens = 16;   // most tokens a block of threads looks for blocks among
+constexpr int kMostBlock = 128;     // slots under one scale
 
 struct AppendPlan {
     RowPlan rows;          // the queries'
@@ -32,23 +33,63 @@ struct AppendPlan {
     int32_t shift;         // log2 of a cache block's tokens
 };
 
-// A lane's eight values as elements, four and four.  The reciprocal of a power of two is
-// exact; another scale, which a cache may have been filled with, divides: a quotient
-// beside the border of two elements stays on its side in 32 bits, a product need not.
-__device__ __forceinline__ uint2 row_elements(const Pair (&x)[4], float scale, float inv) {
-    const bool power = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
+// A lane's eight finite values as elements, four and four; inv: the reciprocal of a power
+// of two.
+__device__ __forceinline__ uint2 row_elements(const Pair (&x)[4], float inv) {
+    const Pair up = make_pair(inv, inv);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float lo, hi;
-        split(x[i], lo, hi);
-        // what is not finite is NaN, not the largest element
-        w[i] = power ? nearest_elements(lo, hi, inv)
-                     : nearest_elements(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale), 1.0f);
+        split(x[i] * up, lo, hi);
+        w[i] = elements_of(lo, hi);
     }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
+// Any eight values: what is not finite becomes NaN, and under a scale that is no power of
+// two, as a cache may have been filled with, the product is mended by what it lacks
+// (Markstein 1990): a quotient on the border of two elements has to be met exactly.
+__device__ __forceinline__ uint2 any_row_elements(const Pair (&x)[4], float scale, float inv) {
+    const Pair down = make_pair(-scale, -scale), up = make_pair(inv, inv);
+    const bool power = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        Pair y = x[i] * up;
+        if (!power) y = fma_pair(fma_pair(y, down, x[i]), up, y);
+        float lo, hi, lo_x, hi_x;
+        split(y, lo, hi);
+        split(x[i], lo_x, hi_x);
+        lo = fabsf(lo_x) < INFINITY ? lo : __int_as_float(0x7FC00000);
+        hi = fabsf(hi_x) < INFINITY ? hi : __int_as_float(0x7FC00000);
+        w[i] = elements_of(lo, hi);
+    }
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// The largest amount of a lane's values, NaN passed over.
+__device__ __forceinline__ float amount(const Pair (&x)[4]) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        split(x[i], lo, hi);
+        most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+    }
+    return most;
+}
+
+// The same of values of 16 bits, which without their signs are in the order of their bits,
+// two at a time; a NaN is above infinity.
+__device__ __forceinline__ uint32_t amount_bits(uint32_t most, const Row& row) {
+    most = __vmaxu2(most, row.a.x & 0x7FFF7FFFu);
+    most = __vmaxu2(most, row.a.y & 0x7FFF7FFFu);
+    most = __vmaxu2(most, row.b.x & 0x7FFF7FFFu);
+    return __vmaxu2(most, row.b.y & 0x7FFF7FFFu);
+}
+
+// Of finite values alone.
 __device__ __forceinline__ float finite_amount(const Pair (&x)[4]) {
     float most = 0.f;
 #pragma unroll
@@ -81,6 +122,11 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
     const int second = kLayout == kPairsHalves && turns ? pairs : 4;
     const float inv_d = 1.0f / (float)a.head_dim;
     const int size = 1 << plan.shift;
+    // a thread's tokens and pairs, when it works out angles
+    const int k0 = pairs ? threadIdx.x / pairs : 0, p0 = threadIdx.x - k0 * pairs;
+    const int k_step = pairs ? kNormThreads / pairs : 0, p_step = kNormThreads - k_step * pairs;
+    // the factors of keys' norms, for their second turn
+    __shared__ float factor_s[kWarps][kMostBlock + RPW];
 
     wait_grid_before();
     int64_t t = (int64_t)block_x * plan.kv_tokens;
@@ -113,8 +159,11 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
         }
         const int in_page = (int)(slot - page_at * a.page_size);
         __syncthreads();
-        for (int i = threadIdx.x; i < count * pairs; i += kNormThreads) {
-            const int k = i / pairs, p = i - k * pairs;
+        for (int k = k0, p = p0; pairs != 0 && k < count; k += k_step, p += p_step) {
+            if (p >= pairs) {
+                p -= pairs;
+                if (++k >= count) break;
+            }
             const uint64_t phase = (uint64_t)(int64_t)__ldg(a.positions + t + k) *
                                    (uint64_t)__ldg(reinterpret_cast<const long long*>(a.rope) + p);
             // 2^-32 turns, signed; sincospif takes half turns, and what the float of them
@@ -122,7 +171,7 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
             // elements stay on their side
             const int32_t turns32 = (int32_t)(uint32_t)(phase >> 32);
             const float near = (float)turns32;
-            const float rest = (float)((int64_t)turns32 - (int64_t)near) +
+            const float rest = (float)(turns32 - __float2int_rn(near)) +
                                (float)(uint32_t)phase * 0x1p-32f;
             float sn, cs;
             sincospif(near * 0x1p-31f, &sn, &cs);
@@ -135,23 +184,25 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
             word[2 + (p & 1)] = sn * a.rope_scale;
         }
         __syncthreads();
-        for (int task = block_y * kWarps + warp; task < 2 * a.kv_heads; task += kWarps * grid_y) {
-            const bool is_k = task < a.kv_heads;
-            const int head = is_k ? task : task - a.kv_heads;
+        // One head's keys, or values.
+        auto append = [&](auto keys, int head) {
+            constexpr bool is_k = keys;
+            // values do not turn: a lane's eight elements stand together
+            const int at0 = is_k ? first : sub * 8, at1 = is_k ? second : 4;
             const int64_t step = is_k ? a.k_token : a.v_token;
-            const unsigned short* src =
-                static_cast<const unsigned short*>(is_k ? a.k : a.v) +
-                (t + in_group) * step + head * (is_k ? a.k_head : a.v_head) + first;
+            const unsigned short* src = static_cast<const unsigned short*>(is_k ? a.k : a.v) +
+                                        (t + in_group) * step +
+                                        head * (is_k ? a.k_head : a.v_head) + at0;
             uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) +
                            page * a.page_stride + head * a.head_stride +
-                           (in_page + in_group) * a.slot_stride + first;
+                           (in_page + in_group) * a.slot_stride + at0;
             unsigned short* scale_at =
                 static_cast<unsigned short*>(is_k ? f.scales.k : f.scales.v) +
                 page * f.scales.page_stride + head * f.scales.head_stride +
                 (in_page >> plan.shift);
             const bool normed = is_k && a.k_weight != nullptr;
             Pair w[4];
-            {
+            if constexpr (is_k) {
                 Row row = {};
                 if (normed && live) {
                     const unsigned short* from =
@@ -164,70 +215,130 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
             unsigned short before = 0;
             if (into != 0) before = *scale_at;
             Row held[kHeldRows];
-            auto load = [&](int i0) {
+            auto load = [&](const unsigned short* from, int i0) {
 #pragma unroll
                 for (int i = 0; i < kHeldRows; ++i) {
                     held[i] = Row{};
-                    const int k = i0 + i * RPW;
-                    if (live && k + in_group < count) held[i] = load_row(src + k * step, second);
+                    if (live && i0 + i * RPW + in_group < count) held[i] = load_row(from, at1);
+                    from += RPW * step;
                 }
             };
-            auto turned = [&](int i0, int i, Pair (&x)[4]) {
-                unpack_row<E>(held[i], x);
-                if (is_k)
-                    turn_row<LPR, kLayout>(
-                        x, w, normed, inv_d, a.eps,
-                        angles + min(i0 + i * RPW + in_group, count - 1) * kPitch, sub, pairs,
-                        turns, row_s);
+            auto turned = [&](auto again, const Row& row, int k, Pair (&x)[4]) {
+                unpack_row<E>(row, x);
+                if constexpr (is_k) {
+                    if (normed) {
+                        float* factor = &factor_s[warp][k + in_group];
+                        if constexpr (!again) {
+                            const float now = norm_factor<LPR>(x, inv_d, a.eps);
+                            if (sub == 0) *factor = now;
+                            scale_row(x, w, now);
+                        } else {
+                            scale_row(x, w, *factor);
+                        }
+                    }
+                    rotate_row<LPR, kLayout>(x, angles + min(k + in_group, count - 1) * kPitch, sub,
+                                             pairs, turns, row_s);
+                }
+            };
+            using First = std::false_type;
+            using Again = std::true_type;
+            auto put = [&](uint8_t* to, int k, uint2 e) {
+                if (!live || k + in_group >= count) return;
+                if constexpr (is_k) {
+                    *reinterpret_cast<uint32_t*>(to) = e.x;
+                    *reinterpret_cast<uint32_t*>(to + second) = e.y;
+                } else {
+                    *reinterpret_cast<uint2*>(to) = e;
+                }
             };
             float most = 0.f;
+            uint32_t most_bits = 0;
             for (int i0 = 0; i0 < count; i0 += kHeldRows * RPW) {
-                load(i0);
+                load(src + i0 * step, i0);
 #pragma unroll
                 for (int i = 0; i < kHeldRows; ++i) {
                     if (i0 + i * RPW >= count) break;
-                    Pair x[4];
-                    turned(i0, i, x);
-                    most = fmaxf(most, finite_amount(x));
+                    if constexpr (is_k) {
+                        Pair x[4];
+                        turned(First{}, held[i], i0 + i * RPW, x);
+                        most = fmaxf(most, amount(x));
+                    } else {
+                        most_bits = amount_bits(most_bits, held[i]);
+                    }
                 }
+            }
+            if constexpr (!is_k) {
+                const float2 both = unpack2<E>(most_bits);
+                // of NaN the one that is looked at: it says that there is one
+                most = both.x < INFINITY && both.y < INFINITY ? fmaxf(both.x, both.y) : INFINITY;
             }
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1)
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+            const bool infinite = !(most < INFINITY);
+            __syncwarp();   // factors
+            if (infinite) {
+                most = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < count; k += RPW) {
+                    load(src + k * step, k);
+                    Pair x[4];
+                    turned(Again{}, held[0], k, x);
+                    most = fmaxf(most, finite_amount(x));
+                }
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1)
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+            }
             float scale = __uint_as_float((uint32_t)(127 + exponent_for(most)) << 23);
             if (into != 0) {
                 const float old = scale_value(before);
                 if (scale > old) {
                     // the tokens that the block holds, under the new scale
                     const float shrink = old / scale;
-                    uint8_t* row = dst - (int64_t)into * a.slot_stride - first + sub * 8;
+                    uint8_t* row = dst - (int64_t)into * a.slot_stride - at0 + sub * 8;
+#pragma unroll 1
                     for (int k = 0; k + in_group < into; k += RPW) {
                         if (!live) break;
                         uint2* at = reinterpret_cast<uint2*>(row + k * a.slot_stride);
                         const uint2 v = *at;
-                        *at = make_uint2(scaled_elements(v.x, shrink), scaled_elements(v.y, shrink));
+                        *at = make_uint2(scaled_elements(v.x, shrink),
+                                         scaled_elements(v.y, shrink));
                     }
                 } else {
                     scale = old;
                 }
             }
             const float inv = 1.0f / scale;
-            for (int i0 = 0; i0 < count; i0 += kHeldRows * RPW) {
-                if (count > kHeldRows * RPW) load(i0);
-#pragma unroll
-                for (int i = 0; i < kHeldRows; ++i) {
-                    if (i0 + i * RPW >= count) break;
+            if (infinite || (__float_as_uint(scale) & 0x7FFFFFu) != 0) {
+#pragma unroll 1
+                for (int k = 0; k < count; k += RPW) {
+                    load(src + k * step, k);
                     Pair x[4];
-                    turned(i0, i, x);
-                    const uint2 e = row_elements(x, scale, inv);
-                    const int k = i0 + i * RPW;
-                    if (live && k + in_group < count) {
-                        *reinterpret_cast<uint32_t*>(dst + k * a.slot_stride) = e.x;
-                        *reinterpret_cast<uint32_t*>(dst + k * a.slot_stride + second) = e.y;
+                    turned(Again{}, held[0], k, x);
+                    put(dst + k * a.slot_stride, k, any_row_elements(x, scale, inv));
+                }
+            } else {
+                for (int i0 = 0; i0 < count; i0 += kHeldRows * RPW) {
+                    if (count > kHeldRows * RPW) load(src + i0 * step, i0);
+                    uint8_t* to = dst + i0 * a.slot_stride;
+#pragma unroll
+                    for (int i = 0; i < kHeldRows; ++i) {
+                        if (i0 + i * RPW >= count) break;
+                        Pair x[4];
+                        turned(Again{}, held[i], i0 + i * RPW, x);
+                        put(to, i0 + i * RPW, row_elements(x, inv));
+                        to += RPW * a.slot_stride;
                     }
                 }
             }
             if (lane == 0) *scale_at = (unsigned short)(__float_as_uint(scale) >> 16);
+        };
+        for (int task = block_y * kWarps + warp; task < 2 * a.kv_heads; task += kWarps * grid_y) {
+            if (task < a.kv_heads)
+                append(std::true_type{}, task);
+            else
+                append(std::false_type{}, task - a.kv_heads);
         }
         t += count;
     }

@@ -9,7 +9,11 @@ namespace {
 
 // ------------------------------------------------------------------- commit
 
-constexpr int kCommitThreads = 128;
+// Threads of a block: a warp a head where few blocks run, and their latency is the call's;
+// two warps where they fill the device several times over.  One branch in one layer of 8
+// heads 3.5 us with 256 threads (6.5 with 64); 64 branches in 16 layers 13.2 us with 64
+// (16.2 with 256).
+constexpr int kCommitThreads = 256, kManyCommitThreads = 64;
 constexpr int kMostBlock = 128;    // slots under one scale
 constexpr int kCommitAhead = 4;    // rows of a lane in flight
 
@@ -79,7 +83,7 @@ tree_commit_fp8_kernel(const __grid_constant__ ple_tree_commit_fp8_args f, const
         const int64_t to = place(first, to_scale);
         if (to < 0) continue;
         __syncthreads();
-        for (int i = threadIdx.x; i < live; i += kCommitThreads) {
+        for (int i = threadIdx.x; i < live; i += blockDim.x) {
             const int64_t slot = first + i;
             int64_t from = to + i * a.slot_stride, scale_at = to_scale;
             if (slot >= ctx) {
@@ -97,7 +101,7 @@ tree_commit_fp8_kernel(const __grid_constant__ ple_tree_commit_fp8_args f, const
             scale_s[i] = scale_at;
         }
         __syncthreads();
-        for (int head = warp; head < a.kv_heads; head += kCommitThreads / 32) {
+        for (int head = warp; head < a.kv_heads; head += blockDim.x / 32) {
             const unsigned short* head_scales = scales + head * f.scales.head_stride;
             float most = 0.f;
             for (int i = lane; i < live; i += 32)
@@ -144,20 +148,24 @@ tree_commit_fp8_kernel(const __grid_constant__ ple_tree_commit_fp8_args f, const
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBlocks = 8;
 
-// The workspace: for each page whether it is carried unwritten, the lowest row that
-// writes it, the free pages by rank, and a moving page's rank; for each row the rank
-// of its first new page and of its doubled one; each block's sums.
+// The workspace: for each page a byte whether it is carried unwritten and one whether a
+// row writes it, the lowest row that does, the free pages by rank, and a moving page's
+// rank; for each row the rank of its first new page and of its doubled one; each block's
+// sums.
 struct PlanSpace {
-    int32_t *carried, *writer, *frees, *rank, *first_new, *first_double, *sums;
+    uint8_t *carried, *written;
+    int32_t *writer, *frees, *rank, *first_new, *first_double, *sums;
 };
 
-__host__ __device__ inline int64_t plan_words(int64_t rows, int64_t pages) {
-    return 4 * pages + 2 * rows + kPlanBlocks * 8;
+constexpr int kPlanChunk = 16;   // pages whose bytes a thread reads at once
+
+__host__ __device__ inline int64_t plan_chunks(int64_t pages) {
+    return (pages + kPlanChunk - 1) / kPlanChunk;
 }
 
 __device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // A row of the next tables.
@@ -226,10 +234,24 @@ __device__ __forceinline__ void block_scan(int32_t (&v)[N], int32_t (&all)[N],
     }
 }
 
+// The bytes of a chunk's pages that are not 0, as bits.
+__device__ __forceinline__ uint32_t byte_bits(const uint8_t* bytes, int64_t chunk) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(bytes) + chunk);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // bytes are 0 or 1: they add up in the product's top byte, each at its place
+        bits |= (w[i] * 0x01020408u >> 24 & 0xF) << (4 * i);
+    }
+    return bits;
+}
+
 // One cluster of eight blocks, in phases with a barrier between them: rows mark the
-// pages that they carry; pages and rows are counted, each block its part in order, and
-// ranked; rows and copies are written.  Every result follows from ranks, none from who
-// came first.  A latency: four barriers, and a few dependent reads in each phase.
+// pages that they carry or write, a byte each; bytes are read sixteen at a time, pages and
+// rows counted, each thread its part in order, and ranked; rows and copies are written.
+// Every result follows from ranks, none from who came first.  A latency: four barriers, and
+// a few dependent reads in each phase, eight entries of a row in flight a lane.
 __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads)
 plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
                   const __grid_constant__ PlanSpace space) {
@@ -237,55 +259,74 @@ plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
     const int block = blockIdx.x;
     const int64_t thread = (int64_t)block * kPlanThreads + threadIdx.x;
     constexpr int64_t kAll = (int64_t)kPlanBlocks * kPlanThreads;
-    const int64_t warp = thread >> 5;
+    // a row's warp: rows spread over the blocks
+    const int64_t warp = (int64_t)(threadIdx.x >> 5) * kPlanBlocks + block;
     const int lane = threadIdx.x & 31;
     const int64_t P = a.num_pages, N = a.num_rows;
-    const int64_t copies = N + P - a.page_limit;
+    const int64_t copies = N + P - a.page_limit, chunks = plan_chunks(P);
+    constexpr int kAhead = 8;
 
     wait_grid_before();
-    for (int64_t p = thread; p < P; p += kAll) {
-        space.carried[p] = 0;
-        space.writer[p] = INT32_MAX;
+    // the first row of this warp, and of this thread
+    PlanRow of_warp = {}, of_thread = {};
+    if (warp < N) of_warp = plan_row(a, warp);
+    const int64_t r0 = N * thread / kAll, r1 = N * (thread + 1) / kAll;
+    if (r0 < r1) of_thread = plan_row(a, r0);
+    for (int64_t c = thread; c < chunks; c += kAll) {
+        reinterpret_cast<uint4*>(space.carried)[c] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(space.written)[c] = make_uint4(0, 0, 0, 0);
+    }
+    for (int64_t i = r0; i < r1; ++i) {
+        const PlanRow p = i == r0 ? of_thread : plan_row(a, i);
+        a.next_ctx_lens[i] = p.ctx;
+        if (p.written < 0) continue;
+        const int32_t page = carried_page(a, p, p.written);
+        if (page >= 0) space.writer[page] = INT32_MAX;
     }
     for (int64_t i = thread; i < 2 * copies; i += kAll) a.copies[i] = -1;
     if (thread == 0) a.counts[0] = 0;
     cluster_barrier();
 
     for (int64_t i = warp; i < N; i += kAll / 32) {
-        const PlanRow p = plan_row(a, i);
-        if (lane == 0) a.next_ctx_lens[i] = p.ctx;
-        for (int32_t e = lane; e < p.held; e += 32) {
-            const int32_t page = carried_page(a, p, e);
-            if (page < 0) continue;
-            if (e == p.written)
-                atomicMin(space.writer + page, (int32_t)i);
-            else
-                space.carried[page] = 1;
+        const PlanRow p = i == warp ? of_warp : plan_row(a, i);
+        for (int64_t e0 = lane; e0 < p.held; e0 += 32 * kAhead) {
+            int32_t page[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                page[u] = p.held - e0 > 32 * u ? carried_page(a, p, (int32_t)e0 + 32 * u) : -1;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (page[u] < 0) continue;
+                if (e0 + 32 * u == p.written) {
+                    space.written[page[u]] = 1;
+                    atomicMin(space.writer + page[u], (int32_t)i);
+                } else {
+                    space.carried[page[u]] = 1;
+                }
+            }
         }
     }
     cluster_barrier();
 
-    // this thread's pages and rows, in order
-    auto used = [&](int64_t p) {
-        return __ldcg(space.carried + p) != 0 || __ldcg(space.writer + p) != INT32_MAX;
+    // this thread's pages, in order
+    auto part = [](int64_t n, int64_t k) { return n * k / kAll; };
+    const int64_t c0 = part(chunks, thread), c1 = part(chunks, thread + 1);
+    // of a chunk: pages in use, and those below the limit
+    auto used = [&](int64_t c) {
+        return byte_bits(space.carried, c) | byte_bits(space.written, c);
+    };
+    auto below = [&](int64_t c) {
+        const int64_t n = a.page_limit - c * kPlanChunk;
+        return n <= 0 ? 0u : n >= kPlanChunk ? 0xFFFFu : (1u << (int)n) - 1;
     };
     // whether row i keeps the page that it writes
     auto keeps = [&](int64_t i, int32_t page) {
         return page >= 0 && __ldcg(space.carried + page) == 0 && __ldcg(space.writer + page) == i;
     };
-    auto part = [](int64_t n, int64_t k) { return n * k / kAll; };
-    const int64_t p0 = part(P, thread), p1 = part(P, thread + 1);
-    const int64_t r0 = part(N, thread), r1 = part(N, thread + 1);
     // free pages, pages that move, pages in use; new pages, doubled pages
     int32_t mine[5] = {}, all[5];
-    for (int64_t p = p0; p < p1; ++p) {
-        const bool in_use = used(p);
-        mine[0] += !in_use && p < a.page_limit;
-        mine[1] += in_use && p >= a.page_limit;
-        mine[2] += in_use;
-    }
-    for (int64_t i = r0; i < r1; ++i) {
-        const PlanRow p = plan_row(a, i);
+    auto count_row = [&](int64_t i) {
+        const PlanRow p = i == r0 ? of_thread : plan_row(a, i);
         mine[3] += max(p.need - p.held, 0);
         if (p.written >= 0) {
             const int32_t page = carried_page(a, p, p.written);
@@ -294,7 +335,14 @@ plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
                 mine[4] += page >= 0;
             }
         }
+    };
+    for (int64_t c = c0; c < c1; ++c) {
+        const uint32_t u = used(c), low = below(c);
+        mine[0] += __popc(~u & low);
+        mine[1] += __popc(u & ~low);
+        mine[2] += __popc(u);
     }
+    for (int64_t i = r0; i < r1; ++i) count_row(i);
     block_scan(mine, all, scratch);
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -303,6 +351,7 @@ plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
     cluster_barrier();
 
     int32_t total[5] = {};
+#pragma unroll
     for (int b = 0; b < kPlanBlocks; ++b) {
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
@@ -311,36 +360,28 @@ plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
             total[k] += x;
         }
     }
-    for (int64_t p = p0; p < p1; ++p) {
-        const bool in_use = used(p);
-        if (!in_use && p < a.page_limit) space.frees[mine[0]++] = (int32_t)p;
-        if (in_use && p >= a.page_limit) space.rank[p] = mine[1]++;
+    const int32_t room = total[0], moving = total[1], moved = min(moving, room);
+    const int64_t asked = (int64_t)moving + total[3];
+    for (int64_t c = c0; c < c1; ++c) {
+        const uint32_t u = used(c), low = below(c);
+        for (uint32_t left = ~u & low; left && mine[0] < asked; left &= left - 1)
+            space.frees[mine[0]++] = (int32_t)(c * kPlanChunk) + __ffs((int)left) - 1;
+        for (uint32_t left = u & ~low; left; left &= left - 1, ++mine[1]) {
+            const int32_t page = (int32_t)(c * kPlanChunk) + __ffs((int)left) - 1;
+            space.rank[page] = mine[1];
+            if (mine[1] < room) a.copies[2 * (int64_t)mine[1]] = page;
+        }
     }
     for (int64_t i = r0; i < r1; ++i) {
-        const PlanRow p = plan_row(a, i);
         space.first_new[i] = mine[3];
         space.first_double[i] = mine[4];
-        mine[3] += max(p.need - p.held, 0);
-        if (p.written >= 0) {
-            const int32_t page = carried_page(a, p, p.written);
-            if (!keeps(i, page)) {
-                mine[3] += 1;
-                mine[4] += page >= 0;
-            }
-        }
+        count_row(i);
     }
     cluster_barrier();
 
-    const int32_t room = total[0], moving = total[1], moved = min(moving, room);
-    for (int64_t p = p0; p < p1; ++p) {
-        if (p < a.page_limit || !used(p)) continue;
-        const int32_t k = space.rank[p];
-        if (k >= room) continue;
-        a.copies[2 * (int64_t)k] = (int32_t)p;
-        a.copies[2 * (int64_t)k + 1] = __ldcg(space.frees + k);
-    }
+    for (int64_t k = thread; k < moved; k += kAll) a.copies[2 * k + 1] = __ldcg(space.frees + k);
     for (int64_t i = warp; i < N; i += kAll / 32) {
-        const PlanRow p = plan_row(a, i);
+        const PlanRow p = i == warp ? of_warp : plan_row(a, i);
         const int64_t fresh = (int64_t)moving + __ldcg(space.first_new + i);
         auto new_page = [&](int64_t k) {
             return fresh + k < room ? __ldcg(space.frees + fresh + k) : -1;
@@ -351,22 +392,26 @@ plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
             page = carried_page(a, p, p.written);
             renewed = !keeps(i, page);
         }
-        for (int32_t e = lane; e < a.max_pages; e += 32) {
-            int32_t to = -1;
-            if (e < p.held) {
-                if (e == p.written && renewed) {
-                    to = new_page(0);
-                } else {
-                    to = carried_page(a, p, e);
-                    if (to >= a.page_limit) {
-                        const int32_t k = __ldcg(space.rank + to);
-                        if (k < room) to = __ldcg(space.frees + k);
-                    }
-                }
-            } else if (e < p.need) {
-                to = new_page(e - p.held + renewed);
+        for (int64_t e0 = lane; e0 < a.max_pages; e0 += 32 * kAhead) {
+            int32_t to[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                to[u] = p.held - e0 > 32 * u ? carried_page(a, p, (int32_t)e0 + 32 * u) : -1;
+            int32_t k[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                k[u] = to[u] >= a.page_limit ? __ldcg(space.rank + to[u]) : room;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (a.max_pages - e0 <= 32 * u) break;
+                const int32_t e = (int32_t)e0 + 32 * u;
+                if (k[u] < room) to[u] = __ldcg(space.frees + k[u]);
+                if (e == p.written && renewed)
+                    to[u] = new_page(0);
+                else if (e >= p.held && e < p.need)
+                    to[u] = new_page(e - p.held + renewed);
+                a.next_table[i * a.max_pages + e] = to[u];
             }
-            a.next_table[i * a.max_pages + e] = to;
         }
         if (lane == 0 && renewed && page >= 0 && new_page(0) >= 0) {
             const int64_t k = (int64_t)moved + __ldcg(space.first_double + i);
@@ -376,7 +421,6 @@ plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
         }
     }
     if (thread == 0) {
-        const int64_t asked = (int64_t)moving + total[3];
         const int32_t taken = (int32_t)min(asked, (int64_t)room);
         atomicAdd(a.counts, moved);
         a.counts[1] = total[2] + taken - moved;
@@ -461,21 +505,28 @@ int64_t page_parts(const ple_copy_pages_args& a) {
 
 }  // namespace
 
-cudaError_t launch_tree_commit_fp8(const ple_tree_commit_fp8_args& f, cudaStream_t stream) {
+cudaError_t launch_tree_commit_fp8(const ple_tree_commit_fp8_args& f, const DeviceFacts& dev,
+                                   cudaStream_t stream) {
+    const int64_t blocks = 2 * (int64_t)f.base.num_requests * f.base.num_layers;
+    const int threads = blocks * kCommitThreads <= 2048 * (int64_t)dev.sm_count
+                            ? kCommitThreads
+                            : kManyCommitThreads;
     return launch_kernel(tree_commit_fp8_kernel,
                          dim3((unsigned)f.base.num_requests, (unsigned)f.base.num_layers, 2),
-                         dim3(kCommitThreads), 0, stream, programmatic_launch(), f,
+                         dim3(threads), 0, stream, programmatic_launch(), f,
                          block_shift(f.scales.block));
 }
 
 int64_t plan_pages_workspace(int32_t num_rows, int32_t num_pages) {
-    return 4 * plan_words(num_rows, num_pages);
+    return 2 * kPlanChunk * plan_chunks(num_pages) +
+           4 * (3 * (int64_t)num_pages + 2 * (int64_t)num_rows + kPlanBlocks * 8);
 }
 
 cudaError_t launch_plan_pages(const ple_plan_pages_args& a, cudaStream_t stream) {
     PlanSpace s;
-    s.carried = static_cast<int32_t*>(a.workspace);
-    s.writer = s.carried + a.num_pages;
+    s.carried = static_cast<uint8_t*>(a.workspace);
+    s.written = s.carried + kPlanChunk * plan_chunks(a.num_pages);
+    s.writer = reinterpret_cast<int32_t*>(s.written + kPlanChunk * plan_chunks(a.num_pages));
     s.frees = s.writer + a.num_pages;
     s.rank = s.frees + a.num_pages;
     s.first_new = s.rank + a.num_pages;

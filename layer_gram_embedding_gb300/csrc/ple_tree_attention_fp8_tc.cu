@@ -604,7 +604,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                                 uint32_t e[4];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    e[i] = nearest_elements(q[2 * i], q[2 * i + 1], 1.0f);
+                                    e[i] = nearest_elements(q[2 * i], q[2 * i + 1]);
                                     // what this term leaves
                                     const uint32_t h = halves_of((uint16_t)e[i]);
                                     const float2 left =

@@ -24,7 +24,8 @@ cudaError_t launch_tree_attention_fp8_tc(const ple_tree_attention_fp8_args& a,
                                          const CUtensorMap& k, const CUtensorMap& v,
                                          const DeviceFacts& dev, cudaStream_t stream);
 
-cudaError_t launch_tree_commit_fp8(const ple_tree_commit_fp8_args& a, cudaStream_t stream);
+cudaError_t launch_tree_commit_fp8(const ple_tree_commit_fp8_args& a, const DeviceFacts& dev,
+                                   cudaStream_t stream);
 
 int64_t plan_pages_workspace(int32_t num_rows, int32_t num_pages);
 cudaError_t launch_plan_pages(const ple_plan_pages_args& a, cudaStream_t stream);
