@@ -12,8 +12,15 @@
 // go on with a request's first one): their tokens' sines and cosines are computed once,
 // and a warp takes one head's keys or values of a cache block, rows as in
 // ple_norm_rope.cuh, twice: once for the largest amount and, with the scale known, once
-// for the elements.  The rows stay in registers in between where they are few.  Bound
-// by the rows' bytes.
+// for the elements, the factors of the norms kept in between.  Values' amounts are
+// compared as bits, two at a time.
+//
+// 32003 prompt tokens, 32 and 2 x 8 heads of 128 in blocks of 16: 165 us, 4.4 TB/s of the
+// rows' 721 MB (106 us at the measured copy's rate; the copy of 16-bit rows 146).  Bound by
+// instructions: appended rows alone take 73 us (29 of bytes) at 57% of the issue slots, 110
+// instructions for a warp's two rows.  One decoded token 4.0 us, a launch and a few
+// dependent reads.  Not kept: several warps to a head, so that its rows are read once (alone
+// 97 us against 87: registers run out), and turned keys kept in registers (the same).
 #include "ple_fp8.cuh"
 #include "ple_norm_rope.cuh"
 #include "ple_tree_fp8_internal.h"
@@ -24,7 +31,17 @@ namespace {
 constexpr int kAppendBlocks = 4;    // resident blocks an SM
 constexpr int kHeldRows = 4;        // of a lane, in registers
 constexpr int kAppendTokens = 16;   // most tokens a block of threads looks for blocks among
-constexpr int kMostBlock = 128;     // slots under one scale
+constexpr int kWalkTasks = 32;      // of a warp, between whose two walks others' come
+
+// Tokens whose angles a block of threads holds: all of a cache block's, or, where they would
+// take more than 48 KB, 16 KB of them (kWalk).  The 32003-token prompts, all at once and in
+// walks: heads of 256 in blocks of 128 tokens (128 KB) 834 and 396 us, in blocks of 64
+// (64 KB) 484 and 346; of 128 in blocks of 128 (64 KB) 247 and 191, in blocks of 64 (32 KB)
+// 165 and 191.
+constexpr int kMostBlock = 128;
+constexpr int kMostTable = 48 * 1024;
+template <int LPR, bool kWalk>
+constexpr int kTableTokens = kWalk ? 512 / LPR : kMostBlock;
 
 struct AppendPlan {
     RowPlan rows;          // the queries'
@@ -103,7 +120,7 @@ __device__ __forceinline__ float finite_amount(const Pair (&x)[4]) {
     return most;
 }
 
-template <typename E, int LPR, int kLayout>
+template <typename E, int LPR, int kLayout, bool kWalk>
 __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f,
                                               const AppendPlan& plan, int block_x, int block_y,
                                               int grid_y) {
@@ -126,7 +143,11 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
     const int k0 = pairs ? threadIdx.x / pairs : 0, p0 = threadIdx.x - k0 * pairs;
     const int k_step = pairs ? kNormThreads / pairs : 0, p_step = kNormThreads - k_step * pairs;
     // the factors of keys' norms, for their second turn
-    __shared__ float factor_s[kWarps][kMostBlock + RPW];
+    __shared__ float factor_s[kWarps][kTableTokens<LPR, kWalk> + RPW];
+    // what is known of a warp's heads between two walks over a block's rows: the largest
+    // amount, then the scale; whether a value is infinite
+    __shared__ float known_s[kWarps][kWalk ? kWalkTasks : 1];
+    __shared__ bool infinite_s[kWarps][kWalk ? kWalkTasks : 1];
 
     wait_grid_before();
     int64_t t = (int64_t)block_x * plan.kv_tokens;
@@ -158,34 +179,40 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
             continue;
         }
         const int in_page = (int)(slot - page_at * a.page_size);
-        __syncthreads();
-        for (int k = k0, p = p0; pairs != 0 && k < count; k += k_step, p += p_step) {
-            if (p >= pairs) {
-                p -= pairs;
-                if (++k >= count) break;
+        // the angles of rows c0 .. c1 - 1
+        auto work_out_angles = [&](int c0, int c1) {
+            if (pairs == 0) return;
+            __syncthreads();
+            for (int k = k0, p = p0; k < c1 - c0; k += k_step, p += p_step) {
+                if (p >= pairs) {
+                    p -= pairs;
+                    if (++k >= c1 - c0) break;
+                }
+                const uint64_t phase = (uint64_t)(int64_t)__ldg(a.positions + t + c0 + k) *
+                                       (uint64_t)__ldg(reinterpret_cast<const long long*>(a.rope) + p);
+                // 2^-32 turns, signed; sincospif takes half turns, and what the float of them
+                // lacks comes in by the first order: keys near the border between two
+                // elements stay on their side
+                const int32_t turns32 = (int32_t)(uint32_t)(phase >> 32);
+                const float near = (float)turns32;
+                const float rest = (float)(turns32 - __float2int_rn(near)) +
+                                   (float)(uint32_t)phase * 0x1p-32f;
+                float sn, cs;
+                sincospif(near * 0x1p-31f, &sn, &cs);
+                const float off = rest * (0x1p-31f * 3.14159265358979f);
+                const float sn0 = sn;
+                sn = fmaf(cs, off, sn);
+                cs = fmaf(-sn0, off, cs);
+                float* word = reinterpret_cast<float*>(&angles[k * kPitch + (p >> 1)]);
+                word[p & 1] = cs * a.rope_scale;
+                word[2 + (p & 1)] = sn * a.rope_scale;
             }
-            const uint64_t phase = (uint64_t)(int64_t)__ldg(a.positions + t + k) *
-                                   (uint64_t)__ldg(reinterpret_cast<const long long*>(a.rope) + p);
-            // 2^-32 turns, signed; sincospif takes half turns, and what the float of them
-            // lacks comes in by the first order: keys near the border between two
-            // elements stay on their side
-            const int32_t turns32 = (int32_t)(uint32_t)(phase >> 32);
-            const float near = (float)turns32;
-            const float rest = (float)(turns32 - __float2int_rn(near)) +
-                               (float)(uint32_t)phase * 0x1p-32f;
-            float sn, cs;
-            sincospif(near * 0x1p-31f, &sn, &cs);
-            const float off = rest * (0x1p-31f * 3.14159265358979f);
-            const float sn0 = sn;
-            sn = fmaf(cs, off, sn);
-            cs = fmaf(-sn0, off, cs);
-            float* word = reinterpret_cast<float*>(&angles[k * kPitch + (p >> 1)]);
-            word[p & 1] = cs * a.rope_scale;
-            word[2 + (p & 1)] = sn * a.rope_scale;
-        }
-        __syncthreads();
-        // One head's keys, or values.
-        auto append = [&](auto keys, int head) {
+            __syncthreads();
+        };
+        // One head's keys, or values, rows c0 .. c1 - 1: their largest amount is looked for, the
+        // block's scale settled, elements stored; number: of the warp's tasks.
+        auto append = [&](auto keys, int head, int number, int c0, int c1, bool look, bool settle,
+                          bool store) {
             constexpr bool is_k = keys;
             // values do not turn: a lane's eight elements stand together
             const int at0 = is_k ? first : sub * 8, at1 = is_k ? second : 4;
@@ -213,37 +240,37 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
                 unpack_row<E>(row, w);
             }
             unsigned short before = 0;
-            if (into != 0) before = *scale_at;
+            if (settle && into != 0) before = *scale_at;
             Row held[kHeldRows];
             auto load = [&](const unsigned short* from, int i0) {
 #pragma unroll
                 for (int i = 0; i < kHeldRows; ++i) {
                     held[i] = Row{};
-                    if (live && i0 + i * RPW + in_group < count) held[i] = load_row(from, at1);
+                    if (live && i0 + i * RPW + in_group < c1) held[i] = load_row(from, at1);
                     from += RPW * step;
                 }
             };
-            auto turned = [&](auto again, const Row& row, int k, Pair (&x)[4]) {
+            auto turned = [&](bool again, const Row& row, int k, Pair (&x)[4]) {
                 unpack_row<E>(row, x);
                 if constexpr (is_k) {
                     if (normed) {
-                        float* factor = &factor_s[warp][k + in_group];
-                        if constexpr (!again) {
-                            const float now = norm_factor<LPR>(x, inv_d, a.eps);
-                            if (sub == 0) *factor = now;
-                            scale_row(x, w, now);
+                        float* kept = &factor_s[warp][k - c0 + in_group];
+                        float factor;
+                        if (again) {
+                            factor = *kept;
                         } else {
-                            scale_row(x, w, *factor);
+                            factor = norm_factor<LPR>(x, inv_d, a.eps);
+                            if (sub == 0) *kept = factor;
                         }
+                        scale_row(x, w, factor);
                     }
-                    rotate_row<LPR, kLayout>(x, angles + min(k + in_group, count - 1) * kPitch, sub,
-                                             pairs, turns, row_s);
+                    rotate_row<LPR, kLayout>(
+                        x, angles + min(k - c0 + in_group, c1 - c0 - 1) * kPitch, sub, pairs, turns,
+                        row_s);
                 }
             };
-            using First = std::false_type;
-            using Again = std::true_type;
             auto put = [&](uint8_t* to, int k, uint2 e) {
-                if (!live || k + in_group >= count) return;
+                if (!live || k + in_group >= c1) return;
                 if constexpr (is_k) {
                     *reinterpret_cast<uint32_t*>(to) = e.x;
                     *reinterpret_cast<uint32_t*>(to + second) = e.y;
@@ -252,105 +279,156 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
                 }
             };
             float most = 0.f;
-            uint32_t most_bits = 0;
-            for (int i0 = 0; i0 < count; i0 += kHeldRows * RPW) {
-                load(src + i0 * step, i0);
+            bool infinite = false;
+            if (look) {
+                uint32_t most_bits = 0;
+                for (int i0 = c0; i0 < c1; i0 += kHeldRows * RPW) {
+                    load(src + i0 * step, i0);
 #pragma unroll
-                for (int i = 0; i < kHeldRows; ++i) {
-                    if (i0 + i * RPW >= count) break;
-                    if constexpr (is_k) {
-                        Pair x[4];
-                        turned(First{}, held[i], i0 + i * RPW, x);
-                        most = fmaxf(most, amount(x));
-                    } else {
-                        most_bits = amount_bits(most_bits, held[i]);
+                    for (int i = 0; i < kHeldRows; ++i) {
+                        if (i0 + i * RPW >= c1) break;
+                        if constexpr (is_k) {
+                            Pair x[4];
+                            turned(false, held[i], i0 + i * RPW, x);
+                            most = fmaxf(most, amount(x));
+                        } else {
+                            most_bits = amount_bits(most_bits, held[i]);
+                        }
                     }
                 }
-            }
-            if constexpr (!is_k) {
-                const float2 both = unpack2<E>(most_bits);
-                // of NaN the one that is looked at: it says that there is one
-                most = both.x < INFINITY && both.y < INFINITY ? fmaxf(both.x, both.y) : INFINITY;
-            }
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1)
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-            const bool infinite = !(most < INFINITY);
-            __syncwarp();   // factors
-            if (infinite) {
-                most = 0.f;
-#pragma unroll 1
-                for (int k = 0; k < count; k += RPW) {
-                    load(src + k * step, k);
-                    Pair x[4];
-                    turned(Again{}, held[0], k, x);
-                    most = fmaxf(most, finite_amount(x));
+                if constexpr (!is_k) {
+                    const float2 both = unpack2<E>(most_bits);
+                    // a NaN is looked at too: it says that there is one
+                    most = both.x < INFINITY && both.y < INFINITY ? fmaxf(both.x, both.y)
+                                                                  : INFINITY;
                 }
 #pragma unroll
                 for (int d = 16; d >= 1; d >>= 1)
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-            }
-            float scale = __uint_as_float((uint32_t)(127 + exponent_for(most)) << 23);
-            if (into != 0) {
-                const float old = scale_value(before);
-                if (scale > old) {
-                    // the tokens that the block holds, under the new scale
-                    const float shrink = old / scale;
-                    uint8_t* row = dst - (int64_t)into * a.slot_stride - at0 + sub * 8;
+                __syncwarp();   // factors
+                infinite = !(most < INFINITY);
+                if (infinite) {
+                    most = 0.f;
 #pragma unroll 1
-                    for (int k = 0; k + in_group < into; k += RPW) {
-                        if (!live) break;
-                        uint2* at = reinterpret_cast<uint2*>(row + k * a.slot_stride);
-                        const uint2 v = *at;
-                        *at = make_uint2(scaled_elements(v.x, shrink),
-                                         scaled_elements(v.y, shrink));
+                    for (int k = c0; k < c1; k += RPW) {
+                        load(src + k * step, k);
+                        Pair x[4];
+                        turned(true, held[0], k, x);
+                        most = fmaxf(most, finite_amount(x));
                     }
-                } else {
-                    scale = old;
+#pragma unroll
+                    for (int d = 16; d >= 1; d >>= 1)
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
                 }
+                if (c0 != 0) {
+                    most = fmaxf(most, known_s[warp][number]);
+                    infinite = infinite || infinite_s[warp][number];
+                }
+            } else {
+                most = known_s[warp][number];
+                infinite = infinite_s[warp][number];
             }
+            float scale = most;
+            if (settle) {
+                scale = __uint_as_float((uint32_t)(127 + exponent_for(most)) << 23);
+                if (into != 0) {
+                    const float old = scale_value(before);
+                    if (scale > old) {
+                        // the tokens that the block holds, under the new scale
+                        const float shrink = old / scale;
+                        uint8_t* row = dst - (int64_t)into * a.slot_stride - at0 + sub * 8;
+#pragma unroll 1
+                        for (int k = 0; k + in_group < into; k += RPW) {
+                            if (!live) break;
+                            uint2* at = reinterpret_cast<uint2*>(row + k * a.slot_stride);
+                            const uint2 v = *at;
+                            *at = make_uint2(scaled_elements(v.x, shrink),
+                                             scaled_elements(v.y, shrink));
+                        }
+                    } else {
+                        scale = old;
+                    }
+                }
+                if (lane == 0) *scale_at = (unsigned short)(__float_as_uint(scale) >> 16);
+            }
+            if (!(look && store)) {
+                __syncwarp();
+                if (lane == 0) {
+                    known_s[warp][number] = scale;
+                    infinite_s[warp][number] = infinite;
+                }
+                __syncwarp();
+            }
+            if (!store) return;
             const float inv = 1.0f / scale;
             if (infinite || (__float_as_uint(scale) & 0x7FFFFFu) != 0) {
 #pragma unroll 1
-                for (int k = 0; k < count; k += RPW) {
+                for (int k = c0; k < c1; k += RPW) {
                     load(src + k * step, k);
                     Pair x[4];
-                    turned(Again{}, held[0], k, x);
+                    turned(look, held[0], k, x);
                     put(dst + k * a.slot_stride, k, any_row_elements(x, scale, inv));
                 }
             } else {
-                for (int i0 = 0; i0 < count; i0 += kHeldRows * RPW) {
-                    if (count > kHeldRows * RPW) load(src + i0 * step, i0);
+                for (int i0 = c0; i0 < c1; i0 += kHeldRows * RPW) {
+                    if (!look || c1 > kHeldRows * RPW) load(src + i0 * step, i0);
                     uint8_t* to = dst + i0 * a.slot_stride;
 #pragma unroll
                     for (int i = 0; i < kHeldRows; ++i) {
-                        if (i0 + i * RPW >= count) break;
+                        if (i0 + i * RPW >= c1) break;
                         Pair x[4];
-                        turned(Again{}, held[i], i0 + i * RPW, x);
+                        turned(look, held[i], i0 + i * RPW, x);
                         put(to, i0 + i * RPW, row_elements(x, inv));
                         to += RPW * a.slot_stride;
                     }
                 }
             }
-            if (lane == 0) *scale_at = (unsigned short)(__float_as_uint(scale) >> 16);
         };
-        for (int task = block_y * kWarps + warp; task < 2 * a.kv_heads; task += kWarps * grid_y) {
+        const int task = block_y * kWarps + warp, task_step = kWarps * grid_y;
+        auto append_task = [&](int task, int number, int c0, int c1, bool look, bool settle,
+                               bool store) {
             if (task < a.kv_heads)
-                append(std::true_type{}, task);
+                append(std::true_type{}, task, number, c0, c1, look, settle, store);
             else
-                append(std::false_type{}, task - a.kv_heads);
+                append(std::false_type{}, task - a.kv_heads, number, c0, c1, look, settle, store);
+        };
+        if constexpr (!kWalk) {
+            // a warp looks at a head's rows and stores them at once
+            work_out_angles(0, count);
+            for (int i = task; i < 2 * a.kv_heads; i += task_step)
+                append_task(i, 0, 0, count, true, true, true);
+        } else {
+            // all of a warp's heads, some at a time, walk over the rows twice, a table after
+            // the other
+            constexpr int kTable = kTableTokens<LPR, kWalk>;
+            const int all = (2 * a.kv_heads - block_y * kWarps + task_step - 1) / task_step;
+            for (int task0 = 0; task0 < all; task0 += kWalkTasks) {
+                const int tasks = min(all - task0, kWalkTasks);
+                for (int walk = 0; walk < 2; ++walk) {
+                    for (int c0 = 0; c0 < count; c0 += kTable) {
+                        const int c1 = min(c0 + kTable, count);
+                        work_out_angles(c0, c1);
+                        for (int number = 0; number < tasks; ++number) {
+                            const int i = task + (task0 + number) * task_step;
+                            if (i >= 2 * a.kv_heads) break;
+                            append_task(i, number, c0, c1, walk == 0, walk == 1 && c0 == 0,
+                                        walk == 1);
+                        }
+                    }
+                }
+            }
         }
         t += count;
     }
 }
 
-template <typename E, int LPR, int kLayout>
+template <typename E, int LPR, int kLayout, bool kWalk>
 __global__ void __launch_bounds__(kNormThreads, kAppendBlocks)
 qk_norm_rope_fp8_kernel(const __grid_constant__ ple_qk_norm_rope_fp8_args f,
                         const __grid_constant__ ple_qk_norm_rope_args queries,
                         const __grid_constant__ AppendPlan plan) {
     if ((int)blockIdx.x < plan.kv_blocks)
-        append_blocks<E, LPR, kLayout>(f, plan, blockIdx.x, blockIdx.y, gridDim.y);
+        append_blocks<E, LPR, kLayout, kWalk>(f, plan, blockIdx.x, blockIdx.y, gridDim.y);
     else
         norm_rope_rows<E, LPR, kLayout>(queries, plan.rows, blockIdx.x - plan.kv_blocks,
                                         blockIdx.y, gridDim.y);
@@ -382,11 +460,23 @@ cudaError_t launch_rows(const ple_qk_norm_rope_fp8_args& f, const DeviceFacts& d
     const int groups = plan.rows.q_groups > 2 * a.kv_heads ? plan.rows.q_groups : 2 * a.kv_heads;
     const int64_t most = (groups + kWarps - 1) / kWarps;
     split = split < 1 ? 1 : split > most ? most : split;
-    auto* fn = a.rotary_dim && a.interleaved
-                   ? qk_norm_rope_fp8_kernel<E, LPR, kPairsInterleaved>
-               : a.rotary_dim % 8 == 0 ? qk_norm_rope_fp8_kernel<E, LPR, kPairsHalves>
-                                       : qk_norm_rope_fp8_kernel<E, LPR, kPairsAnyHalves>;
-    const int smem = a.rotary_dim ? f.scales.block * 2 * LPR * 16 : 0;
+    const int table = f.scales.block * 2 * LPR * 16;
+    const bool walk = LPR > 8 && a.rotary_dim && table > kMostTable;
+    auto pick = [&](auto walks) {
+        constexpr bool kWalk = walks;
+        return a.rotary_dim && a.interleaved
+                   ? qk_norm_rope_fp8_kernel<E, LPR, kPairsInterleaved, kWalk>
+               : a.rotary_dim % 8 == 0 ? qk_norm_rope_fp8_kernel<E, LPR, kPairsHalves, kWalk>
+                                       : qk_norm_rope_fp8_kernel<E, LPR, kPairsAnyHalves, kWalk>;
+    };
+    auto* fn = pick(std::false_type{});
+    int smem = a.rotary_dim ? table : 0;
+    if constexpr (LPR > 8) {
+        if (walk) {
+            fn = pick(std::true_type{});
+            smem = kTableTokens<LPR, true> * 2 * LPR * 16;
+        }
+    }
     if (smem > 16384) {
         const cudaError_t e =
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
