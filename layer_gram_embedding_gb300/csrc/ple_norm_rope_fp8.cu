@@ -189,7 +189,8 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
                     if (++k >= c1 - c0) break;
                 }
                 const uint64_t phase = (uint64_t)(int64_t)__ldg(a.positions + t + c0 + k) *
-                                       (uint64_t)__ldg(reinterpret_cast<const long long*>(a.rope) + p);
+                                       (uint64_t)__ldg(
+                                           reinterpret_cast<const long long*>(a.rope) + p);
                 // 2^-32 turns, signed; sincospif takes half turns, and what the float of them
                 // lacks comes in by the first order: keys near the border between two
                 // elements stay on their side

