@@ -12,6 +12,7 @@ namespace {
 
 // The least scale that the library writes: 2^kLeastExponent.
 constexpr int kLeastExponent = -100;
+constexpr int kMostBlock = 128;    // slots under one scale
 
 // Two elements, the lower byte first, as halves; every element is a half exactly.
 __device__ __forceinline__ uint32_t halves_of(uint16_t two) {

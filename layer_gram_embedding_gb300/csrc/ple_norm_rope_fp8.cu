@@ -38,7 +38,6 @@ constexpr int kWalkTasks = 32;      // of a warp, between whose two walks others
 // walks: heads of 256 in blocks of 128 tokens (128 KB) 834 and 396 us, in blocks of 64
 // (64 KB) 484 and 346; of 128 in blocks of 128 (64 KB) 247 and 191, in blocks of 64 (32 KB)
 // 165 and 191.
-constexpr int kMostBlock = 128;
 constexpr int kMostTable = 48 * 1024;
 template <int LPR, bool kWalk>
 constexpr int kTableTokens = kWalk ? 512 / LPR : kMostBlock;

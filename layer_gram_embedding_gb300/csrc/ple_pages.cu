@@ -14,7 +14,6 @@ namespace {
 // heads 3.5 us with 256 threads (6.5 with 64); 64 branches in 16 layers 13.2 us with 64
 // (16.2 with 256).
 constexpr int kCommitThreads = 256, kManyCommitThreads = 64;
-constexpr int kMostBlock = 128;    // slots under one scale
 constexpr int kCommitAhead = 4;    // rows of a lane in flight
 
 // The accepted rows of one request, one layer and one cache move to the front of the
@@ -164,6 +163,7 @@ __host__ __device__ inline int64_t plan_chunks(int64_t pages) {
 }
 
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
