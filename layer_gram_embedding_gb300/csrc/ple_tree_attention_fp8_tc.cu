@@ -39,6 +39,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "ple_fp8.cuh"
 #include "ple_tc.cuh"
 #include "ple_tree_fp8_internal.h"
@@ -62,7 +64,7 @@ constexpr float kMostSum = 0x1p60f;
 
 // kPairs: units of up to 256 rows (heads of up to 128 elements), 128 for each group; else
 // of up to 128, and the groups take the tiles in turn.
-template <int D, bool kBf16, bool kPairs>
+template <int D, bool kBf16, bool kPairs, int kCopies>
 struct Shape {
     static constexpr int kParts = D > 128 ? 2 : 1;       // of a head
     static constexpr int kWidth = D / kParts;            // elements a part
@@ -70,7 +72,9 @@ struct Shape {
     static constexpr int kBytes = kTile * kWidth;        // of a part's tile of elements
     static constexpr int kTileBytes = 2 * kBytes;        // and of halves
     static constexpr int kHalfBytes = kTile * 128;       // a swizzled block of 64 halves a row
-    static constexpr int kQueryBytes = (kPairs ? 2 : 1) * kTerms * kBytes;
+    static constexpr int kTermBytes = (kPairs ? 2 : 1) * kTerms * kBytes;
+    // (at least what 32 columns of all copies take when they meet)
+    static constexpr int kQueryBytes = kCopies > 1 && kTermBytes < 32768 ? 32768 : kTermBytes;
     // rings of values as halves, those at work and the next ones, and of keys and values as
     // they come, with what is left (an SM's share of the measured bandwidth is 45 GB/s,
     // and a loaded memory answers in 2 us)
@@ -107,6 +111,34 @@ __device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
                  : "memory");
 }
 
+// The weights of 32 columns, two blocks: exp2(f x + at), as halves, and their share of the
+// row's sum.
+__device__ __forceinline__ void weigh(const uint32_t (&x)[32], float f_low, float f_high,
+                                      float at_low, float at_high, float base, float& sum,
+                                      uint32_t (&p)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float f = h ? f_high : f_low, at = h ? at_high : at_low;
+        const uint64_t f2 = pack_f32(f, f), at2 = pack_f32(at, at);
+        uint64_t part[2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t pair =
+                pack_f32(as_float(x[16 * h + 2 * i]), as_float(x[16 * h + 2 * i + 1]));
+            float x0, x1;
+            unpack_f32(fma_f32x2(pair, f2, at2), x0, x1);
+            x0 = exp2_fast(x0);
+            x1 = exp2_fast(x1);
+            const uint64_t e2 = pack_f32(x0, x1);
+            part[i & 1] = i < 2 ? e2 : add_f32x2(part[i & 1], e2);
+            p[8 * h + i] = round_pair<false>(x0, x1);
+        }
+        float p0, p1;
+        unpack_f32(add_f32x2(part[0], part[1]), p0, p1);
+        sum = fmaf(p0 + p1, exp2_fast(-(at + base)), sum);
+    }
+}
+
 // A place in a ring, and how often it was filled before.
 template <int kPlaces>
 struct Turn {
@@ -120,13 +152,13 @@ struct Turn {
     }
 };
 
-template <int D, bool kBf16, bool kPairs>
+template <int D, bool kBf16, bool kPairs, int kCopies>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                              const __grid_constant__ Scales sc,
                              const __grid_constant__ CUtensorMap k_map,
                              const __grid_constant__ CUtensorMap v_map) {
-    using S = Shape<D, kBf16, kPairs>;
+    using S = Shape<D, kBf16, kPairs, kCopies>;
     const ple_tree_attention_args& a = args.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t key_full[S::kKeys], key_empty[S::kKeys];
@@ -146,7 +178,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
     // whether drafted values of a segment hold NaN, as each converting warp found; that
     // warpgroup is at most three segments ahead
     __shared__ int bad_s[4][4];
-    __shared__ float join_s[kTile][2];
+    __shared__ float join_s[kCopies > 1 ? 2 * kTile : kTile][2];
     __shared__ int8_t shift_s[2][kTile];   // of a group's rows
     __shared__ Segment seg_s[2];
     __shared__ int more_s[2];
@@ -530,11 +562,18 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             const int first_row = s.unit * args.unit_rows + row0;
             const int rows = s.pair && !kSplit ? (w == 0 ? kTile : s.rows - kTile) : s.rows;
             const int column0 = kSplit ? w * S::kWidth : 0;       // of the group's accumulators
-            const bool active = (warp & 3) * 32 < rows;   // a warp with no row only keeps step
-            const bool here = row < rows;
-            const int node = (first_row + row) / group;
+            // Few rows stand in the group's tile two or four times, and each copy takes its
+            // part of a tile's columns, a row of its own as far as the softmax goes: the lanes
+            // of a warp hold 32 rows, and no other warp can read their scores
+            constexpr int span = kTile / kCopies;
+            const int own = row % span, copy = row / span;     // the row, and which copy of it
+            constexpr int quarters = 4 / kCopies;              // of the columns
+            const int quarter0 = copy * quarters;
+            const bool active = (own & ~31) < rows;   // a warp with no row only keeps step
+            const bool here = own < rows;
+            const int node = (first_row + own) / group;
             const int64_t token = s.q.begin + node;
-            const int64_t head = (int64_t)s.head * group + (first_row + row) - node * group;
+            const int64_t head = (int64_t)s.head * group + (first_row + own) - node * group;
             const unsigned long long* mask =
                 reinterpret_cast<const unsigned long long*>(a.tree_mask) +
                 (here ? token : 0) * a.mask_words;
@@ -622,8 +661,13 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                                     q[2 * i] -= left.x;
                                     q[2 * i + 1] -= left.y;
                                 }
-                                *reinterpret_cast<uint2*>(to + term * S::kBytes) =
+                                const uint2 two =
                                     make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+                                *reinterpret_cast<uint2*>(to + term * S::kBytes) = two;
+#pragma unroll
+                                for (int i = 1; i < kCopies; ++i)
+                                    *reinterpret_cast<uint2*>(to + term * S::kBytes +
+                                                              i * span * S::kWidth) = two;
                             }
                         }
                     }
@@ -653,12 +697,12 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                         c = args.c *
                             __uint_as_float(
                                 (uint32_t)(127 + *static_cast<volatile int8_t*>(
-                                                     &shift_s[s.pair ? w : 0][row])) << 23);
+                                                     &shift_s[s.pair ? w : 0][own])) << 23);
                     // Scores of what is not seen become -infinity in tensor memory, in a walk
                     // of their own: few tiles have any, and the loops below stay short
                     if (masked) {
 #pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = quarter0; q < quarter0 + quarters; ++q) {
                             const uint32_t bits =
                                 here ? seen_bits(window, a.mask_words, ctx, length,
                                                  first + 32 * q)
@@ -683,6 +727,31 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                     float factor[8], place[8];
                     uint32_t v[2][32];
                     float now = top, reach = -INFINITY;
+                    if constexpr (kCopies > 1) {
+                        // the copy's columns alone, 32 or 64
+                        float m[4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (k < quarters) {
+                                const uint32_t at = s_at + 32 * (quarter0 + k);
+                                tmem_load_max16(at, v[k], 0, m[2 * k]);
+                                tmem_load_max16(at + 16, v[k], 16, m[2 * k + 1]);
+                                const float4 two = scales[quarter0 + k];
+                                factor[2 * k] = fmaxf(c * two.x, 1.17549435e-38f);
+                                place[2 * k] = two.y;
+                                factor[2 * k + 1] = fmaxf(c * two.z, 1.17549435e-38f);
+                                place[2 * k + 1] = two.w;
+                                tmem_wait_load(v[k]);
+                                asm volatile("" : "+f"(m[2 * k]), "+f"(m[2 * k + 1]));
+#pragma unroll
+                                for (int b = 2 * k; b < 2 * k + 2; ++b) {
+                                    const float x = m[b] * factor[b];
+                                    now = fmaxf(now, x);
+                                    reach = fmaxf(reach, x + place[b]);
+                                }
+                            }
+                        }
+                    } else {
 #pragma unroll
                     for (int h = 1; h >= 0; --h) {
                         float m[4];
@@ -708,6 +777,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                             now = fmaxf(now, x);
                             reach = fmaxf(reach, x + place[4 * h + b]);
                         }
+                    }
                     }
                     const float base = now == -INFINITY ? 0.f : now;
                     sum *= exp2_fast(top - base);
@@ -744,35 +814,38 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                     // of what the reference stands for counts as that: its weights, which
                     // the sum needs, would be lost, and its values are nothing to the row.
                     const float to_ref = ref == -INFINITY ? 0.f : kBias - ref, least = -100.f - base;
+                    if constexpr (kCopies > 1) {
+                        // no weights for the other copies' columns
+                        const uint32_t none[16] = {};
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q)
+                            if (q / quarters != copy) tmem_store(s_at + 16 * q, none);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (k < quarters) {
+                                uint32_t p[16];
+                                weigh(v[k], factor[2 * k], factor[2 * k + 1],
+                                      fmaxf(place[2 * k] + to_ref, least),
+                                      fmaxf(place[2 * k + 1] + to_ref, least), base, sum, p);
+                                tmem_store(s_at + 16 * (quarter0 + k), p);
+                            }
+                        }
+                        tmem_wait_store();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&p_low[w]);
+                            mbar_arrive(&p_high[w]);
+                        }
+                    } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t(&x)[32] = v[q & 1];
+                        uint32_t (&x)[32] = v[q & 1];
                         if (q > 1) tmem_wait_load(x);
                         uint32_t p[16];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int b = 2 * q + h;
-                            const float f = factor[b];
-                            const float at = fmaxf(place[b] + to_ref, least);
-                            const uint64_t f2 = pack_f32(f, f), at2 = pack_f32(at, at);
-                            uint64_t part[2];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint64_t pair =
-                                    pack_f32(as_float(x[16 * h + 2 * i]),
-                                             as_float(x[16 * h + 2 * i + 1]));
-                                float x0, x1;
-                                unpack_f32(fma_f32x2(pair, f2, at2), x0, x1);
-                                x0 = exp2_fast(x0);
-                                x1 = exp2_fast(x1);
-                                const uint64_t e2 = pack_f32(x0, x1);
-                                part[i & 1] = i < 2 ? e2 : add_f32x2(part[i & 1], e2);
-                                p[8 * h + i] = round_pair<false>(x0, x1);
-                            }
-                            float p0, p1;
-                            unpack_f32(add_f32x2(part[0], part[1]), p0, p1);
-                            sum = fmaf(p0 + p1, exp2_fast(-(at + base)), sum);
-                        }
+                        weigh(x, factor[2 * q], factor[2 * q + 1],
+                              fmaxf(place[2 * q] + to_ref, least),
+                              fmaxf(place[2 * q + 1] + to_ref, least), base, sum, p);
                         if (q < 2) tmem_load(s_at + 32 * (q + 2), x);
                         // over columns whose scores have been read
                         tmem_store(s_at + 16 * q, p);
@@ -782,6 +855,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                             __syncwarp();
                             if (lane == 0) mbar_arrive(q == 1 ? &p_low[w] : &p_high[w]);
                         }
+                    }
                     }
                 } else {
                     tmem_fence_before();
@@ -801,7 +875,9 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             // ------------------------------------ the segment's rows go out
             // Where both groups hold states of the same rows, group 1's go to group 0
             // through the queries' memory, half the columns at a time.
-            const bool join = !s.pair && n > 1;
+            // Copies of rows all meet there, 32 columns at a time.
+            constexpr bool meet = kCopies > 1;
+            const bool join = !meet && !s.pair && n > 1;
             float4* exchange = reinterpret_cast<float4*>(q_tiles);
             constexpr int kChunks = S::kWidth / 64;   // of 32 columns, in a half
             auto hand_over = [&](int part) {
@@ -833,8 +909,71 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 hand_over(0);
             }
+            // a row's states lie `span` threads apart
+            constexpr int states = 2 * kCopies;
+            float meet_f = 0.f;
+            if constexpr (meet) {
+                mbar_wait(&q_empty, seg & 1, failed);
+                const int me = w * kTile + row;
+                join_s[me][0] = top;
+                join_s[me][1] = sum;
+                named_barrier<256>(1);
+                for (int i = 0; i < states; ++i) top = fmaxf(top, join_s[i * span + own][0]);
+                const float base = top == -INFINITY ? 0.f : top;
+                sum = 0.f;
+                for (int i = 0; i < states; ++i)
+                    sum = fmaf(join_s[i * span + own][1],
+                               exp2_fast(join_s[i * span + own][0] - base), sum);
+                meet_f = ref == -INFINITY ? 0.f : exp2_fast(fminf(ref - kBias - top, 126.f));
+            }
+            // the accumulators of all states of a row, 32 columns, to its first one's thread
+            auto meet_columns = [&](int q, float (&x)[32]) {
+                const int me = w * kTile + row;
+                if (begun) {
+                    uint32_t o[32];
+                    tmem_load(o_at + 32 * q, o);
+                    tmem_wait_load(o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        exchange[i * 2 * kTile + me] = make_float4(
+                            __uint_as_float(o[4 * i]) * meet_f,
+                            __uint_as_float(o[4 * i + 1]) * meet_f,
+                            __uint_as_float(o[4 * i + 2]) * meet_f,
+                            __uint_as_float(o[4 * i + 3]) * meet_f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        exchange[i * 2 * kTile + me] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                named_barrier<256>(1);
+                for (int i = me / span; i < 8; i += states) {
+                    float4* at = exchange + i * 2 * kTile + own;
+                    float4 y = at[0];
+                    for (int k = 1; k < states; ++k) {
+                        const float4 z = at[k * span];
+                        y.x += z.x;
+                        y.y += z.y;
+                        y.z += z.z;
+                        y.w += z.w;
+                    }
+                    at[0] = y;
+                }
+                named_barrier<256>(1);
+                if (me < span) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 y = exchange[i * 2 * kTile + own];
+                        x[4 * i] = y.x;
+                        x[4 * i + 1] = y.y;
+                        x[4 * i + 2] = y.z;
+                        x[4 * i + 3] = y.w;
+                    }
+                }
+                named_barrier<256>(1);
+            };
             {
-                const bool out = s.pair || w == 0;   // whether these rows are this group's
+                // whether these rows are this group's
+                const bool out = s.pair || (w == 0 && copy == 0);
                 // accumulators relative to the row's top
                 float f1 = 0.f;
                 if (join && w == 0 && here) {
@@ -865,7 +1004,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                 const int64_t o_row = token * a.q_heads + head;
                 float* state = static_cast<float*>(a.workspace) +
                                state_at(blockIdx.x, s.k0 == 0 ? 1 : 0, args.rows_cap, D);
-                const int state_row = row0 + row;
+                const int state_row = row0 + own;
                 float* pairs = state + 2 * state_row;
                 float* acc = state + (2 + column0) * args.rows_cap + 8 * state_row;
                 const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
@@ -875,18 +1014,23 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                         named_barrier<256>(1);
                         hand_over(1);
                     }
-                    if (!out || !active) continue;
+                    if (!meet && (!out || !active)) continue;
 #pragma unroll 1
                     for (int q = part * kChunks; q < (part + 1) * kChunks; ++q) {
                         const int column = column0 + 32 * q;
-                        uint32_t o[32];
-                        if (begun) {
-                            tmem_load(o_at + 32 * q, o);
-                            tmem_wait_load(o);
-                        }
                         float x[32];
+                        if constexpr (meet) {
+                            meet_columns(q, x);
+                            if (!out || !active) continue;
+                        } else {
+                            uint32_t o[32];
+                            if (begun) {
+                                tmem_load(o_at + 32 * q, o);
+                                tmem_wait_load(o);
+                            }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * f0;
+                            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * f0;
+                        }
                         if (kSplit && spoiled) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) x[i] = __int_as_float(0x7FC00000);
@@ -968,11 +1112,11 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
     if (warp == kIssueWarp) tmem_free(tmem, 512);
 }
 
-template <int D, bool kBf16, bool kPairs>
+template <int D, bool kBf16, bool kPairs, int kCopies>
 cudaError_t launch_tc(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
                       const CUtensorMap& v, cudaStream_t stream) {
-    using S = Shape<D, kBf16, kPairs>;
-    auto* fn = tree_attention_fp8_tc_kernel<D, kBf16, kPairs>;
+    using S = Shape<D, kBf16, kPairs, kCopies>;
+    auto* fn = tree_attention_fp8_tc_kernel<D, kBf16, kPairs, kCopies>;
     cudaError_t e =
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
@@ -988,16 +1132,18 @@ cudaError_t launch_tc(const TcArgs& args, const Scales& sc, const CUtensorMap& k
 template <bool kBf16>
 cudaError_t launch_dtype(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
                          const CUtensorMap& v, cudaStream_t stream) {
-    const bool pairs = args.unit_rows > kTile;
+    auto width = [&](auto d) {
+        constexpr int D = d;
+        return args.unit_rows > kTile        ? launch_tc<D, kBf16, true, 1>(args, sc, k, v, stream)
+               : args.unit_rows == kTile     ? launch_tc<D, kBf16, false, 1>(args, sc, k, v, stream)
+               : args.unit_rows == kTile / 2 ? launch_tc<D, kBf16, false, 2>(args, sc, k, v, stream)
+                                             : launch_tc<D, kBf16, false, 4>(args, sc, k, v, stream);
+    };
     switch (padded_width(args.a.head_dim)) {
-        case 64:
-            return pairs ? launch_tc<64, kBf16, true>(args, sc, k, v, stream)
-                         : launch_tc<64, kBf16, false>(args, sc, k, v, stream);
-        case 128:
-            return pairs ? launch_tc<128, kBf16, true>(args, sc, k, v, stream)
-                         : launch_tc<128, kBf16, false>(args, sc, k, v, stream);
-        default:  // both parts' queries, as of two groups
-            return launch_tc<256, kBf16, true>(args, sc, k, v, stream);
+        case 64: return width(std::integral_constant<int, 64>{});
+        case 128: return width(std::integral_constant<int, 128>{});
+        // both parts' queries, as of two groups
+        default: return launch_tc<256, kBf16, true, 1>(args, sc, k, v, stream);
     }
 }
 
@@ -1019,7 +1165,12 @@ cudaError_t launch_tree_attention_fp8_tc(const ple_tree_attention_fp8_args& f,
     args.rows_cap = tc_rows_cap(a.num_tokens, a.q_heads, a.kv_heads, a.head_dim);
     // units of two groups' rows where a request's are so many on the average
     args.unit_rows = unit_rows(padded_width(a.head_dim));
-    if (a.num_tokens * args.group <= kTile * (int64_t)a.num_requests) args.unit_rows = kTile;
+    const int64_t rows = a.num_tokens * args.group, B = a.num_requests;
+    if (rows <= kTile * B) args.unit_rows = kTile;
+    if (padded_width(a.head_dim) <= 128) {
+        if (rows <= kTile / 2 * B) args.unit_rows = kTile / 2;
+        if (rows <= kTile / 4 * B) args.unit_rows = kTile / 4;
+    }
     if (args.rows_cap > args.unit_rows) args.rows_cap = args.unit_rows;
     args.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
     args.flip = a.scale < 0 ? 0x80008000u : 0u;
