@@ -721,8 +721,8 @@ ple_status ple_qk_norm_rope_fp8(const ple_qk_norm_rope_fp8_args* args, void* str
  * Arguments and results as there, base.dtype that of q and out, and
  * max_pages * page_size <= INT32_MAX - 128.  Queries enter the products as halves
  * (float16 exactly, bfloat16 to 2^-40 of the row's largest element) or, where requests
- * have more than 16 rows a key head on the average, as sums of elements (what lies below
- * 2^-17 of the row's largest is lost); elements enter exactly; scales, scores, the
+ * have more than 8 rows a key head on the average, as sums of elements (what lies below
+ * 2^-17 of the row's largest may be lost); elements enter exactly; scales, scores, the
  * softmax's maximum and sum and the output are held in 32 bits.  A weight times its
  * value's scale enters the product with the elements to 2^-11 of itself, or to 2^-27 of
  * the largest such among the 128 slots around it, however far below the row's largest

@@ -769,7 +769,8 @@ cudaError_t launch_rows(const TcArgs& args, const Scales& sc, const CUtensorMap&
 template <int W, bool kBf16>
 cudaError_t launch_width(const TcArgs& args, const Scales& sc, const CUtensorMap& k,
                          const CUtensorMap& v, cudaStream_t stream) {
-    if (args.unit_rows <= 8) return launch_rows<W, 1, W == 256 ? 1 : 2, kBf16>(args, sc, k, v, stream);
+    if (args.unit_rows <= 8)
+        return launch_rows<W, 1, W == 256 ? 1 : 2, kBf16>(args, sc, k, v, stream);
     return launch_rows<W, 2, 1, kBf16>(args, sc, k, v, stream);
 }
 
@@ -783,11 +784,17 @@ cudaError_t launch_dtype(const TcArgs& args, const Scales& sc, const CUtensorMap
     }
 }
 
-// Whether a call's key heads have so many rows that the tensor cores' kernel takes it.  16
-// rows over 64 x 512 slots take 41 us here and 59 there; 32 rows over 32 x 16384, as four
-// products a slice, 489 here and 239 there.
-bool many_rows(const ple_tree_attention_args& a) {
-    return a.num_tokens * (a.q_heads / a.kv_heads) > 16 * (int64_t)a.num_requests;
+// Whether a call's key heads have so many rows that the tensor cores' kernel takes it.  32
+// rows over 32 x 16384 slots, as four products a slice, take 489 us here and 214 there.
+// With 9 to 16 rows a slot costs less there and a unit more: 32 x 16384 slots 226 and 207
+// us, 32 of 100 to 9000 100 and 84, 64 x 512 41 and 53 (heads of 256, 32 x 8192: 238 and
+// 285), so it takes them where the page tables have room for some 100 tiles a block.
+bool many_rows(const ple_tree_attention_args& a, const DeviceFacts& dev) {
+    const int64_t rows = a.num_tokens * (a.q_heads / a.kv_heads), B = a.num_requests;
+    if (rows > 16 * B) return true;
+    const int64_t tiles = ((int64_t)a.max_pages * a.page_size + kTile - 1) / kTile;
+    return rows > 8 * B && a.head_dim <= 128 &&
+           B * a.kv_heads * tiles >= 96 * (int64_t)tc_blocks(dev);
 }
 
 }  // namespace
@@ -804,7 +811,7 @@ cudaError_t launch_tree_attention_fp8(const ple_tree_attention_fp8_args& f,
     CUtensorMap k, v;
     if (!encode_cache(&k, a, a.k_cache) || !encode_cache(&v, a, a.v_cache))
         return cudaErrorInvalidValue;
-    if (many_rows(a)) return launch_tree_attention_fp8_tc(f, k, v, dev, stream);
+    if (many_rows(a, dev)) return launch_tree_attention_fp8_tc(f, k, v, dev, stream);
     TcArgs args;
     args.a = a;
     args.blocks = tc_blocks(dev);

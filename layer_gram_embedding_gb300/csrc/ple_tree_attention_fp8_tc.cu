@@ -23,15 +23,25 @@
 // tiles of keys, of values (tiled bulk copies, page by page), to issue the matrix
 // instructions and to walk the segments ahead.  Registers are dealt out anew among them.
 //
+// Copies.  The lanes of a warp hold 32 rows' scores and no other warp can read them, so
+// with 32 rows one warp of four would do all exponentials.  Up to 64 rows stand two times
+// in their tile, up to 32 four times, and each copy takes its part of a tile's columns (the
+// others' weights are zeros), a row of its own until the copies meet at the segment's end.
+// 8 nodes of 4 heads over 32 x 16384 slots: 241 us without, 214 with four copies; 16 nodes
+// 261 and 238 with two; heads of 64, 8 nodes, 210 and 169.  Units of 64 rows where requests
+// have more on the average read keys twice: 32 ragged requests of 66 on the average 360 us
+// instead of 288.
+//
 // Measured (bf16, heads of 128, 32 query and 8 key heads, 64-slot pages, the join with
-// it; in brackets the cache in 16 bits).  32 requests over 16384 slots: 8 nodes 239 us
-// (324), 32 nodes 289 (337), 64 nodes 496 (421); 64 nodes of 64 heads over 130981 slots,
-// float16, 269 (221); 32 ragged requests of 17 to 32749 slots 288 (343).  160 us are the
-// bytes.  Above, the chain of a group does: some 1900 clocks of softmax for 128 rows of 128
-// keys, and 1400 from the weights to the next scores.  With 256 rows a tile's products
-// read more shared memory than those of the cache in 16 bits (each term of a query once,
-// 3 x 128 x 128 bytes more in float16), the turned values are written and read once more,
-// and that is what the halved bytes cost.
+// it; in brackets the cache in 16 bits).  32 requests over 16384 slots: 4 nodes 207 us, 8
+// nodes 214 (324), 32 nodes 289 (337), 64 nodes 495 (421); 64 nodes of 64 heads over
+// 130981 slots, float16, 270 (221); 32 ragged requests of 17 to 32749 slots 288 (343).
+// 160 us are the bytes.  A tile is some 2000 clocks at few rows, where shared memory alone
+// is read and written for 1400; with 128 rows the chain of a group: some 1900 clocks of
+// softmax for 128 rows of 128 keys, and 1400 from the weights to the next scores.  With
+// 256 rows a tile's products read more shared memory than those of the cache in 16 bits
+// (the queries' terms), and the turned values are written and read once more: that is what
+// the halved bytes cost.
 //
 // What is not seen: as in ple_tree_attention_tc.cu.  Values past the request's tokens and
 // elements of drafted nodes that are NaN are cleared as they are converted; rows that
@@ -63,7 +73,7 @@ constexpr float kRise = 5.0f, kFall = 7.0f, kBias = 9.0f;
 constexpr float kMostSum = 0x1p60f;
 
 // kPairs: units of up to 256 rows (heads of up to 128 elements), 128 for each group; else
-// of up to 128, and the groups take the tiles in turn.
+// of up to 128 / kCopies, and the groups take the tiles in turn.
 template <int D, bool kBf16, bool kPairs, int kCopies>
 struct Shape {
     static constexpr int kParts = D > 128 ? 2 : 1;       // of a head
@@ -421,8 +431,8 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                                      smem_addr(places) + at * S::kBytes +
                                          lane * box * S::kWidth,
                                      &filled[at], part * S::kWidth,
-                                     sc.in_page((s.k0 + j) * kTile + lane * box, a.page_size), s.head,
-                                     page);
+                                     sc.in_page((s.k0 + j) * kTile + lane * box, a.page_size),
+                                     s.head, page);
                         if (++at == most) {
                             at = 0;
                             ++round;
@@ -562,9 +572,6 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
             const int first_row = s.unit * args.unit_rows + row0;
             const int rows = s.pair && !kSplit ? (w == 0 ? kTile : s.rows - kTile) : s.rows;
             const int column0 = kSplit ? w * S::kWidth : 0;       // of the group's accumulators
-            // Few rows stand in the group's tile two or four times, and each copy takes its
-            // part of a tile's columns, a row of its own as far as the softmax goes: the lanes
-            // of a warp hold 32 rows, and no other warp can read their scores
             constexpr int span = kTile / kCopies;
             const int own = row % span, copy = row / span;     // the row, and which copy of it
             constexpr int quarters = 4 / kCopies;              // of the columns
@@ -753,31 +760,31 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                     } else {
 #pragma unroll
-                    for (int h = 1; h >= 0; --h) {
-                        float m[4];
-                        tmem_load_max16(s_at + 64 * h, v[0], 0, m[0]);
-                        tmem_load_max16(s_at + 64 * h + 16, v[0], 16, m[1]);
-                        tmem_load_max16(s_at + 64 * h + 32, v[1], 0, m[2]);
-                        tmem_load_max16(s_at + 64 * h + 48, v[1], 16, m[3]);
+                        for (int h = 1; h >= 0; --h) {
+                            float m[4];
+                            tmem_load_max16(s_at + 64 * h, v[0], 0, m[0]);
+                            tmem_load_max16(s_at + 64 * h + 16, v[0], 16, m[1]);
+                            tmem_load_max16(s_at + 64 * h + 32, v[1], 0, m[2]);
+                            tmem_load_max16(s_at + 64 * h + 48, v[1], 16, m[3]);
 #pragma unroll
-                        for (int b = 4 * h; b < 4 * h + 4; b += 2) {
-                            const float4 two = scales[b / 2];
-                            factor[b] = fmaxf(c * two.x, 1.17549435e-38f);
-                            place[b] = two.y;
-                            factor[b + 1] = fmaxf(c * two.z, 1.17549435e-38f);
-                            place[b + 1] = two.w;
-                        }
-                        tmem_wait_load(v[0]);
-                        tmem_settle(v[0], m[0]);
-                        tmem_settle(v[1], m[1]);
-                        asm volatile("" : "+f"(m[2]), "+f"(m[3]));
+                            for (int b = 4 * h; b < 4 * h + 4; b += 2) {
+                                const float4 two = scales[b / 2];
+                                factor[b] = fmaxf(c * two.x, 1.17549435e-38f);
+                                place[b] = two.y;
+                                factor[b + 1] = fmaxf(c * two.z, 1.17549435e-38f);
+                                place[b + 1] = two.w;
+                            }
+                            tmem_wait_load(v[0]);
+                            tmem_settle(v[0], m[0]);
+                            tmem_settle(v[1], m[1]);
+                            asm volatile("" : "+f"(m[2]), "+f"(m[3]));
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const float x = m[b] * factor[4 * h + b];
-                            now = fmaxf(now, x);
-                            reach = fmaxf(reach, x + place[4 * h + b]);
+                            for (int b = 0; b < 4; ++b) {
+                                const float x = m[b] * factor[4 * h + b];
+                                now = fmaxf(now, x);
+                                reach = fmaxf(reach, x + place[4 * h + b]);
+                            }
                         }
-                    }
                     }
                     const float base = now == -INFINITY ? 0.f : now;
                     sum *= exp2_fast(top - base);
@@ -813,7 +820,8 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                     // sum takes a block's together, that scale out again.  A scale 2^-100
                     // of what the reference stands for counts as that: its weights, which
                     // the sum needs, would be lost, and its values are nothing to the row.
-                    const float to_ref = ref == -INFINITY ? 0.f : kBias - ref, least = -100.f - base;
+                    const float to_ref = ref == -INFINITY ? 0.f : kBias - ref;
+                    const float least = -100.f - base;
                     if constexpr (kCopies > 1) {
                         // no weights for the other copies' columns
                         const uint32_t none[16] = {};
@@ -839,23 +847,23 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                         }
                     } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t (&x)[32] = v[q & 1];
-                        if (q > 1) tmem_wait_load(x);
-                        uint32_t p[16];
-                        weigh(x, factor[2 * q], factor[2 * q + 1],
-                              fmaxf(place[2 * q] + to_ref, least),
-                              fmaxf(place[2 * q + 1] + to_ref, least), base, sum, p);
-                        if (q < 2) tmem_load(s_at + 32 * (q + 2), x);
-                        // over columns whose scores have been read
-                        tmem_store(s_at + 16 * q, p);
-                        if (q & 1) {
-                            tmem_wait_store();
-                            tmem_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(q == 1 ? &p_low[w] : &p_high[w]);
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t (&x)[32] = v[q & 1];
+                            if (q > 1) tmem_wait_load(x);
+                            uint32_t p[16];
+                            weigh(x, factor[2 * q], factor[2 * q + 1],
+                                  fmaxf(place[2 * q] + to_ref, least),
+                                  fmaxf(place[2 * q + 1] + to_ref, least), base, sum, p);
+                            if (q < 2) tmem_load(s_at + 32 * (q + 2), x);
+                            // over columns whose scores have been read
+                            tmem_store(s_at + 16 * q, p);
+                            if (q & 1) {
+                                tmem_wait_store();
+                                tmem_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(q == 1 ? &p_low[w] : &p_high[w]);
+                            }
                         }
-                    }
                     }
                 } else {
                     tmem_fence_before();
@@ -1134,10 +1142,11 @@ cudaError_t launch_dtype(const TcArgs& args, const Scales& sc, const CUtensorMap
                          const CUtensorMap& v, cudaStream_t stream) {
     auto width = [&](auto d) {
         constexpr int D = d;
-        return args.unit_rows > kTile        ? launch_tc<D, kBf16, true, 1>(args, sc, k, v, stream)
-               : args.unit_rows == kTile     ? launch_tc<D, kBf16, false, 1>(args, sc, k, v, stream)
-               : args.unit_rows == kTile / 2 ? launch_tc<D, kBf16, false, 2>(args, sc, k, v, stream)
-                                             : launch_tc<D, kBf16, false, 4>(args, sc, k, v, stream);
+        auto* launch = args.unit_rows > kTile        ? launch_tc<D, kBf16, true, 1>
+                       : args.unit_rows == kTile     ? launch_tc<D, kBf16, false, 1>
+                       : args.unit_rows == kTile / 2 ? launch_tc<D, kBf16, false, 2>
+                                                     : launch_tc<D, kBf16, false, 4>;
+        return launch(args, sc, k, v, stream);
     };
     switch (padded_width(args.a.head_dim)) {
         case 64: return width(std::integral_constant<int, 64>{});
@@ -1167,6 +1176,8 @@ cudaError_t launch_tree_attention_fp8_tc(const ple_tree_attention_fp8_args& f,
     args.unit_rows = unit_rows(padded_width(a.head_dim));
     const int64_t rows = a.num_tokens * args.group, B = a.num_requests;
     if (rows <= kTile * B) args.unit_rows = kTile;
+    // (a prompt of 512 nodes among 64 decodes over 8192 slots each, whose keys small units
+    // read four times as often, takes 369 us instead of 360; 65 nodes among 32, 139 for 152)
     if (padded_width(a.head_dim) <= 128) {
         if (rows <= kTile / 2 * B) args.unit_rows = kTile / 2;
         if (rows <= kTile / 4 * B) args.unit_rows = kTile / 4;

@@ -127,6 +127,19 @@ def test_append_whose_angles_come_in_parts(page, block, D, Hk):
                  np.zeros(v.shape), cache.table, ctx, cu, exact=True)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("counts", [[5, 4, 3, 4], [8, 0, 7, 1], [1, 30, 0, 0], [2, 2, 3, 3]])
+def test_page_tables_with_room_for_long_contexts(D, counts):
+    # the kernel is chosen by rows a key head and the tables' width: 8 to 32 rows in wide ones
+    rng = np.random.default_rng(103)
+    q, cache, ctx, cu, masks = attention_inputs(rng, counts, [700, 3, 129, 64], 16, 4, D, 128, 32,
+                                                torch.bfloat16)
+    narrow = check_attention(q, cache, ctx, cu, masks)
+    cache.table = np.concatenate([cache.table, np.full((4, 2000), -1, np.int32)], 1)
+    wide = check_attention(q, cache, ctx, cu, masks)
+    assert narrow[0].shape == wide[0].shape
+
+
 def test_one_tensor_for_keys_and_values():
     # attention reads them alone: they may be one
     rng = np.random.default_rng(97)
