@@ -15,7 +15,7 @@
 // for the elements, the factors of the norms kept in between.  Values' amounts are
 // compared as bits, two at a time.
 //
-// 32003 prompt tokens, 32 and 2 x 8 heads of 128 in blocks of 16: 165 us, 4.4 TB/s of the
+// 32003 prompt tokens, 32 and 2 x 8 heads of 128 in blocks of 16: 166 us, 4.3 TB/s of the
 // rows' 721 MB (106 us at the measured copy's rate; the copy of 16-bit rows 146).  Bound by
 // instructions: appended rows alone take 73 us (29 of bytes) at 57% of the issue slots, 110
 // instructions for a warp's two rows.  One decoded token 4.0 us, a launch and a few
@@ -48,6 +48,33 @@ struct AppendPlan {
     int32_t kv_tokens;     // each one's tokens
     int32_t shift;         // log2 of a cache block's tokens
 };
+
+// Sine and cosine of a phase in 2^-64 turns, rounded about once: keys near the border
+// between two elements stay on their side.  The angle from the nearest quarter turn, at
+// most pi / 4, is p + e in two floats; Taylor's series give what is added to p and to 1.
+__device__ __forceinline__ void sine_cosine(uint64_t phase, float& sn, float& cs) {
+    constexpr float kPi = 3.14159274f, kPiRest = -8.74227766e-8f;   // their sum is pi
+    const uint32_t turn = (uint32_t)(phase >> 32);                  // 2^-32 turns
+    const uint32_t quarter = (turn + (1u << 29)) >> 30;
+    const int32_t rest = (int32_t)(turn - (quarter << 30));
+    const float near = (float)rest;                                 // below 2^30: converts back
+    const float y = near * 0x1p-31f;                                // half turns
+    const float y_rest = ((float)(rest - (int32_t)near) + (float)(uint32_t)phase * 0x1p-32f) *
+                         0x1p-31f;
+    const float p = y * kPi;
+    const float e = fmaf(y_rest, kPi, fmaf(y, kPiRest, fmaf(y, kPi, -p)));
+    const float z = p * p, z_rest = fmaf(p, p, -z);
+    const float odd = fmaf(fmaf(fmaf(1.f / 362880, z, -1.f / 5040), z, 1.f / 120), z, -1.f / 6);
+    const float even = fmaf(fmaf(fmaf(-1.f / 3628800, z, 1.f / 40320), z, -1.f / 720), z, 1.f / 24);
+    const float sine = p + fmaf(p * z, odd, fmaf(-0.5f * z, e, e));
+    const float one = fmaf(-0.5f, z, 1.f);
+    const float lost = fmaf(-0.5f, z, 1.f - one);
+    const float cosine = one + (lost + fmaf(z * z, even, fmaf(-0.5f, z_rest, -p * e)));
+    sn = quarter & 1 ? cosine : sine;
+    cs = quarter & 1 ? sine : cosine;
+    if (quarter & 2) sn = -sn;
+    if ((quarter + 1) & 2) cs = -cs;
+}
 
 // A lane's eight finite values as elements, four and four; inv: the reciprocal of a power
 // of two.
@@ -190,19 +217,8 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
                 const uint64_t phase = (uint64_t)(int64_t)__ldg(a.positions + t + c0 + k) *
                                        (uint64_t)__ldg(
                                            reinterpret_cast<const long long*>(a.rope) + p);
-                // 2^-32 turns, signed; sincospif takes half turns, and what the float of them
-                // lacks comes in by the first order: keys near the border between two
-                // elements stay on their side
-                const int32_t turns32 = (int32_t)(uint32_t)(phase >> 32);
-                const float near = (float)turns32;
-                const float rest = (float)(turns32 - __float2int_rn(near)) +
-                                   (float)(uint32_t)phase * 0x1p-32f;
                 float sn, cs;
-                sincospif(near * 0x1p-31f, &sn, &cs);
-                const float off = rest * (0x1p-31f * 3.14159265358979f);
-                const float sn0 = sn;
-                sn = fmaf(cs, off, sn);
-                cs = fmaf(-sn0, off, cs);
+                sine_cosine(phase, sn, cs);
                 float* word = reinterpret_cast<float*>(&angles[k * kPitch + (p >> 1)]);
                 word[p & 1] = cs * a.rope_scale;
                 word[2 + (p & 1)] = sn * a.rope_scale;
