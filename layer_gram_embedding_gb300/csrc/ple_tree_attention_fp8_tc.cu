@@ -67,6 +67,7 @@ constexpr int kSoftmaxRegisters = 176, kOneTaskRegisters = 64, kTurnRegisters = 
 static_assert(2 * kSoftmaxRegisters + kOneTaskRegisters + kTurnRegisters == 4 * 128, "");
 
 constexpr int kScaleTiles = 16;
+constexpr int kBadSegments = 8;
 
 // As in ple_tree_attention_fp8.cu.
 constexpr float kRise = 5.0f, kFall = 7.0f, kBias = 9.0f;
@@ -185,9 +186,12 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
     __shared__ Share share_s;
     __shared__ uint32_t tmem_s;
     __shared__ int failed_s;
-    // whether drafted values of a segment hold NaN, as each converting warp found; that
-    // warpgroup is at most three segments ahead
-    __shared__ int bad_s[4][4];
+    // Whether drafted values of a segment hold NaN, as each converting warp found.  A segment's
+    // flags are read while its rows go out: until then no place of the next ones' values is given
+    // back, so that warpgroup has converted kSlots segments of one tile at most behind it, and
+    // cleared the flags of one more.
+    __shared__ int bad_s[kBadSegments][4];
+    static_assert(S::kSlots + 2 <= kBadSegments, "");
     __shared__ float join_s[kCopies > 1 ? 2 * kTile : kTile][2];
     __shared__ int8_t shift_s[2][kTile];   // of a group's rows
     __shared__ Segment seg_s[2];
@@ -265,7 +269,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
         const uint32_t stages_at = smem_addr(stages), ring_at = smem_addr(ring);
         bool ended = false;
         while (!ended && walk.next(args, s)) {
-            if (lane == 0) bad_s[seg & 3][mine] = 0;
+            if (lane == 0) bad_s[seg % kBadSegments][mine] = 0;
             __syncwarp();
             for (int i = 0; i < (s.k1 - s.k0) * S::kParts; ++i) {
                 if (!mbar_wait(&stage_full[stage.at], stage.round & 1, failed) ||
@@ -302,7 +306,8 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                             }
                         }
                     }
-                    if (__any_sync(0xffffffffu, bad) && lane == 0) bad_s[seg & 3][mine] = 1;
+                    if (__any_sync(0xffffffffu, bad) && lane == 0)
+                        bad_s[seg % kBadSegments][mine] = 1;
                     __syncwarp();
                 }
 #pragma unroll
@@ -1007,7 +1012,7 @@ tree_attention_fp8_tc_kernel(const __grid_constant__ TcArgs args,
                 }
                 const bool spoiled = *failed;
                 if (spoiled) sum = __int_as_float(0x7FC00000);  // NaN, not an unfinished sum
-                const volatile int* found = bad_s[seg & 3];
+                const volatile int* found = bad_s[seg % kBadSegments];
                 const bool bad = found[0] | found[1] | found[2] | found[3];
                 const int64_t o_row = token * a.q_heads + head;
                 float* state = static_cast<float*>(a.workspace) +

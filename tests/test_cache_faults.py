@@ -1,0 +1,47 @@
+"""Faults that the operators on caches in 8 bits and on pages once had, on the GPU: a
+test for each, against plain 64-bit host implementations (cache_reference.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import layer_gram_embedding_gb300 as ple
+from test_cache_ops import attention_inputs, check_attention, dev
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+DEV = torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("D,nodes,longest,dtype", [
+    # rows a key head on the average: up to 32, 64, 128 and more
+    (64, (5, 7), 60, torch.bfloat16), (64, (9, 15), 60, torch.float16),
+    (64, (17, 31), 60, torch.bfloat16), (64, (33, 60), 60, torch.float16),
+    (32, (5, 40), 60, torch.float16), (48, (5, 7), 60, torch.bfloat16),
+    (64, (5, 7), 300, torch.float16), (64, (17, 60), 300, torch.bfloat16),
+    (128, (5, 7), 60, torch.float16), (128, (17, 31), 60, torch.bfloat16),
+    (256, (9, 15), 60, torch.bfloat16),
+])
+def test_nan_in_one_segment_of_many(D, nodes, longest, dtype):
+    # Units of one tile (and some of a few), several in a row in every block: what was found in a
+    # unit's drafted values stays known until its rows go out.  A NaN changes nothing but its own
+    # column of the rows that see it.
+    rng = np.random.default_rng(D + nodes[1] + longest)
+    B, Hk, group = 160, 8, 4
+    counts = [int(x) for x in rng.integers(nodes[0], nodes[1] + 1, B)]
+    ctx = [int(x) for x in rng.integers(0, longest, B)]
+    q, cache, ctx, cu, masks = attention_inputs(rng, counts, ctx, group * Hk, Hk, D, 32, 16, dtype)
+    out, lse = check_attention(q, cache, ctx, cu, masks)
+    want = out.clone()
+    for r in range(0, B, 3):
+        node, h, d = (int(rng.integers(n)) for n in (counts[r], Hk, D))
+        p, s = cache.where(r, int(ctx[r]) + node)
+        cache.v[0, p, h, s, d] = rng.choice([0x7F, 0xFF])
+        sees = dev(masks[cu[r]:cu[r + 1], 0] >> node & 1 != 0)
+        want[cu[r]:cu[r + 1], h * group:(h + 1) * group, d][sees] = float("nan")
+    assert bool(want.isnan().any())
+    got, got_lse = ple.ple_tree_attention_fp8(q, *cache.device(), dev(cache.table), dev(ctx),
+                                              dev(cu), dev(masks), return_lse=True)
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0)) and torch.equal(got_lse, lse)
