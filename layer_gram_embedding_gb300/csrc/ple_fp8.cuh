@@ -44,6 +44,26 @@ __device__ __forceinline__ uint32_t scaled_elements(uint32_t w, float f) {
     return elements_of(a.x * f, a.y * f) | elements_of(b.x * f, b.y * f) << 16;
 }
 
+// Four elements kept under a scale that is `f + rest` of the new one, f of 20 significant bits
+// and rest >= 0 (a zero keeps its sign): e * f is exact, so that a quotient on the border of two
+// elements, which one factor of 24 bits may miss, is met there.  Any other is 2^-13 of itself
+// away from it.
+__device__ __forceinline__ uint32_t scaled_elements(uint32_t w, float f, float rest) {
+    uint32_t low, high;
+    halves_of(w, low, high);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&low));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&high));
+    return elements_of(fmaf(a.x, rest, a.x * f), fmaf(a.y, rest, a.y * f)) |
+           elements_of(fmaf(b.x, rest, b.x * f), fmaf(b.y, rest, b.y * f)) << 16;
+}
+
+// What takes a scale to [1, 2), the least ones, which are no normal numbers, to below that: so
+// quotients of scales, and what is left of them, stay inside 32 bits.
+__device__ __forceinline__ float scale_to_one(float scale) {
+    const uint32_t e = __float_as_uint(scale) >> 23;
+    return e < 254 ? __uint_as_float((254 - e) << 23) : 0x1p-127f;
+}
+
 // The same where infinities are NaN too.
 __device__ __forceinline__ uint32_t nearest_elements(float lo, float hi) {
     lo = fabsf(lo) < INFINITY ? lo : __int_as_float(0x7FC00000);

@@ -11,10 +11,27 @@ namespace {
 
 // Threads of a block: a warp a head where few blocks run, and their latency is the call's;
 // two warps where they fill the device several times over.  One branch in one layer of 8
-// heads 3.5 us with 256 threads (6.5 with 64); 64 branches in 16 layers 13.2 us with 64
-// (16.2 with 256).
+// heads 3.6 us with 256 threads (7.1 with 64); 64 branches in 16 layers 14.5 us with 64
+// (16.6 with 256).
 constexpr int kCommitThreads = 256, kManyCommitThreads = 64;
 constexpr int kCommitAhead = 4;    // rows of a lane in flight
+// resident blocks of 256 threads, or as many threads: with more registers 64 branches in 16
+// layers take 18 us
+constexpr int kCommitBlocks = 4;
+
+// Sixteen elements kept under a scale `under` of at most `top`, which is no power of two, as a
+// cache may have been filled with.  The quotient is taken in two parts: its first 20 bits, a
+// little low, and what they lack.  A call, so that its registers are not the common path's.
+__device__ __noinline__ uint4 odd_elements(uint4 x, float under, float top) {
+    const float to_one = scale_to_one(top);
+    under *= to_one;
+    top *= to_one;
+    const float inv = 1.0f / top;
+    const float f = __uint_as_float((max(__float_as_uint(under * inv), 16u) - 8) & ~15u);
+    const float rest = fmaf(-f, top, under) * inv;
+    return make_uint4(scaled_elements(x.x, f, rest), scaled_elements(x.y, f, rest),
+                      scaled_elements(x.z, f, rest), scaled_elements(x.w, f, rest));
+}
 
 // The accepted rows of one request, one layer and one cache move to the front of the
 // tree's slots, block by block of slots under one scale: what a block will hold is
@@ -22,8 +39,8 @@ constexpr int kCommitAhead = 4;    // rows of a lane in flight
 // largest of the rows' scales, and moves its rows some at a time, elements scaled to
 // it.  Row j comes from node path[j] >= j, so no later source lies below a block that
 // was written, nor below a row that was.  Bound by latencies: a few dependent reads a
-// block (64 branches in 16 layers move 15 MB in 13.8 us).
-__global__ void __launch_bounds__(kCommitThreads)
+// block (64 branches in 16 layers move 15 MB in 14.5 us).
+__global__ void __launch_bounds__(kCommitThreads, kCommitBlocks)
 tree_commit_fp8_kernel(const __grid_constant__ ple_tree_commit_fp8_args f, const int shift) {
     __shared__ int64_t from_s[kMostBlock], scale_s[kMostBlock];
     wait_grid_before();
@@ -108,6 +125,8 @@ tree_commit_fp8_kernel(const __grid_constant__ ple_tree_commit_fp8_args f, const
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1)
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+            // a quotient by a power of two, as every scale is that the library writes, is exact
+            const bool odd = (__float_as_uint(most) & 0x7FFFFFu) != 0;
             uint8_t* rows = cache + head * a.head_stride + sub * 16;
             for (int i0 = 0; i0 < live; i0 += kCommitAhead * rows_at_once) {
                 uint4 v[kCommitAhead];
@@ -128,7 +147,9 @@ tree_commit_fp8_kernel(const __grid_constant__ ple_tree_commit_fp8_args f, const
                     const int i = i0 + k * rows_at_once + group;
                     if (by[k] < 0.f) continue;
                     uint4 x = v[k];
-                    if (by[k] != 1.f)
+                    if (by[k] != 1.f && odd)
+                        x = odd_elements(x, scale_value(head_scales[scale_s[i]]), most);
+                    else if (by[k] != 1.f)
                         x = make_uint4(scaled_elements(x.x, by[k]), scaled_elements(x.y, by[k]),
                                        scaled_elements(x.z, by[k]), scaled_elements(x.w, by[k]));
                     *reinterpret_cast<uint4*>(rows + to + i * a.slot_stride) = x;

@@ -5,8 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+import cache_reference as ref8
 import layer_gram_embedding_gb300 as ple
-from test_cache_ops import attention_inputs, check_attention, dev
+import tree_reference as ref
+from test_cache_ops import FP8, attention_inputs, check_attention, dev
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -45,3 +47,37 @@ def test_nan_in_one_segment_of_many(D, nodes, longest, dtype):
                                               dev(cu), dev(masks), return_lse=True)
     assert torch.equal(got.isnan(), want.isnan())
     assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0)) and torch.equal(got_lse, lse)
+
+
+def test_commit_under_any_two_scales():
+    # Eight older tokens under one scale, eight moved behind them from a block under another: of
+    # all pairs of significands, all bytes of the ones or of the others are rounded under the
+    # larger scale.  Products of an element and a scale are exact in 64 bits, and so is a quotient
+    # of them on the border of two elements; every other one is 2^-13 of itself away from it.
+    requests, heads, D = 128, 128, 256
+    pages = 2 * requests
+    table = np.arange(pages, dtype=np.int32).reshape(requests, 2)
+    ctx, cu = np.full(requests, 8, np.int32), ref.prefix([16] * requests)
+    path = np.tile(np.arange(8, 16, dtype=np.int32), (requests, 1))
+    one, two = np.broadcast_arrays(128.0 + np.arange(requests)[:, None], 128.0 + np.arange(heads))
+    for exponent in (-13, -100, -139, 119):
+        scales = [np.stack([one, two * step], 1) * 2.0 ** exponent for step in (1, 2)]
+        caches = [dev(np.arange(256, dtype=np.uint8)).expand(pages, heads, 16, D).contiguous()
+                  .view(FP8) for _ in range(2)]
+        caches += [dev(s.reshape(pages, heads, 1)).to(torch.bfloat16) for s in scales]
+        scales = [s.double().cpu().numpy().reshape(requests, 2, heads) for s in caches[2:]]
+        ple.ple_tree_commit_fp8(dev(np.zeros(16 * requests, np.int64)), dev(path),
+                                dev(np.full(requests, 8, np.int32)), dev(cu), None, dev(ctx),
+                                dev(table), *caches)
+        for c, now, had in zip(caches[:2], caches[2:], scales):
+            got = c.view(torch.uint8).view(requests, 2, heads, 16, D)[:, 0].cpu().numpy()
+            top = had.max(1)
+            assert np.array_equal(now.double().cpu().numpy().reshape(had.shape)[:, 0], top)
+            for part in (0, 1):
+                with np.errstate(invalid="ignore"):     # NaN elements
+                    want = ref8.encode(ref8.VALUES * had[:, part, :, None] / top[..., None])
+                nan = np.isnan(ref8.VALUES)
+                x = got[:, :, 8 * part:8 * part + 8]
+                assert np.all(x[..., nan] & 0x7F == 0x7F)
+                differ = x[..., ~nan] != want[:, :, None, ~nan]
+                assert not differ.any(), (exponent, part, differ.mean())
