@@ -726,8 +726,8 @@ ple_status ple_qk_norm_rope_fp8(const ple_qk_norm_rope_fp8_args* args, void* str
  * softmax's maximum and sum and the output are held in 32 bits.  A weight times its
  * value's scale enters the product with the elements to 2^-11 of itself, or to 2^-27 of
  * the largest such among the 128 slots around it, however far below the row's largest
- * those are (not under 2^-50 of the row's sum).  A slot that is seen and holds a NaN
- * makes the row NaN.
+ * those are (not under 2^-50 of the row's sum of them).  A slot that is seen and holds a
+ * NaN makes the row NaN.
  */
 typedef struct {
     ple_tree_attention_args base;

@@ -51,8 +51,12 @@ constexpr int kTeam = kTile / kSlice;     // warps of a tile
 // row's reference before that moves, and where weights are placed as halves: between
 // 2^2 and 2^15 with these, and a scale's significand below 2.
 constexpr float kRise = 5.0f, kFall = 7.0f, kBias = 9.0f;
-// A reference falls only while the row's weights sum up to less than this.
-constexpr float kMostSum = 0x1p60f;
+// A reference falls only where the row's weights, relative to the new one, sum up to less than
+// this.  That sum is taken as the most that each slice's (or tile's) largest weight allows: up to
+// 2^8 times what it is.  So a tile whose largest weight is 2^-50 of the row's sum or more is still
+// followed (2^(50 + 8 + kBias) is below it), and accumulators, 448 times the sum at most, stay far
+// inside 32 bits.
+constexpr float kMostSum = 0x1p68f;
 
 // W: a head's width in shared memory (64, 128 or 256); NT: tiles of eight rows; Teams: of
 // eight warps, which take the tiles in turn.

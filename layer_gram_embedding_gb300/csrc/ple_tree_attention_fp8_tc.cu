@@ -71,7 +71,7 @@ constexpr int kBadSegments = 8;
 
 // As in ple_tree_attention_fp8.cu.
 constexpr float kRise = 5.0f, kFall = 7.0f, kBias = 9.0f;
-constexpr float kMostSum = 0x1p60f;
+constexpr float kMostSum = 0x1p68f;
 
 // kPairs: units of up to 256 rows (heads of up to 128 elements), 128 for each group; else
 // of up to 128 / kCopies, and the groups take the tiles in turn.

@@ -8,7 +8,7 @@ import torch
 import cache_reference as ref8
 import layer_gram_embedding_gb300 as ple
 import tree_reference as ref
-from test_cache_ops import FP8, attention_inputs, check_attention, dev
+from test_cache_ops import FP8, KERNELS, U, attention_inputs, check_attention, dev, host
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -81,3 +81,36 @@ def test_commit_under_any_two_scales():
                 assert np.all(x[..., nan] & 0x7F == 0x7F)
                 differ = x[..., ~nan] != want[:, :, None, ~nan]
                 assert not differ.any(), (exponent, part, differ.mean())
+
+
+@pytest.mark.parametrize("counts,Hq", KERNELS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("below", [40, 44, 48])
+def test_values_far_below_a_key_that_takes_nearly_all(counts, Hq, dtype, below):
+    # One key's weight is 2^below times any other's, its values are zeros and so are those of the
+    # 128 slots around it: all that comes out has weights of 2^-below, which enter the product to
+    # 2^-11 of themselves.  Enough requests that a block has most of a unit's tiles.
+    rng = np.random.default_rng(41)
+    B, c, scale = 120, 600, float(np.log(2.0))
+    q, cache, ctx, cu, masks = attention_inputs(rng, counts * B, [c] * B, Hq, 2, 64, 16, 16, dtype)
+    q[:] = 0
+    q[..., 0] = 1
+    for r in range(B):
+        p, s = cache.where(r, np.arange(c + counts[0]))
+        cache.k[0, p, :, s, 0] = 0
+        cache.k[0, p[0], :, s[0], 0] = ref8.encode(float(below))
+        cache.k_scale[0, p] = 1
+        cache.v[0, p[:128], :, s[:128]] = 0
+        cache.v_scale[0, p] = 2.0 ** (below - 8)
+    out, lse = ple.ple_tree_attention_fp8(q, *cache.device(), dev(cache.table), dev(ctx), dev(cu),
+                                          dev(masks), scale=scale, return_lse=True)
+    k, v = (ref8.dequantise(x[0], y[0]) for x, y in ((cache.k, cache.k_scale),
+                                                     (cache.v, cache.v_scale)))
+    want, want_lse, weight = ref8.attention(host(q), k, v, cache.v_scale[0], cache.table, ctx, cu,
+                                            masks, scale)[:3]
+    # the output's rounding, the weights', that of exponents up to `below` (scores are exact but
+    # for scale * log2(e)) and of one sum for each 16 slots
+    bound = U[dtype] * (1 + 2.0 ** -8) * np.abs(want) + \
+        (2.0 ** -11 + 2.0 ** -22 * below + 2.0 ** -20 + 2.0 ** -23 * c / 16) * weight
+    assert np.all(np.abs(host(out) - want) <= bound)
+    assert np.all(np.abs(host(lse) - want_lse) <= 2.0 ** -20 * np.abs(want_lse) + 2.0 ** -20)
