@@ -365,6 +365,7 @@ __device__ __forceinline__ void append_blocks(const ple_qk_norm_rope_fp8_args& f
                         scale = old;
                     }
                 }
+                __syncwarp();   // all lanes have read what lies there
                 if (lane == 0) *scale_at = (unsigned short)(__float_as_uint(scale) >> 16);
             }
             if (!(look && store)) {

@@ -8,7 +8,8 @@ import torch
 import cache_reference as ref8
 import layer_gram_embedding_gb300 as ple
 import tree_reference as ref
-from test_cache_ops import FP8, KERNELS, U, attention_inputs, check_attention, dev, host
+from test_cache_ops import (FP8, KERNELS, U, Cache8, attention_inputs, check_append,
+                            check_attention, dev, host, read, rows, same)
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -114,3 +115,30 @@ def test_values_far_below_a_key_that_takes_nearly_all(counts, Hq, dtype, below):
         (2.0 ** -11 + 2.0 ** -22 * below + 2.0 ** -20 + 2.0 ** -23 * c / 16) * weight
     assert np.all(np.abs(host(out) - want) <= bound)
     assert np.all(np.abs(host(lse) - want_lse) <= 2.0 ** -20 * np.abs(want_lse) + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("block,D,into", [(128, 128, 127), (128, 256, 65), (64, 256, 33)])
+def test_older_tokens_grow_with_their_block(block, D, into):
+    # angles in parts: every lane sees the scale that the block had, not the one that it gets, and
+    # rounds its part of the older tokens anew
+    rng = np.random.default_rng(43)
+    B, Hk = 40, 8
+    ctx, cu = np.full(B, into, np.int32), ref.prefix([2] * B)
+    cache = Cache8(rng, [into + 2] * B, block, block, Hk, D)
+    for r in range(B):
+        cache.fill(rng, r, 0, into, -16, -12)
+    k, v = (rows(rng, (2 * B, Hk, D), torch.bfloat16) for _ in range(2))
+    positions = dev(np.zeros(2 * B, np.int32))     # turned by nothing
+    args = (dev(cache.table), dev(ctx), dev(cu))
+    first = None
+    for _ in range(5):
+        caches = cache.device()
+        before = read(caches)
+        ple.ple_qk_norm_rope_fp8(k[:, :0], k, v, positions, ple.ple_prepare_rope(D), None, None,
+                                 *caches, *args)
+        after = read(caches)
+        for i, x in enumerate((k, v)):
+            check_append((after[i][0], after[i + 2][0]), (before[i][0], before[i + 2][0]), host(x),
+                         np.zeros(x.shape), cache.table, ctx, cu, exact=True)
+        first = first or after
+        assert all(same(x, y) for x, y in zip(first, after))
