@@ -94,13 +94,15 @@ __device__ __forceinline__ uint2 row_elements(const Pair (&x)[4], float inv) {
 // two, as a cache may have been filled with, the product is mended by what it lacks
 // (Markstein 1990): a quotient on the border of two elements has to be met exactly.
 __device__ __forceinline__ uint2 any_row_elements(const Pair (&x)[4], float scale, float inv) {
-    const Pair down = make_pair(-scale, -scale), up = make_pair(inv, inv);
+    const Pair whole = make_pair(scale, scale), up = make_pair(inv, inv);
+    const Pair less = make_pair(-inv, -inv), minus = make_pair(-1.f, -1.f);
     const bool power = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         Pair y = x[i] * up;
-        if (!power) y = fma_pair(fma_pair(y, down, x[i]), up, y);
+        // (what y is above the quotient, times less: so that a zero keeps its sign)
+        if (!power) y = fma_pair(fma_pair(y, whole, x[i] * minus), less, y);
         float lo, hi, lo_x, hi_x;
         split(y, lo, hi);
         split(x[i], lo_x, hi_x);

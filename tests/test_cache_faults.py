@@ -142,3 +142,26 @@ def test_older_tokens_grow_with_their_block(block, D, into):
                          np.zeros(x.shape), cache.table, ctx, cu, exact=True)
         first = first or after
         assert all(same(x, y) for x, y in zip(first, after))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scale", [1.5, 1.0, 255 * 2.0 ** -100])
+def test_appended_zeros_keep_their_signs(dtype, scale):
+    # under a scale that the block has, a power of two or not, and beside what is not finite
+    cache = Cache8(np.random.default_rng(44), [12], 16, 16, 2, 64)
+    cache.fill(np.random.default_rng(45), 0, 0, 4)
+    p, _ = cache.where(0, 0)
+    cache.k_scale[0, p] = cache.v_scale[0, p] = scale
+    x = torch.zeros((8, 2, 64), dtype=dtype, device=DEV)
+    x[:, :, ::3] = -0.0
+    x[:, :, 1::3] = scale * 4.5
+    x[5, 1, 7] = float("inf")
+    ctx, cu = np.array([4], np.int32), np.array([0, 8], np.int32)
+    caches = cache.device()
+    before = read(caches)
+    ple.ple_qk_norm_rope_fp8(x[:, :0], x, x, None, None, None, None, *caches, dev(cache.table),
+                             dev(ctx), dev(cu))
+    after = read(caches)
+    for i in (0, 1):
+        check_append((after[i][0], after[i + 2][0]), (before[i][0], before[i + 2][0]), host(x),
+                     np.zeros(x.shape), cache.table, ctx, cu, exact=True)
