@@ -437,21 +437,24 @@ def ple_plan_pages(page_table: torch.Tensor, ctx_lens: torch.Tensor, source: tor
     if N * M > 2 ** 31 - 1 - P:
         raise ValueError(f"{where}: num_rows * max_pages + num_pages must stay below 2^31")
     size = lib().ple_plan_pages_workspace(N, P) // 4 if 0 < P < 2 ** 31 else 0
-    # one piece of memory: tables, lengths, copies, counts, and the call's own
-    parts = [N * M, N, 2 * (N + P - L), 3, max(size, 0)]
-    at = [0]
-    for n in parts:
-        at.append(at[-1] + (n + 3) // 4 * 4)
-    memory = _empty(at[-1], dtype=_i32, device=device)
-    _lend(stream, dev, memory)
-    next_table, next_ctx_lens, copies, counts, workspace = (
-        memory[a:a + n] for a, n in zip(at, parts))
+    # one piece of memory for tables, lengths, copies and counts; the call's own is another, so
+    # that it is not kept as long as they are
+    lens_at = (N * M + 3) // 4 * 4
+    copies_at = lens_at + (N + 3) // 4 * 4
+    counts_at = copies_at + (2 * (N + P - L) + 3) // 4 * 4
+    memory = _empty(counts_at + 4, dtype=_i32, device=device)
+    workspace = _empty(max(size, 0), dtype=_i32, device=device)
+    _lend(stream, dev, memory, workspace)
+    next_table = memory.as_strided((N, M), (M, 1))
+    next_ctx_lens = memory.as_strided((N,), (1,), lens_at)
+    copies = memory.as_strided((N + P - L, 2), (2, 1), copies_at)
+    counts = memory.as_strided((3,), (1,), counts_at)
     args = _PLAN.pack(
         page_table.data_ptr(), ctx_lens.data_ptr(), source.data_ptr(), want.data_ptr(),
         next_table.data_ptr(), next_ctx_lens.data_ptr(), copies.data_ptr(), counts.data_ptr(),
-        workspace.data_ptr(), 4 * parts[4], B, N, M, page_size, P, L)
+        workspace.data_ptr(), 4 * max(size, 0), B, N, M, page_size, P, L)
     _call(where, lib().ple_plan_pages, dev, stream, args)
-    return next_table.view(N, M), next_ctx_lens, copies.view(-1, 2), counts
+    return next_table, next_ctx_lens, copies, counts
 
 
 def ple_copy_pages(copies: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

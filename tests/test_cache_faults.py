@@ -165,3 +165,11 @@ def test_appended_zeros_keep_their_signs(dtype, scale):
     for i in (0, 1):
         check_append((after[i][0], after[i + 2][0]), (before[i][0], before[i + 2][0]), host(x),
                      np.zeros(x.shape), cache.table, ctx, cu, exact=True)
+
+
+def test_a_plan_does_not_keep_its_workspace():
+    pages = 2 ** 20
+    table, zero = dev(np.zeros((1, 1), np.int32)), dev(np.zeros(1, np.int32))
+    got = ple.ple_plan_pages(table, zero, zero, dev(np.ones(1, np.int32)), pages, 16)
+    assert got[3].tolist() == [0, 1, 0]
+    assert all(t.untyped_storage().nbytes() < 2 ** 16 for t in got)
