@@ -726,8 +726,9 @@ ple_status ple_qk_norm_rope_fp8(const ple_qk_norm_rope_fp8_args* args, void* str
  * softmax's maximum and sum and the output are held in 32 bits.  A weight times its
  * value's scale enters the product with the elements to 2^-11 of itself, or to 2^-27 of
  * the largest such among the 128 slots around it, however far below the row's largest
- * those are (not under 2^-50 of the row's sum of them).  A slot that is seen and holds a
- * NaN makes the row NaN.
+ * those are (not under 2^-50 of the row's sum of them, nor where all weights of these slots
+ * are under 2^-100 of the row's largest).  A slot that is seen and holds a NaN makes the
+ * row NaN: its keys' all of it, its values' the elements where they are NaN.
  */
 typedef struct {
     ple_tree_attention_args base;
@@ -821,7 +822,7 @@ int64_t ple_plan_pages_workspace(int32_t num_rows, int32_t num_pages);
  * page may be both a source and a destination of one call, or twice a destination.
  */
 typedef struct {
-    const int32_t* copies;
+    const int32_t* copies;          /* 8-byte aligned */
     void *k_cache, *v_cache;        /* 16-byte aligned */
     int64_t layer_stride, page_stride, head_stride, slot_stride;  /* in elements */
     ple_cache_scales scales;        /* of caches in 8 bits; k and v NULL: none */

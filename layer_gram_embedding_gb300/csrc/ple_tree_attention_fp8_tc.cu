@@ -34,9 +34,10 @@
 //
 // Measured (bf16, heads of 128, 32 query and 8 key heads, 64-slot pages, the join with
 // it; in brackets the cache in 16 bits).  32 requests over 16384 slots: 4 nodes 207 us, 8
-// nodes 214 (324), 32 nodes 289 (337), 64 nodes 495 (421); 64 nodes of 64 heads over
-// 130981 slots, float16, 270 (221); 32 ragged requests of 17 to 32749 slots 288 (343).
-// 160 us are the bytes.  A tile is some 2000 clocks at few rows, where shared memory alone
+// nodes 211 (324), 32 nodes 289 (337), 64 nodes 493 (421); 64 nodes of 64 heads over
+// 130981 slots, float16, 268 (221); 32 ragged requests of 17 to 32749 slots 286 to 306, as
+// long contexts meet large trees or not (343).  160 us are the bytes.  512 nodes, a prompt's
+// chunk, over 0, 4096 and 16384 slots 37, 69 and 142; four such 62, 177 and 476.  A tile is some 2000 clocks at few rows, where shared memory alone
 // is read and written for 1400; with 128 rows the chain of a group: some 1900 clocks of
 // softmax for 128 rows of 128 keys, and 1400 from the weights to the next scores.  With
 // 256 rows a tile's products read more shared memory than those of the cache in 16 bits
